@@ -349,6 +349,126 @@ mxq_status mxq_quantize_blockwise(const uint16_t *x, int64_t rows, int64_t cols,
                                   int64_t ss_cb, void *stream);
 
 /*
+ * Mixture-of-experts routing around the quantized grouped products: which
+ * experts a token goes to, the token groups (`offs`) that the quantizers
+ * read, the token rows laid out group after group, and the way back.  These
+ * calls are not in the pages; their definitions stand here.
+ *
+ * Numerics: elements are bf16 or fp32 (mxq_dtype); every sum is held in fp32
+ * or more and rounded once to the output's type, in an order that does not
+ * change from call to call.  Strides as above; the last dim has unit stride
+ * (others -> MXQ_ERR_UNSUPPORTED); rows need only the element's alignment.
+ * Rows of inputs may repeat (a zero row stride).  (tokens, top_k) arrays are
+ * contiguous.  1 <= top_k <= min(num_experts, MXQ_MAX_TOP_K),
+ * num_experts <= MXQ_MAX_GROUPS, tokens * top_k < 2^31.
+ */
+#define MXQ_MAX_TOP_K 32
+#define MXQ_MAX_GROUP_ALIGN 4096
+
+typedef enum mxq_dtype { MXQ_BF16 = 0, MXQ_F32 = 1 } mxq_dtype;
+
+/* Rows a grouped buffer needs whatever the router picks: tokens * top_k plus
+ * align - 1 for every expert that can have a slot; -1 for invalid arguments
+ * or a count past INT32_MAX. */
+int64_t mxq_moe_row_capacity(int64_t tokens, int32_t top_k, int32_t num_experts, int32_t align);
+
+/* Workspace bytes of mxq_moe_route; -1 for invalid arguments. */
+int64_t mxq_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts, int32_t top_k);
+
+/*
+ * Router: softmax, the top_k largest logits, per-expert counts, token groups
+ * and the two auxiliary losses.
+ *
+ * logits      (tokens, num_experts), strides (sl_t, sl_e).  -inf marks an
+ *             expert that the token cannot take.
+ * token_mask  NULL, or one byte per token; 0 = the token takes part in
+ *             nothing (padding).  A token without any logit > -inf neither.
+ * ids         (tokens, top_k) int32: the experts of the largest logits in
+ *             descending order, ties to the lower index; -1 where no expert
+ *             is left (an empty slot).
+ * weights     (tokens, top_k) fp32: softmax probability of the slot's expert,
+ *             with renormalize = 1 over the sum of the token's slots; 0 for
+ *             an empty slot.
+ * rows        (tokens, top_k) int32: the slot's row in the grouped buffer, in
+ *             token order inside each expert's group; -1 for an empty slot.
+ * lse         (tokens) fp32: log-sum-exp of the logits; +inf for a token that
+ *             takes part in nothing.
+ * counts      (num_experts) int32: slots per expert.
+ * offs        (num_experts) int32: group ends; each group's length is its
+ *             count rounded up to a multiple of align.  What the jagged
+ *             quantizers take as `offs`.
+ * mean_prob   (num_experts) fp32: mean probability over the live tokens.
+ * losses      2 fp32: balance = num_experts * sum_e f_e mean_prob_e with
+ *             f_e = counts_e / (live * top_k), and z = mean of lse^2; both 0
+ *             when no token is live.
+ * live        1 int32: number of live tokens.
+ * workspace   mxq_moe_route_workspace_bytes bytes, 4-byte aligned, contents
+ *             arbitrary before and after; too small -> MXQ_ERR_WORKSPACE.
+ * A NaN logit is never taken and makes the token's probabilities, and the
+ * losses, NaN.
+ */
+mxq_status mxq_moe_route(const void *logits, int32_t dtype, int64_t tokens, int32_t num_experts,
+                         int64_t sl_t, int64_t sl_e, const uint8_t *token_mask, int32_t top_k,
+                         int32_t renormalize, int32_t align, int32_t *ids, float *weights,
+                         int32_t *rows, float *lse, int32_t *counts, int32_t *offs,
+                         float *mean_prob, float *losses, int32_t *live, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of mxq_moe_route's weights and losses with respect to the logits
+ * (the selection and the counts are constants).
+ *
+ * ids, weights, lse, counts, live   the forward call's outputs.
+ * grad_weights  (tokens, top_k) fp32, or NULL for none.
+ * grad_losses   2 fp32 on the device (balance, z), or NULL for none.
+ * grad_logits   (tokens, num_experts) of dtype, strides (sg_t, sg_e); zeros
+ *               for a token that takes part in nothing.
+ */
+mxq_status mxq_moe_route_backward(const void *logits, int32_t dtype, int64_t tokens,
+                                  int32_t num_experts, int64_t sl_t, int64_t sl_e, int32_t top_k,
+                                  int32_t renormalize, const int32_t *ids, const float *weights,
+                                  const float *lse, const int32_t *counts, const int32_t *live,
+                                  const float *grad_weights, const float *grad_losses,
+                                  void *grad_logits, int64_t sg_t, int64_t sg_e, void *stream);
+
+/*
+ * Token rows into their groups: xg[rows[t, j]] = x[t] for every slot.  Rows of
+ * xg that no slot names (a group's padding, and everything past the last
+ * group) become 0, so all `capacity` rows are written.
+ * x (tokens, width), xg (capacity, width); rows, counts, offs from
+ * mxq_moe_route; a row outside [0, capacity) is an empty slot.
+ */
+mxq_status mxq_moe_dispatch(const void *x, int32_t dtype, int64_t tokens, int64_t width,
+                            int64_t sx_t, int64_t sx_c, const int32_t *rows, int32_t top_k,
+                            const int32_t *counts, const int32_t *offs, int32_t num_experts,
+                            void *xg, int64_t capacity, int64_t sg_r, int64_t sg_c, void *stream);
+
+/*
+ * The way back: y[t] = residual[t] + sum_j weights[t, j] * yg[rows[t, j]], in
+ * fp32 in the order of the slots.  weights NULL: all 1 (with it this is the
+ * gradient of mxq_moe_dispatch); residual NULL: none.  Empty slots add
+ * nothing, whatever the buffer holds.
+ */
+mxq_status mxq_moe_combine(const void *yg, int32_t dtype, int64_t capacity, int64_t width,
+                           int64_t sg_r, int64_t sg_c, const int32_t *rows, const float *weights,
+                           int32_t top_k, const void *residual, int64_t sr_t, int64_t sr_c, void *y,
+                           int64_t sy_t, int64_t sy_c, int64_t tokens, void *stream);
+
+/*
+ * Gradients of mxq_moe_combine: grad_yg[rows[t, j]] = weights[t, j] *
+ * grad_y[t], 0 in the rows that no slot names; grad_weights[t, j] =
+ * <grad_y[t], yg[rows[t, j]]> in fp32, 0 for an empty slot.  (The residual's
+ * gradient is grad_y.)
+ */
+mxq_status mxq_moe_combine_backward(const void *grad_y, int32_t dtype, int64_t tokens,
+                                    int64_t width, int64_t sy_t, int64_t sy_c, const void *yg,
+                                    int64_t sg_r, int64_t sg_c, const int32_t *rows,
+                                    const float *weights, int32_t top_k, const int32_t *counts,
+                                    const int32_t *offs, int32_t num_experts, int64_t capacity,
+                                    void *grad_yg, int64_t sd_r, int64_t sd_c, float *grad_weights,
+                                    void *stream);
+
+/*
  * TEST-ONLY diagnostics, not part of the quantization API: the library's own
  * device conversions applied to n fp32 values, so that tests can check them
  * against the CPU definition over whole fp32 ranges.  y: n floats, out: n

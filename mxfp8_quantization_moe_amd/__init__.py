@@ -25,7 +25,10 @@ from ._capi import (MXQ_ERR_INVALID_ARG, MXQ_ERR_LAUNCH, MXQ_ERR_UNSUPPORTED, MX
                     mxq_quantize_jagged_colwise, mxq_quantize_jagged_mx_colwise,
                     mxq_quantize_jagged_mx_rowwise, mxq_quantize_jagged_rowwise,
                     mxq_quantize_mx_3d_colwise, mxq_quantize_mx_rowwise,
-                    mxq_relayout_mx_scales_grouped)
+                    mxq_relayout_mx_scales_grouped, MXQ_BF16, MXQ_F32, MXQ_MAX_GROUP_ALIGN,
+                    MXQ_MAX_TOP_K, mxq_moe_combine, mxq_moe_combine_backward, mxq_moe_dispatch,
+                    mxq_moe_route, mxq_moe_route_backward, mxq_moe_route_workspace_bytes,
+                    mxq_moe_row_capacity)
 
 __all__ = [
     "quantize_jagged_rowwise", "quantize_jagged_colwise", "quantize_mx_3d_colwise",
@@ -39,6 +42,10 @@ __all__ = [
     "mxq_quantize_jagged_colwise_ws", "mxq_jagged_colwise_workspace_bytes",
     "mxq_debug_jagged_colwise_ws_spin", "mxq_quantize_jagged_colwise_noalloc",
     "mxq_abi_version", "LibraryMissing",
+    "MoeRoute", "moe_route", "moe_route_backward", "moe_dispatch", "moe_dispatch_backward",
+    "moe_combine", "moe_combine_backward", "moe_row_capacity",
+    "mxq_moe_route", "mxq_moe_route_backward", "mxq_moe_route_workspace_bytes",
+    "mxq_moe_row_capacity", "mxq_moe_dispatch", "mxq_moe_combine", "mxq_moe_combine_backward",
 ]
 
 
@@ -316,3 +323,7 @@ def debug_cast4_e4m3(y, unclamped: bool, *, stream=None):
     _check(mxq_debug_cast4_e4m3(y.data_ptr(), y.numel(), out.data_ptr(), 1 if unclamped else 0,
                                 _stream(y, stream)), "mxq_debug_cast4_e4m3")
     return out
+
+
+from .moe import (MoeRoute, moe_combine, moe_combine_backward, moe_dispatch,  # noqa: E402
+                  moe_dispatch_backward, moe_route, moe_route_backward, moe_row_capacity)

@@ -22,6 +22,10 @@ MXQ_ERR_WORKSPACE = 4
 MXQ_SCALE_FLOOR = 0
 MXQ_SCALE_RCEIL = 1
 MXQ_MAX_GROUPS = 4096
+MXQ_MAX_TOP_K = 32
+MXQ_MAX_GROUP_ALIGN = 4096
+MXQ_BF16 = 0
+MXQ_F32 = 1
 MXQ_NOALLOC_SCRATCH_BYTES = 4 << 20
 
 _i64 = ctypes.c_int64
@@ -55,10 +59,23 @@ SIGNATURES = {
                                             _i64, _vp, _i64, _i64, _vp],
     "mxq_debug_jagged_colwise_ws_spin": [_vp, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _i64, _i64,
                                          _vp, _i64, _i64, _vp, _i64, _i32, _vp],
+    "mxq_moe_row_capacity": [_i64, _i32, _i32, _i32],
+    "mxq_moe_route_workspace_bytes": [_i64, _i32, _i32],
+    "mxq_moe_route": [_vp, _i32, _i64, _i32, _i64, _i64, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
+                      _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
+    "mxq_moe_route_backward": [_vp, _i32, _i64, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp,
+                               _vp, _vp, _vp, _vp, _i64, _i64, _vp],
+    "mxq_moe_dispatch": [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _i64,
+                         _i64, _i64, _vp],
+    "mxq_moe_combine": [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _vp, _i64, _i64, _vp,
+                        _i64, _i64, _i64, _vp],
+    "mxq_moe_combine_backward": [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i32,
+                                 _vp, _vp, _i32, _i64, _vp, _i64, _i64, _vp, _vp],
     "mxq_debug_cast_e4m3": [_vp, _i64, _vp, _vp],
     "mxq_debug_cast4_e4m3": [_vp, _i64, _vp, _i32, _vp],
 }
-RESTYPES = {"mxq_status_string": ctypes.c_char_p, "mxq_jagged_colwise_workspace_bytes": _i64}
+RESTYPES = {"mxq_status_string": ctypes.c_char_p, "mxq_jagged_colwise_workspace_bytes": _i64,
+            "mxq_moe_row_capacity": _i64, "mxq_moe_route_workspace_bytes": _i64}
 
 _lib = None
 
@@ -111,5 +128,12 @@ mxq_quantize_jagged_colwise_ws = _fwd("mxq_quantize_jagged_colwise_ws")
 mxq_jagged_colwise_workspace_bytes = _fwd("mxq_jagged_colwise_workspace_bytes")
 mxq_debug_jagged_colwise_ws_spin = _fwd("mxq_debug_jagged_colwise_ws_spin")
 mxq_quantize_jagged_colwise_noalloc = _fwd("mxq_quantize_jagged_colwise_noalloc")
+mxq_moe_row_capacity = _fwd("mxq_moe_row_capacity")
+mxq_moe_route_workspace_bytes = _fwd("mxq_moe_route_workspace_bytes")
+mxq_moe_route = _fwd("mxq_moe_route")
+mxq_moe_route_backward = _fwd("mxq_moe_route_backward")
+mxq_moe_dispatch = _fwd("mxq_moe_dispatch")
+mxq_moe_combine = _fwd("mxq_moe_combine")
+mxq_moe_combine_backward = _fwd("mxq_moe_combine_backward")
 mxq_debug_cast_e4m3 = _fwd("mxq_debug_cast_e4m3")
 mxq_debug_cast4_e4m3 = _fwd("mxq_debug_cast4_e4m3")

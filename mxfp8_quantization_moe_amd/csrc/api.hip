@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "mxq.h"
+#include "api_common.hpp"
 #include "block_kernels.hpp"
 #include "colwise_tile_kernels.hpp"
 #include "jagged_kernels.hpp"
@@ -49,8 +50,6 @@ int tile_chunk(int64_t nblocks) { return nblocks >= kTileOrderMinBlocks ? kTileC
 // it reduces the group's rows itself
 constexpr int kColwiseSpinLimit = 4000;
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // column-major q whose 128-row column runs start on 128-byte lines: base and
 // the column (and batch) strides on lines
 int line_aligned(const void *q, int64_t ldq, int64_t sqe)
@@ -66,12 +65,6 @@ int mx3d_store_mode(const void *q, int64_t N, int64_t K, int64_t ldq, int64_t sq
     if (!line_aligned(q, ldq, sqe))
         return 0;
     return (K - 1) * ldq + N <= (int64_t)UINT32_MAX ? 2 : 1;
-}
-
-mxq_status launch_status()
-{
-    hipError_t e = hipGetLastError();
-    return e == hipSuccess ? MXQ_OK : MXQ_ERR_LAUNCH;
 }
 
 // number of compute units of the device that runs `st` (the calling
