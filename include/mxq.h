@@ -469,6 +469,38 @@ mxq_status mxq_moe_combine_backward(const void *grad_y, int32_t dtype, int64_t t
                                     void *stream);
 
 /*
+ * Newton-Schulz orthogonalisation of weight updates, as the Muon optimiser
+ * applies it to each expert's matrix.  Per matrix G (rows, cols):
+ *   X = G / (|G|_F + eps), transposed if rows > cols;
+ *   `steps` times  A = X X^T,  B = b A + c A^2,  X = a X + B X;
+ *   out = scale * X (transposed back), rounded to bf16.
+ * (a, b, c) = (3.4445, -4.7750, 2.0315) takes singular values towards
+ * [0.7, 1.2] in five steps.
+ *
+ * Numerics: products of f16 operands with fp32 sums; X is carried in 22 bits
+ * and the diagonals of A and B in fp32.  Against 64 bits the result is off by
+ * the bf16 rounding (1.7e-3 of its 2-norm) and about 0.5e-3 more.  The powers
+ * of two that keep the operands inside f16 leave room for iterates with
+ * entries up to 8 and entries of A and B up to 32; coefficients that let X
+ * grow past that give inf or NaN.  The norm is summed in fp64: any finite G
+ * is in range.  A G of zeros gives zeros; a NaN or infinity anywhere in a
+ * matrix makes that whole matrix NaN or zero.
+ *
+ * g       (count, rows, cols) bf16 or fp32, strides (sg_e, sg_r, sg_c);
+ *         rows and cols <= 65536.
+ * out     (count, rows, cols) bf16, strides (so_e, so_r, so_c).
+ * Layouts with a kernel: sg_c == 1 or sg_r == 1, so_c == 1 or so_r == 1.
+ * workspace  mxq_muon_workspace_bytes bytes, 16-byte aligned, contents
+ *         arbitrary before and after; too small -> MXQ_ERR_WORKSPACE.
+ */
+int64_t mxq_muon_workspace_bytes(int64_t count, int64_t rows, int64_t cols);
+mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, int64_t rows,
+                                  int64_t cols, int64_t sg_e, int64_t sg_r, int64_t sg_c,
+                                  uint16_t *out, int64_t so_e, int64_t so_r, int64_t so_c,
+                                  int32_t steps, float a, float b, float c, float eps, float scale,
+                                  void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
  * TEST-ONLY diagnostics, not part of the quantization API: the library's own
  * device conversions applied to n fp32 values, so that tests can check them
  * against the CPU definition over whole fp32 ranges.  y: n floats, out: n

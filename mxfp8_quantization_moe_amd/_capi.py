@@ -32,6 +32,7 @@ _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _vp = ctypes.c_void_p
 _st = ctypes.c_int
+_f32 = ctypes.c_float
 
 # name -> argument types (restype is mxq_status == int unless listed below)
 SIGNATURES = {
@@ -71,11 +72,15 @@ SIGNATURES = {
                         _i64, _i64, _i64, _vp],
     "mxq_moe_combine_backward": [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i32,
                                  _vp, _vp, _i32, _i64, _vp, _i64, _i64, _vp, _vp],
+    "mxq_muon_workspace_bytes": [_i64, _i64, _i64],
+    "mxq_muon_orthogonalize": [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _i64,
+                               _i32, _f32, _f32, _f32, _f32, _f32, _vp, _i64, _vp],
     "mxq_debug_cast_e4m3": [_vp, _i64, _vp, _vp],
     "mxq_debug_cast4_e4m3": [_vp, _i64, _vp, _i32, _vp],
 }
 RESTYPES = {"mxq_status_string": ctypes.c_char_p, "mxq_jagged_colwise_workspace_bytes": _i64,
-            "mxq_moe_row_capacity": _i64, "mxq_moe_route_workspace_bytes": _i64}
+            "mxq_moe_row_capacity": _i64, "mxq_moe_route_workspace_bytes": _i64,
+            "mxq_muon_workspace_bytes": _i64}
 
 _lib = None
 
@@ -135,5 +140,7 @@ mxq_moe_route_backward = _fwd("mxq_moe_route_backward")
 mxq_moe_dispatch = _fwd("mxq_moe_dispatch")
 mxq_moe_combine = _fwd("mxq_moe_combine")
 mxq_moe_combine_backward = _fwd("mxq_moe_combine_backward")
+mxq_muon_workspace_bytes = _fwd("mxq_muon_workspace_bytes")
+mxq_muon_orthogonalize = _fwd("mxq_muon_orthogonalize")
 mxq_debug_cast_e4m3 = _fwd("mxq_debug_cast_e4m3")
 mxq_debug_cast4_e4m3 = _fwd("mxq_debug_cast4_e4m3")

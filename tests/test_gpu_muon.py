@@ -1,0 +1,174 @@
+"""The Newton-Schulz orthogonalisation against the formula in 64 bits, over
+types, shapes around the tiles, tall and wide, layouts, ill-conditioned and
+degenerate matrices."""
+import pytest
+import torch
+
+import mxfp8_quantization_moe_amd as mxq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+A, B, C = mxq.MUON_COEFFICIENTS
+
+# bf16 output: a relative rounding error uniform in +-2^-9 of a value in
+# [1, 2) has an rms of 2^-9 / sqrt(3) * (mean of 1/m^2)^0.5 ~ 1.7e-3 at most.
+# f16 operands: each of the four operand roundings of a step has a relative
+# rms of 2^-12 / sqrt(3) * ~1.5 = 2.1e-4; B's cancelling terms raise one step
+# to about 5e-4 and later steps halve (|p'| < 1 near one) what earlier ones
+# left: below 2e-3.  Together below 2.7e-3; 4e-3 leaves room for small
+# matrices, whose errors average over few elements.
+BOUND = 4e-3
+
+
+def reference(g, steps=5, coefficients=(A, B, C), eps=1e-7, scale=1.0):
+    a, b, c = coefficients
+    out = []
+    for m in g.double().cpu().reshape(-1, *g.shape[-2:]):
+        x = m.t() if m.shape[0] > m.shape[1] else m
+        x = x / (torch.linalg.vector_norm(x) + eps)
+        for _ in range(steps):
+            s = x @ x.t()
+            x = a * x + (b * s + c * (s @ s)) @ x
+        out.append(scale * (x.t() if m.shape[0] > m.shape[1] else x))
+    return torch.stack(out).reshape(g.shape)
+
+
+def update(count, rows, cols, dtype, seed, kind="tokens"):
+    g = torch.Generator().manual_seed(seed)
+    r, k = rows, cols
+    if kind == "tokens":     # gradients: rows of tokens times features with scales of their own
+        t = 2 * min(r, k)
+        x = torch.stack([torch.randn(r, t, generator=g) @ (torch.randn(t, k, generator=g) *
+                         torch.exp(torch.randn(1, k, generator=g))) for _ in range(count)])
+    elif kind == "gauss":    # singular values close together
+        x = torch.randn(count, r, k, generator=g)
+    elif kind == "lowrank":  # a few directions over a small floor
+        x = torch.randn(count, r, 4, generator=g) @ torch.randn(count, 4, k, generator=g)
+        x = x + 0.05 * torch.randn(count, r, k, generator=g)
+    elif kind == "rows":     # rows of very different size
+        x = torch.randn(count, r, k, generator=g) * torch.exp(2 * torch.randn(count, r, 1, generator=g))
+    return x.to(dtype)
+
+
+def err(got, want):
+    got = got.double().cpu()
+    assert torch.isfinite(got).all()
+    return float(torch.linalg.vector_norm(got - want) / torch.linalg.vector_norm(want))
+
+
+def check(g, bound=BOUND, **kw):
+    out = mxq.muon_orthogonalize(g.to(DEV), **kw)
+    assert out.dtype == torch.bfloat16 and out.shape == g.shape and out.is_contiguous()
+    e = err(out, reference(g, **kw))
+    assert e <= bound, e
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (1, 1, 7), (1, 5, 1), (2, 3, 5), (1, 63, 65), (3, 64, 64), (1, 65, 200),
+                                   (2, 200, 130), (1, 257, 255), (1, 100, 777), (1, 777, 100)])
+def test_shapes(shape, dtype):
+    check(update(*shape, dtype, sum(shape)), bound=BOUND if min(shape[1:]) > 8 else 8e-3)
+
+
+@pytest.mark.parametrize("shape", [(300, 64, 96), (70, 130, 260), (20, 384, 512), (12, 1100, 1030)])
+def test_many_matrices_take_larger_tiles(shape):
+    check(update(*shape, torch.bfloat16, 5))
+
+
+@pytest.mark.parametrize("kind", ["gauss", "lowrank", "rows"])
+@pytest.mark.parametrize("shape", [(1, 128, 512), (2, 400, 400), (1, 640, 96)])
+def test_spectra(kind, shape):
+    check(update(*shape, torch.float32, 11, kind))
+
+
+def test_duplicate_and_zero_rows():
+    g = update(1, 96, 300, torch.float32, 2)
+    g[:, 48:] = g[:, :48]
+    check(g)
+    g[:, 10:20] = 0
+    check(g)
+    out = mxq.muon_orthogonalize(g.to(DEV))
+    assert (out[:, 10:20] == 0).all()
+
+
+@pytest.mark.parametrize("factor", [1e-37, 1e-30, 1e-12, 1e20, 1e36])
+def test_any_finite_size_of_input(factor):
+    g = update(1, 80, 120, torch.float32, 3)
+    g = g / g.abs().max() * factor
+    check(g, eps=0.0)
+
+
+def test_zero_matrix_beside_others():
+    g = update(3, 70, 90, torch.bfloat16, 4)
+    g[1] = 0
+    out = mxq.muon_orthogonalize(g.to(DEV))
+    assert (out[1] == 0).all()
+    want = reference(g[[0, 2]])
+    assert err(out[[0, 2]], want) <= BOUND
+
+
+def test_a_nan_stays_in_its_matrix():
+    g = update(3, 70, 90, torch.float32, 6)
+    want = reference(g[[0, 2]])
+    g[1, 5, 5] = float("nan")
+    out = mxq.muon_orthogonalize(g.to(DEV))
+    assert torch.isnan(out[1]).all()
+    assert err(out[[0, 2]], want) <= BOUND
+
+
+@pytest.mark.parametrize("steps", [0, 1, 2, 8])
+def test_steps_coefficients_and_scale(steps):
+    g = update(2, 150, 220, torch.float32, 7)
+    check(g, steps=steps, scale=0.2 * 220 ** 0.5)
+    check(g, steps=steps, coefficients=(1.5, -0.5, 0.0), eps=1e-3)
+
+
+def test_layouts():
+    g = update(3, 90, 140, torch.bfloat16, 8).to(DEV)
+    want = mxq.muon_orthogonalize(g)
+    big = torch.full((3, 95, 149), float("nan"), dtype=torch.bfloat16, device=DEV)
+    big[:, 2:92, 3:143] = g
+    assert torch.equal(mxq.muon_orthogonalize(big[:, 2:92, 3:143]), want)
+    col = g.transpose(1, 2).contiguous().transpose(1, 2)
+    assert torch.equal(mxq.muon_orthogonalize(col), want)
+    assert torch.equal(mxq.muon_orthogonalize(g[1]), want[1])
+    assert torch.equal(mxq.muon_orthogonalize(g.flip(0)), want.flip(0))
+    one = g[:1].expand(4, 90, 140)
+    assert torch.equal(mxq.muon_orthogonalize(one), want[:1].expand(4, 90, 140))
+    # a tall matrix is its transpose's result
+    tall = mxq.muon_orthogonalize(g.transpose(1, 2))
+    assert torch.equal(tall, want.transpose(1, 2))
+
+
+def test_workspace_streams_and_repeats():
+    g = update(2, 300, 200, torch.bfloat16, 9).to(DEV)
+    ws = mxq.muon_workspace(2, 300, 200)
+    first = mxq.muon_orthogonalize(g)
+    side = torch.cuda.Stream()
+    ws.fill_(255)  # its contents do not matter
+    assert torch.equal(mxq.muon_orthogonalize(g, workspace=ws), first)
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        out = mxq.muon_orthogonalize(g, workspace=ws, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    with pytest.raises(mxq.MXQError):
+        mxq.muon_orthogonalize(g, workspace=ws[:-16])
+
+
+def test_empty():
+    for shape in ((0, 5, 5), (2, 0, 5), (2, 5, 0)):
+        assert mxq.muon_orthogonalize(torch.empty(shape, device=DEV)).shape == shape
+
+
+def test_refusals():
+    g = torch.randn(8, 8, device=DEV)
+    for bad in (g.half(), g.cpu(), g[0]):
+        with pytest.raises(TypeError):
+            mxq.muon_orthogonalize(bad)
+    with pytest.raises(mxq.MXQError):
+        mxq.muon_orthogonalize(torch.randn(16, 16, device=DEV)[::2, ::2])
+    with pytest.raises(mxq.MXQError):
+        mxq.muon_orthogonalize(g, steps=-1)
+    with pytest.raises(mxq.MXQError):
+        mxq.muon_orthogonalize(g, eps=float("nan"))
