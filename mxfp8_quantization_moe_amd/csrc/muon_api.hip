@@ -15,25 +15,36 @@ using namespace mxq;
 
 constexpr int64_t kMaxDim = 65536;
 
+// 72 KB of LDS and at most 256 registers: two workgroups per CU, so one's
+// epilogue and LDS reads run beside the other's products
+using TileLarge = MuonTile<256, 128, 2, 2, 3>;
+using TileMedium = MuonTile<128, 128, 2, 2, 4>;
+using TileSmall = MuonTile<64, 64, 2, 2, 8>;
+
 struct MuonPlan {
-    int tile;            // tile edge of the products
+    int tile;            // 2 large, 1 medium, 0 small
     int64_t mp, np;      // padded extents, m <= n
     int64_t bytes;
 };
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// 256-wide tiles reuse each operand byte most and are taken when they still
-// fill the machine; smaller problems take smaller tiles.
+// Larger tiles reuse each operand byte more and are taken when they still
+// fill the machine.
 MuonPlan muon_plan(int64_t count, int64_t rows, int64_t cols)
 {
     const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
     MuonPlan p;
-    auto tiles = [&](int64_t t) { return count * ((m + t - 1) / t) * ((n + t - 1) / t); };
-    p.tile = tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
-    p.mp = round_up(m, p.tile);
-    p.np = round_up(n, p.tile);
-    p.bytes = count * (8 * p.mp * p.np + 6 * p.mp * p.mp + 8 * p.mp + 8 * kNormParts);
+    auto tiles = [&](int64_t tm, int64_t tn) { return count * ((m + tm - 1) / tm) * ((n + tn - 1) / tn); };
+#ifdef MXQ_MUON_TILE
+    p.tile = MXQ_MUON_TILE;
+#else
+    p.tile = tiles(256, 128) >= 256 ? 2 : tiles(128, 128) >= 256 ? 1 : 0;
+#endif
+    const int64_t edge = p.tile == 2 ? 256 : p.tile == 1 ? 128 : 64;
+    p.mp = round_up(m, edge);
+    p.np = round_up(n, std::min<int64_t>(edge, 128));
+    p.bytes = count * (6 * p.mp * p.np + 6 * p.mp * p.mp + 8 * p.mp + 8 * kNormParts);
     return p;
 }
 
@@ -42,27 +53,27 @@ bool sizes_ok(int64_t count, int64_t rows, int64_t cols)
     return count >= 0 && rows >= 0 && cols >= 0 && rows <= kMaxDim && cols <= kMaxDim && count <= 65535;
 }
 
-template <int MODE, int T>
-void launch_product(const MuonBuffers &b, const MuonStep &st, int count, uint16_t *out, const MuonView &ov,
+template <int MODE, typename TILE>
+void launch_product(const MuonBuffers &b, const MuonStep &st, int64_t count, uint16_t *out, const MuonView &ov,
                     hipStream_t s)
 {
     constexpr bool SYM = MODE == kModeA || MODE == kModeB;
-    const int64_t tm = b.mp / T, tn = b.np / T;
-    const int64_t blocks = count * (SYM ? tm * (tm + 1) / 2 : tm * tn);
-    constexpr int WM = 2, WN = T == 256 ? 4 : 2;
-    muon_product_kernel<MODE, T, T, WM, WN><<<dim3((unsigned)blocks), dim3(WM * WN * 64), 0, s>>>(b, st, out, ov);
+    const int64_t tm = b.mp / TILE::TM, tn = b.np / TILE::TN;
+    const int64_t blocks = count * (SYM ? TILE::SYM_STEP * (tm * (tm + 1) / 2) : tm * tn);
+    muon_product_kernel<MODE, TILE><<<dim3((unsigned)blocks), dim3(TILE::THREADS), 0, s>>>(b, st, out, ov);
 }
 
-template <int T>
-void launch_steps(MuonBuffers &b, MuonStep st, int steps, int count, uint16_t *out, const MuonView &ov, hipStream_t s)
+template <typename TILE>
+void launch_steps(MuonBuffers &b, MuonStep st, int steps, int64_t count, uint16_t *out, const MuonView &ov,
+                  hipStream_t s)
 {
     for (int k = 0; k < steps; ++k) {
-        launch_product<kModeA, T>(b, st, count, out, ov, s);
-        launch_product<kModeB, T>(b, st, count, out, ov, s);
+        launch_product<kModeA, TILE>(b, st, count, out, ov, s);
+        launch_product<kModeB, TILE>(b, st, count, out, ov, s);
         if (k + 1 < steps)
-            launch_product<kModeX, T>(b, st, count, out, ov, s);
+            launch_product<kModeX, TILE>(b, st, count, out, ov, s);
         else
-            launch_product<kModeOut, T>(b, st, count, out, ov, s);
+            launch_product<kModeOut, TILE>(b, st, count, out, ov, s);
         st.cur ^= 1;
     }
 }
@@ -71,7 +82,14 @@ template <typename T>
 void launch_load(const void *g, const MuonView &gv, const MuonBuffers &b, int count, float eps, hipStream_t s)
 {
     const T *p = reinterpret_cast<const T *>(g);
-    muon_norm_kernel<T><<<dim3(kNormParts, (unsigned)count), dim3(256), 0, s>>>(p, gv, b.part);
+    // as rows along the unit stride; one row when they follow one another
+    int64_t inner = gv.sj == 1 ? gv.n : gv.m, outer = gv.sj == 1 ? gv.m : gv.n;
+    const int64_t so = gv.sj == 1 ? gv.si : gv.sj;
+    if (so == inner) {
+        inner *= outer;
+        outer = 1;
+    }
+    muon_norm_kernel<T><<<dim3(kNormParts, (unsigned)count), dim3(256), 0, s>>>(p, gv.se, inner, outer, so, b.part);
     muon_load_kernel<T><<<dim3((unsigned)(b.np / 64), (unsigned)(b.mp / 64), (unsigned)count), dim3(256), 0, s>>>(
         p, gv, b, eps);
 }
@@ -104,7 +122,7 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
     const MuonPlan p = muon_plan(count, rows, cols);
     if (workspace_bytes < p.bytes || !workspace)
         return MXQ_ERR_WORKSPACE;
-    if (count * (p.mp / p.tile) * (p.np / p.tile) > INT32_MAX)
+    if (count * (p.mp / 64) * (p.np / 64) > INT32_MAX)
         return MXQ_ERR_INVALID_ARG;
 
     MuonBuffers buf;
@@ -112,11 +130,10 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
     buf.np = (int)p.np;
     buf.part = reinterpret_cast<double *>(workspace);
     const int64_t nx = count * p.mp * p.np, na = count * p.mp * p.mp;
-    buf.xh = reinterpret_cast<_Float16 *>(buf.part + count * kNormParts);
-    buf.xl = buf.xh + nx;
-    buf.xt[0] = buf.xl + nx;
-    buf.xt[1] = buf.xt[0] + nx;
-    buf.oh = buf.xt[1] + nx;
+    buf.xh[0] = reinterpret_cast<_Float16 *>(buf.part + count * kNormParts);
+    buf.xh[1] = buf.xh[0] + nx;
+    buf.xl = buf.xh[1] + nx;
+    buf.oh = buf.xl + nx;
     buf.ol = buf.oh + na;
     buf.bo = buf.ol + na;
     buf.d = reinterpret_cast<float *>(buf.bo + na);
@@ -136,12 +153,12 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
     if (steps == 0)
         muon_copy_kernel<<<dim3((unsigned)((gv.n + 255) / 256), (unsigned)gv.m, (unsigned)count), dim3(256), 0, s>>>(
             buf, st.out_scale, out, ov);
-    else if (p.tile == 256)
-        launch_steps<256>(buf, st, steps, (int)count, out, ov, s);
-    else if (p.tile == 128)
-        launch_steps<128>(buf, st, steps, (int)count, out, ov, s);
+    else if (p.tile == 2)
+        launch_steps<TileLarge>(buf, st, steps, count, out, ov, s);
+    else if (p.tile == 1)
+        launch_steps<TileMedium>(buf, st, steps, count, out, ov, s);
     else
-        launch_steps<64>(buf, st, steps, (int)count, out, ov, s);
+        launch_steps<TileSmall>(buf, st, steps, count, out, ov, s);
     return launch_status();
 }
 

@@ -23,16 +23,18 @@
 //     A = diag(d) + O,  A^2 = O O + d_i O_ij + O_ij d_j + diag(d^2), and the
 //     last three terms are fp32 in the epilogue (O there from two f16 parts).
 //
-// Layout.  Every operand of a product is stored with the summed dim
-// contiguous (X row-major for X X^T, X transposed for B X), padded with zeros
-// to whole tiles, so the products need no bounds checks: padding rows of X
-// stay zero through the iteration.
+// Layout.  X is row-major.  X X^T and O O sum along rows; B X sums along X's
+// columns and reads its operand through the transposing LDS read, so X is
+// stored once (two high parts in turn, since B X reads whole columns of one
+// while the other is written).  Buffers are padded with zeros to whole tiles,
+// so the products need no bounds checks: padding stays zero through the steps.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <hip/hip_fp16.h>
 #include <stdint.h>
 
+#include "moe_rows_kernels.hpp"
 #include "mxq_device.hpp"
 
 namespace mxq {
@@ -45,13 +47,12 @@ constexpr float kScaleX = 8192.0f;   // |x| <= 1.3: up to 10650; room to 8
 constexpr float kScaleA = 2048.0f;   // |o| <= 1.7; room to 32
 constexpr float kScaleB = 2048.0f;   // |b| <= 3; room to 32
 constexpr float kLow = 2048.0f;      // the low parts are stored times 2^11
-constexpr int kBK = 64;              // summed elements per LDS tile: 128-byte rows
-constexpr int kNormParts = 64;       // partial sums of a matrix's squared norm
+constexpr int kBK = 32;              // summed elements per LDS stage
+constexpr int kNormParts = 256;      // partial sums of a matrix's squared norm
 
 // Buffers of one call; matrix e's parts are `e` strides further.
 struct MuonBuffers {
-    _Float16 *xh, *xl;      // [mp][np] high and low parts of X
-    _Float16 *xt[2];        // [np][mp] the high part transposed, this step's and the next
+    _Float16 *xh[2], *xl;   // [mp][np] high parts of X, this step's and the next; low part
     _Float16 *oh, *ol, *bo; // [mp][mp] off-diagonal A (two parts) and B
     float *d, *db;          // [mp] diagonals of A and B
     double *part;           // [kNormParts] partial sums of squares
@@ -73,33 +74,38 @@ __device__ __forceinline__ float join_half(_Float16 hi, _Float16 lo) { return (f
 
 // ---------------------------------------------------------------- norm, load
 
-template <typename T>
-__device__ __forceinline__ float muon_elem(const T *p)
-{
-    if constexpr (sizeof(T) == 2)
-        return __uint_as_float((uint32_t)*p << 16);
-    else
-        return *p;
-}
-
 // Squares in fp64: no value of a finite bf16 or fp32 matrix over- or
-// underflows, and the rate does not matter beside the reads.
+// underflows, and the rate does not matter beside the reads.  The matrix is
+// read along its unit-stride dim, 16 bytes per lane, as `outer` rows of
+// `inner` elements (one row when it is contiguous).
 template <typename T>
-__global__ __launch_bounds__(256) void muon_norm_kernel(const T *__restrict__ g, MuonView v, double *part)
+__global__ __launch_bounds__(256) void muon_norm_kernel(const T *__restrict__ g, int64_t se, int64_t inner,
+                                                        int64_t outer, int64_t so, double *part)
 {
+    constexpr int N = Piece<T>::N;
     __shared__ double sums[256];
     const int e = blockIdx.y;
-    const T *p = g + e * v.se;
-    // along the unit-stride dim
-    const bool inner_j = v.sj == 1;
-    const int64_t inner = inner_j ? v.n : v.m, outer = inner_j ? v.m : v.n, so = inner_j ? v.si : v.sj;
-    const int64_t sin = inner_j ? v.sj : v.si;
+    const T *p = g + e * se;
     double s = 0.0;
-    const int64_t total = inner * outer;
-    for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < total; k += (int64_t)kNormParts * 256) {
-        const int64_t o = k / inner, i = k % inner;
-        const double x = (double)muon_elem<T>(p + o * so + i * sin);
-        s += x * x;
+    const int64_t span = 256 * N * 4, chunks = (inner + span - 1) / span;
+    for (int64_t item = blockIdx.x; item < outer * chunks; item += kNormParts) {
+        const int64_t o = item / chunks, i0 = (item - o * chunks) * span + threadIdx.x * N;
+        const T *row = p + o * so;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + u * 256 * N;
+            if (i + N <= inner) {
+                const Piece<T> v = ld_piece<T>(row + i);
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    s = fma((double)v.get(k), (double)v.get(k), s);
+            } else {
+                for (int64_t k = i; k < inner; ++k) {
+                    const double x = (double)Piece<T>::to_f32(row[k]);
+                    s = fma(x, x, s);
+                }
+            }
+        }
     }
     sums[threadIdx.x] = s;
     __syncthreads();
@@ -113,36 +119,78 @@ __global__ __launch_bounds__(256) void muon_norm_kernel(const T *__restrict__ g,
 }
 
 // X = G / (norm + eps) into the padded buffers, 64 x 64 elements per
-// workgroup through LDS, so that both layouts are written in rows.
+// workgroup.  A lane takes 8 elements along G's unit-stride dim and passes
+// them through LDS to lanes that hold 8 along X's rows.
 template <typename T>
 __global__ __launch_bounds__(256) void muon_load_kernel(const T *__restrict__ g, MuonView v, MuonBuffers b, float eps)
 {
     __shared__ float tile[64][65];
+    __shared__ double sums[256];
+    const int tid = threadIdx.x;
     const int e = blockIdx.z, i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-    double s = 0.0;
-    for (int k = 0; k < kNormParts; ++k)
-        s += b.part[(int64_t)e * kNormParts + k];
+    sums[tid] = b.part[(int64_t)e * kNormParts + tid];
+    __syncthreads();
+    for (int m = 128; m > 0; m >>= 1) {
+        if (tid < m)
+            sums[tid] += sums[tid + m];
+        __syncthreads();
+    }
     // in fp64: the reciprocal of a tiny norm overflows fp32
-    const double mul = (double)kScaleX / (sqrt(s) + (double)eps);
+    const double mul = (double)kScaleX / (sqrt(sums[0]) + (double)eps);
     const T *p = g + e * v.se;
-    const int lane = threadIdx.x & 63, row = threadIdx.x >> 6;
     const bool inner_j = v.sj == 1;
-    for (int r = row; r < 64; r += 4) {
-        const int i = inner_j ? r : lane, j = inner_j ? lane : r;
-        float x = 0.0f;
-        if (i0 + i < v.m && j0 + j < v.n)
-            x = (float)((double)muon_elem<T>(p + (i0 + i) * v.si + (j0 + j) * v.sj) * mul);
-        tile[i][j] = x;
+    const int n_in = inner_j ? v.n - j0 : v.m - i0, n_out = inner_j ? v.m - i0 : v.n - j0;
+    const int64_t so = inner_j ? v.si : v.sj;
+    p += inner_j ? (int64_t)i0 * v.si + j0 : (int64_t)j0 * v.sj + i0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int o = (tid >> 3) + 32 * h, in = (tid & 7) * 8;
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] = 0.0f;
+        if (o < n_out) {
+            const T *row = p + o * so + in;
+            if (in + 8 <= n_in) {
+#pragma unroll
+                for (int q = 0; q < 8; q += Piece<T>::N) {
+                    const Piece<T> w = ld_piece<T>(row + q);
+#pragma unroll
+                    for (int k = 0; k < Piece<T>::N; ++k)
+                        x[q + k] = w.get(k);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (in + k < n_in)
+                        x[k] = Piece<T>::to_f32(row[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float y = (float)((double)x[k] * mul);
+            if (inner_j)
+                tile[o][in + k] = y;
+            else
+                tile[in + k][o] = y;
+        }
     }
     __syncthreads();
     const int64_t xo = (int64_t)e * b.mp * b.np;
-    for (int r = row; r < 64; r += 4) {
-        _Float16 hi, lo;
-        split_half(tile[r][lane], hi, lo);
-        b.xh[xo + (int64_t)(i0 + r) * b.np + j0 + lane] = hi;
-        b.xl[xo + (int64_t)(i0 + r) * b.np + j0 + lane] = lo;
-        split_half(tile[lane][r], hi, lo);
-        b.xt[0][xo + (int64_t)(j0 + r) * b.mp + i0 + lane] = hi;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = (tid >> 3) + 32 * h, j = (tid & 7) * 8;
+        half8 hi, lo;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            _Float16 a, c;
+            split_half(tile[i][j + k], a, c);
+            hi[k] = a;
+            lo[k] = c;
+        }
+        const int64_t at = xo + (int64_t)(i0 + i) * b.np + j0 + j;
+        *reinterpret_cast<half8 *>(b.xh[0] + at) = hi;
+        *reinterpret_cast<half8 *>(b.xl + at) = lo;
     }
 }
 
@@ -156,202 +204,316 @@ __device__ __forceinline__ void load_lds16(const void *src, uint32_t lds)
                                      (__attribute__((address_space(3))) void *)(uintptr_t)lds, 16, 0, 0);
 }
 
-// This wave's loads into LDS have landed and its LDS reads have returned;
-// then the workgroup meets.
-__device__ __forceinline__ void wait_tiles()
+// At most PENDING of this wave's loads into LDS are still on their way and its
+// LDS reads have returned; then the workgroup meets.
+template <int PENDING>
+__device__ __forceinline__ void wait_stage()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\t"
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\t"
                  "s_barrier"
                  :
-                 :
+                 : "n"(PENDING)
                  : "memory");
+}
+
+// four rows (summed dim) by 16 columns of f16, one column per lane: lane i of
+// 16 points at row i / 4, columns 4 (i % 4) and receives column i of all four
+__device__ __forceinline__ half4 read_transposed(const _Float16 *p)
+{
+    typedef short short4v __attribute__((ext_vector_type(4)));
+    const uint32_t a = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+    return __builtin_bit_cast(half4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) short4v *)(uintptr_t)a));
 }
 
 enum MuonMode { kModeA, kModeB, kModeX, kModeOut };
 
 struct MuonStep {
     float a, b, c, out_scale;
-    int cur;  // which xt holds X now
+    int cur;  // which xh holds X now
 };
 
-// C[i][j] = sum_k P[i][k] Q[j][k] on TM x TN tiles, WM x WN waves.
-//   kModeA  P = Q = X (K = np): off-diagonal A in two parts, diagonal d
-//   kModeB  P = Q = O (K = mp): off-diagonal B, diagonal db
-//   kModeX  P = B, Q = X^T (K = mp): the next X in its three forms
-//   kModeOut  the same, written to the caller's output instead
-template <int MODE, int TM, int TN, int WM, int WN, typename TO = uint16_t>
-__global__ __launch_bounds__(WM *WN * 64) void muon_product_kernel(MuonBuffers b, MuonStep st, TO *out, MuonView ov)
+// One tile edge, wave grid and depth of the pipeline of the products.
+//   TM x TN  tile of the result, WM x WN waves, NST stages of kBK in LDS
+template <int TM_, int TN_, int WM_, int WN_, int NST_>
+struct MuonTile {
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, NST = NST_;
+    static constexpr int THREADS = WM * WN * 64;
+    static constexpr int FP = TM / WM / 16, FQ = TN / WN / 16;  // 16 x 16 fragments of a wave
+    static constexpr int STAGE = (TM + TN) * kBK;               // f16 elements of a stage
+    static constexpr int LOADS = STAGE * 2 / 16 / THREADS;      // 16-byte loads of a thread
+    static constexpr int SYM_STEP = TM / TN;                    // column tiles per row tile on the diagonal
+};
+
+// C[i][j] = sum_k P[i][k] Q[k][j].
+//   kModeA    P = X, Q = X^T: off-diagonal A in two parts, diagonal d
+//   kModeB    P = Q = O (symmetric): off-diagonal B, diagonal db
+//   kModeX    P = B, Q = X: the next X in both parts
+//   kModeOut  the same, to the caller's output
+//
+// A stage holds TM rows of P, 32 elements (4 chunks of 16 bytes) each, chunk c
+// of row r at c ^ ((r >> 2) & 3); then Q, in the symmetric modes as TN rows
+// like P's, else as 32 rows of TN elements whose 32-byte chunks are exchanged
+// by row, so that the lanes of one LDS read fall on different banks.  Loads
+// into LDS are linear; the exchange is in the addresses they read.
+template <int MODE, typename TILE>
+__global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuffers b, MuonStep st, uint16_t *out,
+                                                                     MuonView ov)
 {
-    constexpr int THREADS = WM * WN * 64;
+    constexpr int TM = TILE::TM, TN = TILE::TN, THREADS = TILE::THREADS, FP = TILE::FP, FQ = TILE::FQ;
+    constexpr int NST = TILE::NST, STAGE = TILE::STAGE, LOADS = TILE::LOADS;
     constexpr bool SYM = MODE == kModeA || MODE == kModeB;
-    constexpr int FM = TM / WM / 16, FN = TN / WN / 16;  // 16 x 16 fragments of a wave
-    constexpr int STAGE = (TM + TN) * kBK;               // f16 elements of one LDS stage
-    static_assert(!SYM || TM == TN, "symmetric products use square tiles");
-    __shared__ _Float16 lds[2 * STAGE];
+    __shared__ __attribute__((aligned(16))) _Float16 lds[NST * STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WN, wn = wave % WN;
+    const int wp = wave / TILE::WN, wq = wave % TILE::WN;
 
-    // tile of this workgroup.  Workgroups go to the 8 XCDs in turn: give each
-    // XCD a contiguous run of tiles, so neighbours share operand rows in its L2
+    // tile of this workgroup.  Workgroups go to the 8 XCDs in turn: each XCD
+    // gets a contiguous run of tiles, so neighbours share operands in its L2
     const int total = gridDim.x, xcd = blockIdx.x & 7, per = total >> 3, rem = total & 7;
     const int id = xcd * per + min(xcd, rem) + (blockIdx.x >> 3);
-    const int tm = b.mp / TM, tn = SYM ? tm : b.np / TN;
-    const int per_matrix = SYM ? tm * (tm + 1) / 2 : tm * tn;
+    const int tm = b.mp / TM, tn = SYM ? b.mp / TN : b.np / TN;
+    constexpr int SS = TILE::SYM_STEP;
+    const int per_matrix = SYM ? SS * (tm * (tm + 1) / 2) : tm * tn;
     const int e = id / per_matrix;
-    int t = id % per_matrix, bi, bj;
+    const int t = id % per_matrix;
+    int bi, bj;
     if (SYM) {
-        bi = (int)((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
-        while ((bi + 1) * (bi + 2) / 2 <= t)
+        // row tile bi has the SS (bi + 1) column tiles up to its diagonal block
+        const int q = t / SS;
+        bi = (int)((sqrtf(8.0f * q + 1.0f) - 1.0f) * 0.5f);
+        while ((bi + 1) * (bi + 2) / 2 <= q)
             ++bi;
-        while (bi * (bi + 1) / 2 > t)
+        while (bi * (bi + 1) / 2 > q)
             --bi;
-        bj = t - bi * (bi + 1) / 2;
+        bj = t - SS * (bi * (bi + 1) / 2);
     } else {
         bi = t % tm;
         bj = t / tm;
     }
     const int64_t xo = (int64_t)e * b.mp * b.np, ao = (int64_t)e * b.mp * b.mp;
     const int K = MODE == kModeA ? b.np : b.mp;
-    const _Float16 *P, *Q;
-    if (MODE == kModeA)
-        P = Q = b.xh + xo;
-    else if (MODE == kModeB)
-        P = Q = b.oh + ao;
-    else {
-        P = b.bo + ao;
-        Q = b.xt[st.cur] + xo;
-    }
+    const _Float16 *P = MODE == kModeA ? b.xh[st.cur] + xo : MODE == kModeB ? b.oh + ao : b.bo + ao;
+    const _Float16 *Q = SYM ? P + (int64_t)bj * TN * K : b.xh[st.cur] + xo + (int64_t)bj * TN;
     P += (int64_t)bi * TM * K;
-    Q += (int64_t)bj * TN * K;
+    const int64_t ldq = SYM ? K : b.np;
 
-    // A stage holds TM rows of P, then TN rows of Q, 64 elements (8 chunks of
-    // 16 bytes) each; chunk c of row r lies at chunk c ^ ((r >> 1) & 7), so
-    // that the 16 rows a fragment read touches fall on different banks.  The
-    // loads into LDS are linear; the swizzle is in the address they read.
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds;
-    auto load_stage = [&](int kt, int s) {
+    // 32-byte chunk exchange of a row of Q in the transposed reads
+    auto qswap = [](int k) {
+        return TN >= 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+    };
+    // this thread's part of a stage: one source pointer per load, moved on by
+    // a stage each time
+    const _Float16 *src[LOADS];
 #pragma unroll
-        for (int u = 0; u < (TM + TN) * 8 / THREADS; ++u) {
-            const int slot = u * THREADS + tid;          // 16-byte slot of the stage
-            const int r = slot >> 3, c = (slot & 7) ^ ((r >> 1) & 7);
-            const _Float16 *src = r < TM ? P + (int64_t)r * K : Q + (int64_t)(r - TM) * K;
+    for (int u = 0; u < LOADS; ++u) {
+        const int slot = u * THREADS + tid;  // 16-byte slot of the stage
+        if (slot < TM * 4) {
+            const int r = slot >> 2, c = (slot & 3) ^ ((r >> 2) & 3);
+            src[u] = P + (int64_t)r * K + c * 8;
+        } else if (SYM) {
+            const int s = slot - TM * 4, r = s >> 2, c = (s & 3) ^ ((r >> 2) & 3);
+            src[u] = Q + (int64_t)r * K + c * 8;
+        } else {
+            const int s = slot - TM * 4, k = s / (TN / 8), c = (s % (TN / 8)) ^ (qswap(k) << 1);
+            src[u] = Q + (int64_t)k * ldq + c * 8;
+        }
+    }
+    const int64_t qstep = SYM ? kBK : kBK * ldq;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds;
+    auto load_stage = [&](int s) {
+#pragma unroll
+        for (int u = 0; u < LOADS; ++u) {
             const uint32_t dst = lds0 + (uint32_t)(s * STAGE * 2 + (u * THREADS + wave * 64) * 16);
-            load_lds16(src + kt * kBK + c * 8, __builtin_amdgcn_readfirstlane(dst));
+            load_lds16(src[u], __builtin_amdgcn_readfirstlane(dst));
+            src[u] += u * THREADS < TM * 4 ? kBK : qstep;
         }
     };
+    static_assert(TM * 4 % THREADS == 0, "a load is of P or of Q for the whole workgroup");
 
-    float4v acc[FM][FN];
+    float4v acc[FP][FQ];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < FP; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < FQ; ++j)
             acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const int kt_end = K / kBK;
     const int fr = lane & 15, fk = lane >> 4;
-    load_stage(0, 0);
-    wait_tiles();
-    for (int kt = 0; kt < kt_end; ++kt) {
-        if (kt + 1 < kt_end)
-            load_stage(kt + 1, (kt + 1) & 1);
-        const _Float16 *base = lds + (kt & 1) * STAGE;
+    auto compute = [&](int s) {
+        const _Float16 *pb = lds + s * STAGE, *qb = pb + TM * kBK;
+        half8 pf[FP], qf[FQ];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            half8 pf[FM], qf[FN];
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int r = wm * FM * 16 + i * 16 + fr;
-                pf[i] = *reinterpret_cast<const half8 *>(base + r * kBK + (((ks * 4 + fk) ^ ((r >> 1) & 7)) * 8));
+        for (int j = 0; j < FQ; ++j) {
+            const int j0 = (wq * FQ + j) * 16;
+            if constexpr (SYM) {
+                const int r = j0 + fr;
+                qf[j] = *reinterpret_cast<const half8 *>(qb + r * kBK + ((fk ^ ((r >> 2) & 3)) * 8));
+            } else {
+                // rows 8 fk + 0..3, then + 4..7
+                const int k = 8 * fk + (fr >> 2), c = (j0 / 16) ^ qswap(k);
+                const half4 a = read_transposed(qb + k * TN + c * 16 + (fr & 3) * 4);
+                const half4 h = read_transposed(qb + (k + 4) * TN + ((j0 / 16) ^ qswap(k + 4)) * 16 + (fr & 3) * 4);
+                qf[j] = half8{a[0], a[1], a[2], a[3], h[0], h[1], h[2], h[3]};
             }
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const int r = TM + wn * FN * 16 + j * 16 + fr;
-                qf[j] = *reinterpret_cast<const half8 *>(base + r * kBK + (((ks * 4 + fk) ^ ((r >> 1) & 7)) * 8));
-            }
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(pf[i], qf[j], acc[i][j], 0, 0, 0);
         }
-        wait_tiles();
+#pragma unroll
+        for (int i = 0; i < FP; ++i) {
+            const int r = (wp * FP + i) * 16 + fr;
+            pf[i] = *reinterpret_cast<const half8 *>(pb + r * kBK + ((fk ^ ((r >> 2) & 3)) * 8));
+        }
+        // Q is the first operand: a lane's four results lie along j
+#pragma unroll
+        for (int i = 0; i < FP; ++i)
+#pragma unroll
+            for (int j = 0; j < FQ; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[j], pf[i], acc[i][j], 0, 0, 0);
+    };
+
+    // Stage kt is computed while NST - 1 later ones load.  One barrier per
+    // stage: after it every wave has the stage, and none still reads the
+    // stage before, which the next load overwrites.
+    const int end = K / kBK;
+    for (int s = 0; s < NST - 1; ++s)
+        if (s < end)
+            load_stage(s);
+    int s_now = 0, s_next = NST - 1;
+    int kt = 0;
+    for (; kt + NST - 1 < end; ++kt) {
+        wait_stage<(NST - 2) * LOADS>();
+        load_stage(s_next);
+        compute(s_now);
+        s_now = s_now + 1 == NST ? 0 : s_now + 1;
+        s_next = s_next + 1 == NST ? 0 : s_next + 1;
+    }
+    for (; kt < end; ++kt) {
+        wait_stage<0>();
+        compute(s_now);
+        s_now = s_now + 1 == NST ? 0 : s_now + 1;
     }
 
-    // lane l holds rows 4 (l / 16) + 0..3 of column l % 16 of each fragment
-    const int gi0 = bi * TM + wm * FM * 16 + 4 * fk, gj0 = bj * TN + wn * FN * 16 + fr;
-    const bool mirror = SYM && bi != bj;
+    // Lane l holds row l % 16, columns 4 (l / 16) + 0..3 of each fragment.
+    const int wi0 = bi * TM + wp * FP * 16, wj0 = bj * TN + wq * FQ * 16;
+    // Values stored a second time transposed go through LDS, RC rows of the
+    // wave's part at a time, each wave in its own region.
+    constexpr int WI = FP * 16, WJ = FQ * 16, RC = WI < 64 ? WI : 64, LDT = WJ + 8;
+    static_assert(RC * LDT * THREADS / 64 <= NST * STAGE, "the transposition fits in the stages");
+    _Float16 *turn = lds + wave * RC * LDT;
+    const bool turned = SYM ? bj < bi * SS : MODE == kModeOut && ov.si == 1 && ov.sj != 1;
+    if (turned)
+        wait_stage<0>();  // every wave is done with the stages
+    const float *d = b.d + (int64_t)e * b.mp, *db = b.db + (int64_t)e * b.mp;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int ic = 0; ic < WI; ic += RC) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int gi = gi0 + 16 * i, gj = gj0 + 16 * j;
-            if constexpr (MODE == kModeA) {
-                half4 hi, lo;
+        for (int i = ic / 16; i < (ic + RC) / 16; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float v = acc[i][j][r] * (1.0f / (kScaleX * kScaleX));
-                    const bool diag = gi + r == gj;
-                    if (diag)
-                        b.d[(int64_t)e * b.mp + gj] = v;
-                    _Float16 h, l;
-                    split_half(diag ? 0.0f : v * kScaleA, h, l);
-                    hi[r] = h;
-                    lo[r] = l;
-                    b.oh[ao + (int64_t)(gi + r) * b.mp + gj] = h;
-                    b.ol[ao + (int64_t)(gi + r) * b.mp + gj] = l;
-                }
-                if (mirror) {
-                    *reinterpret_cast<half4 *>(b.oh + ao + (int64_t)gj * b.mp + gi) = hi;
-                    *reinterpret_cast<half4 *>(b.ol + ao + (int64_t)gj * b.mp + gi) = lo;
-                }
-            } else if constexpr (MODE == kModeB) {
-                const float *d = b.d + (int64_t)e * b.mp;
-                // O is symmetric: its (gj, gi..gi+3) entries are contiguous
-                const half4 oh = *reinterpret_cast<const half4 *>(b.oh + ao + (int64_t)gj * b.mp + gi);
-                const half4 ol = *reinterpret_cast<const half4 *>(b.ol + ao + (int64_t)gj * b.mp + gi);
-                const float dj = d[gj];
+            for (int j = 0; j < FQ; ++j) {
+                const int gi = wi0 + 16 * i + fr, gj = wj0 + 16 * j + 4 * fk;
                 half4 h4;
+                if constexpr (MODE == kModeA) {
+                    half4 l4;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float oo = acc[i][j][r] * (1.0f / (kScaleA * kScaleA));
-                    const float o = join_half(oh[r], ol[r]) * (1.0f / kScaleA);
-                    const bool diag = gi + r == gj;
-                    const float di = d[gi + r];
-                    const float aij = diag ? di : o;
-                    const float a2 = oo + (diag ? di * di : (di + dj) * o);
-                    const float v = st.b * aij + st.c * a2;
-                    if (diag)
-                        b.db[(int64_t)e * b.mp + gj] = v;
-                    h4[r] = (_Float16)(diag ? 0.0f : v * kScaleB);
-                    b.bo[ao + (int64_t)(gi + r) * b.mp + gj] = h4[r];
-                }
-                if (mirror)
-                    *reinterpret_cast<half4 *>(b.bo + ao + (int64_t)gj * b.mp + gi) = h4;
-            } else {
-                const float *db = b.db + (int64_t)e * b.mp;
-                half4 h4;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int64_t at = xo + (int64_t)(gi + r) * b.np + gj;
-                    const float x = join_half(b.xh[at], b.xl[at]);
-                    const float v = (st.a + db[gi + r]) * x + acc[i][j][r] * (1.0f / kScaleB);
-                    if constexpr (MODE == kModeX) {
+                    for (int r = 0; r < 4; ++r) {
+                        const float v = acc[i][j][r] * (1.0f / (kScaleX * kScaleX));
+                        const bool diag = gi == gj + r;
+                        if (diag)
+                            b.d[(int64_t)e * b.mp + gi] = v;
                         _Float16 h, l;
-                        split_half(v, h, l);
+                        split_half(diag ? 0.0f : v * kScaleA, h, l);
                         h4[r] = h;
-                        b.xh[at] = h;
-                        b.xl[at] = l;
-                    } else if (gi + r < ov.m && gj < ov.n) {
-                        const float o = v * st.out_scale;
-                        out[e * ov.se + (int64_t)(gi + r) * ov.si + (int64_t)gj * ov.sj] =
-                            __builtin_bit_cast(uint16_t, (__bf16)o);
+                        l4[r] = l;
+                    }
+                    const int64_t at = ao + (int64_t)gi * b.mp + gj;
+                    *reinterpret_cast<half4 *>(b.oh + at) = h4;
+                    *reinterpret_cast<half4 *>(b.ol + at) = l4;
+                } else if constexpr (MODE == kModeB) {
+                    const int64_t at = ao + (int64_t)gi * b.mp + gj;
+                    const half4 oh = *reinterpret_cast<const half4 *>(b.oh + at);
+                    const half4 ol = *reinterpret_cast<const half4 *>(b.ol + at);
+                    const float di = d[gi];
+                    const float4v dj = *reinterpret_cast<const float4v *>(d + gj);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float oo = acc[i][j][r] * (1.0f / (kScaleA * kScaleA));
+                        const float o = join_half(oh[r], ol[r]) * (1.0f / kScaleA);
+                        const bool diag = gi == gj + r;
+                        const float aij = diag ? di : o;
+                        const float a2 = oo + (diag ? di * di : (di + dj[r]) * o);
+                        const float v = st.b * aij + st.c * a2;
+                        if (diag)
+                            b.db[(int64_t)e * b.mp + gi] = v;
+                        h4[r] = (_Float16)(diag ? 0.0f : v * kScaleB);
+                    }
+                    *reinterpret_cast<half4 *>(b.bo + at) = h4;
+                } else {
+                    const int64_t at = xo + (int64_t)gi * b.np + gj;
+                    const half4 xh = *reinterpret_cast<const half4 *>(b.xh[st.cur] + at);
+                    const half4 xl = *reinterpret_cast<const half4 *>(b.xl + at);
+                    const float own = st.a + db[gi];
+                    half4 l4;
+                    float v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        v[r] = own * join_half(xh[r], xl[r]) + acc[i][j][r] * (1.0f / kScaleB);
+                        if constexpr (MODE == kModeX) {
+                            _Float16 h, l;
+                            split_half(v[r], h, l);
+                            h4[r] = h;
+                            l4[r] = l;
+                        } else {
+                            h4[r] = __builtin_bit_cast(_Float16, (__bf16)(v[r] * st.out_scale));
+                        }
+                    }
+                    if constexpr (MODE == kModeX) {
+                        *reinterpret_cast<half4 *>(b.xh[st.cur ^ 1] + at) = h4;
+                        *reinterpret_cast<half4 *>(b.xl + at) = l4;
+                    } else if (!turned && gi < ov.m) {
+                        typedef _Float16 Out4 __attribute__((ext_vector_type(4), aligned(2)));
+                        _Float16 *o = reinterpret_cast<_Float16 *>(out) + e * ov.se + (int64_t)gi * ov.si;
+                        if (ov.sj == 1 && gj + 4 <= ov.n) {
+                            *reinterpret_cast<Out4 *>(o + gj) = h4;
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (gj + r < ov.n)
+                                    o[(int64_t)(gj + r) * ov.sj] = h4[r];
+                        }
                     }
                 }
-                if constexpr (MODE == kModeX)
-                    *reinterpret_cast<half4 *>(b.xt[st.cur ^ 1] + xo + (int64_t)gj * b.mp + gi) = h4;
+                if (MODE != kModeX && turned)
+                    *reinterpret_cast<half4 *>(turn + ((i * 16 - ic) + fr) * LDT + j * 16 + 4 * fk) = h4;
             }
-        }
+        if (MODE == kModeX || !turned)
+            continue;
+        // lane l reads column l % 16 of rows 8 (l / 16) + 0..7 of a block of 32
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < RC; i += 32)
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) {
+                const int row = i + 8 * fk + (fr >> 2), col = j * 16 + (fr & 3) * 4;
+                const half4 a = read_transposed(turn + row * LDT + col);
+                const half4 h = read_transposed(turn + (row + 4) * LDT + col);
+                const half8 w = {a[0], a[1], a[2], a[3], h[0], h[1], h[2], h[3]};
+                const int gi = wi0 + ic + i + 8 * fk, gj = wj0 + 16 * j + fr;
+                if constexpr (SYM) {
+                    _Float16 *o = (MODE == kModeA ? b.oh : b.bo) + ao + (int64_t)gj * b.mp + gi;
+                    *reinterpret_cast<half8 *>(o) = w;
+                } else if (gj < ov.n) {
+                    typedef _Float16 Out8 __attribute__((ext_vector_type(8), aligned(2)));
+                    _Float16 *o = reinterpret_cast<_Float16 *>(out) + e * ov.se + (int64_t)gj * ov.sj + gi;
+                    if (gi + 8 <= ov.m) {
+                        *reinterpret_cast<Out8 *>(o) = w;
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            if (gi + r < ov.m)
+                                o[r] = w[r];
+                    }
+                }
+            }
+        __builtin_amdgcn_wave_barrier();
+    }
 }
 
 // With no steps the result is scale * X itself.
@@ -361,7 +523,7 @@ __global__ __launch_bounds__(256) void muon_copy_kernel(MuonBuffers b, float mul
     if (i >= ov.m || j >= ov.n)
         return;
     const int64_t at = (int64_t)e * b.mp * b.np + (int64_t)i * b.np + j;
-    out[e * ov.se + i * ov.si + j * ov.sj] = __builtin_bit_cast(uint16_t, (__bf16)(join_half(b.xh[at], b.xl[at]) * mul));
+    out[e * ov.se + i * ov.si + j * ov.sj] = __builtin_bit_cast(uint16_t, (__bf16)(join_half(b.xh[0][at], b.xl[at]) * mul));
 }
 
 }  // namespace mxq
