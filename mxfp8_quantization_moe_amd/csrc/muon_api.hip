@@ -15,11 +15,9 @@ using namespace mxq;
 
 constexpr int64_t kMaxDim = 65536;
 
-// 72 KB of LDS and at most 256 registers: two workgroups per CU, so one's
-// epilogue and LDS reads run beside the other's products
-using TileLarge = MuonTile<256, 128, 2, 2, 3>;
-using TileMedium = MuonTile<128, 128, 2, 2, 4>;
-using TileSmall = MuonTile<64, 64, 2, 2, 8>;
+using TileLarge = MuonTile<256, 256, 2, 4, 64, 2>;
+using TileMedium = MuonTile<128, 128, 2, 2, 32, 4>;
+using TileSmall = MuonTile<64, 64, 2, 2, 32, 8>;
 
 struct MuonPlan {
     int tile;            // 2 large, 1 medium, 0 small
@@ -39,11 +37,11 @@ MuonPlan muon_plan(int64_t count, int64_t rows, int64_t cols)
 #ifdef MXQ_MUON_TILE
     p.tile = MXQ_MUON_TILE;
 #else
-    p.tile = tiles(256, 128) >= 256 ? 2 : tiles(128, 128) >= 256 ? 1 : 0;
+    p.tile = tiles(256, 256) >= 192 ? 2 : tiles(128, 128) >= 256 ? 1 : 0;
 #endif
     const int64_t edge = p.tile == 2 ? 256 : p.tile == 1 ? 128 : 64;
     p.mp = round_up(m, edge);
-    p.np = round_up(n, std::min<int64_t>(edge, 128));
+    p.np = round_up(n, edge);
     p.bytes = count * (6 * p.mp * p.np + 6 * p.mp * p.mp + 8 * p.mp + 8 * kNormParts);
     return p;
 }
@@ -59,7 +57,7 @@ void launch_product(const MuonBuffers &b, const MuonStep &st, int64_t count, uin
 {
     constexpr bool SYM = MODE == kModeA || MODE == kModeB;
     const int64_t tm = b.mp / TILE::TM, tn = b.np / TILE::TN;
-    const int64_t blocks = count * (SYM ? TILE::SYM_STEP * (tm * (tm + 1) / 2) : tm * tn);
+    const int64_t blocks = count * (SYM ? TILE::SS * (tm * (tm + 1) / 2) : tm * tn);
     muon_product_kernel<MODE, TILE><<<dim3((unsigned)blocks), dim3(TILE::THREADS), 0, s>>>(b, st, out, ov);
 }
 

@@ -47,7 +47,7 @@ constexpr float kScaleX = 8192.0f;   // |x| <= 1.3: up to 10650; room to 8
 constexpr float kScaleA = 2048.0f;   // |o| <= 1.7; room to 32
 constexpr float kScaleB = 2048.0f;   // |b| <= 3; room to 32
 constexpr float kLow = 2048.0f;      // the low parts are stored times 2^11
-constexpr int kBK = 32;              // summed elements per LDS stage
+constexpr int kBand = 8;              // row tiles of a band (order of the tiles)
 constexpr int kNormParts = 256;      // partial sums of a matrix's squared norm
 
 // Buffers of one call; matrix e's parts are `e` strides further.
@@ -233,103 +233,284 @@ struct MuonStep {
     int cur;  // which xh holds X now
 };
 
-// One tile edge, wave grid and depth of the pipeline of the products.
-//   TM x TN  tile of the result, WM x WN waves, NST stages of kBK in LDS
-template <int TM_, int TN_, int WM_, int WN_, int NST_>
+// Tile of the result, grid of waves and LDS stages of a product.
+//   TM x TN  tile, WM x WN waves, BK summed elements per stage, NST stages
+template <int TM_, int TN_, int WM_, int WN_, int BK_, int NST_>
 struct MuonTile {
-    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, NST = NST_;
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, BK = BK_, NST = NST_;
     static constexpr int THREADS = WM * WN * 64;
     static constexpr int FP = TM / WM / 16, FQ = TN / WN / 16;  // 16 x 16 fragments of a wave
-    static constexpr int STAGE = (TM + TN) * kBK;               // f16 elements of a stage
+    static constexpr int STAGE = (TM + TN) * BK;                // f16 elements of a stage
     static constexpr int LOADS = STAGE * 2 / 16 / THREADS;      // 16-byte loads of a thread
-    static constexpr int SYM_STEP = TM / TN;                    // column tiles per row tile on the diagonal
+    static constexpr int SS = TM / TN;                          // column tiles per row tile on the diagonal
+    // values turned in LDS on their way out: RC rows of a wave's part at a time
+    static constexpr int RC = FP * 16 < 64 ? FP * 16 : 64, LDT = FQ * 16 + 8;
+    static_assert(RC * LDT * WM * WN <= NST * STAGE, "the transposition fits in the stages");
+    static_assert(TM * BK / 8 % THREADS == 0, "a load is of P or of Q for the whole workgroup");
+    static_assert(TM % TN == 0, "the diagonal blocks are whole tiles");
 };
+
+// Matrix e and tile (bi, bj) of a workgroup.  Workgroups go to the 8 XCDs in
+// turn: each XCD gets a contiguous run of the order below.  Bands of kBand row
+// tiles, columns outermost in a band: the tiles that an XCD works on at a time
+// form a block and share their operands in its L2.
+template <typename TILE, bool SYM>
+__device__ __forceinline__ void muon_tile(int mp, int np, int &e, int &bi, int &bj)
+{
+    const int total = gridDim.x, xcd = blockIdx.x & 7, per = total >> 3, rem = total & 7;
+    const int id = xcd * per + min(xcd, rem) + (blockIdx.x >> 3);
+    constexpr int SS = TILE::SS;
+    const int tm = mp / TILE::TM, tn = SYM ? mp / TILE::TN : np / TILE::TN;
+    const int per_matrix = SYM ? SS * (tm * (tm + 1) / 2) : tm * tn;
+    e = id / per_matrix;
+    int t = id % per_matrix;
+    if (SYM) {
+        // row tile r has the SS (r + 1) column tiles up to its diagonal block
+        int r0 = 0, size = min(kBand, tm);
+        for (;;) {
+            const int r1 = r0 + size, band = SS * ((r1 * (r1 + 1) - r0 * (r0 + 1)) / 2);
+            if (t < band)
+                break;
+            t -= band;
+            r0 = r1;
+            size = min(kBand, tm - r0);
+        }
+        const int full = SS * (r0 + 1) * size;
+        if (t < full) {
+            bj = t / size;
+            bi = r0 + t % size;
+        } else {
+            t -= full;
+            int x = 1;  // row tiles of the band that the column no longer has
+            while (t >= SS * (size - x)) {
+                t -= SS * (size - x);
+                ++x;
+            }
+            bj = SS * (r0 + x) + t / (size - x);
+            bi = r0 + x + t % (size - x);
+        }
+    } else {
+        const int band = t / (kBand * tn), size = min(kBand, tm - band * kBand);
+        t -= band * kBand * tn;
+        bi = band * kBand + t % size;
+        bj = t / size;
+    }
+}
+
+// The stages of a tile's operands in LDS: loads and fragment reads.
+//
+// A stage holds TM rows of P, BK elements each, then Q: in the symmetric modes
+// (QT false) TN rows like P's, else BK rows of TN elements.  Loads into LDS
+// are linear; to spread the lanes of one LDS read over the banks, the order of
+// the chunks of a row is exchanged in the addresses that are loaded.
+//   16-byte chunk c of a row of P is at c ^ rswap(row).  A 16-byte LDS read
+//   runs 16 lanes at a time, lanes 0-3, 12-15, 20-27 first.
+//   32-byte chunk c of row k of a transposed Q is at c ^ qswap(k).
+template <typename TILE, bool QT>
+struct MuonStages {
+    static constexpr int TM = TILE::TM, TN = TILE::TN, BK = TILE::BK, LOADS = TILE::LOADS, CH = BK / 8;
+    const _Float16 *src[LOADS];  // one source pointer per load, moved on by a stage each time
+    int64_t qstep;
+    uint32_t lds0;
+    const _Float16 *lds;
+    int wave, fr, fk;
+
+    static __device__ __forceinline__ int rswap(int r) { return BK == 64 ? (r >> 1) & 7 : -(r >> 2) & 3; }
+    static __device__ __forceinline__ int qswap(int k)
+    {
+        return TN >= 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+    }
+
+    __device__ __forceinline__ MuonStages(const _Float16 *l, const _Float16 *P, const _Float16 *Q, int64_t K,
+                                          int64_t ldq, int w)
+        : qstep(QT ? BK * ldq : BK), lds0((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)l),
+          lds(l), wave(w), fr(threadIdx.x & 15), fk((threadIdx.x & 63) >> 4)
+    {
+#pragma unroll
+        for (int u = 0; u < LOADS; ++u) {
+            const int slot = u * TILE::THREADS + threadIdx.x, s = slot - TM * CH;  // 16-byte slot of the stage
+            if (s < 0) {
+                const int r = slot / CH;
+                src[u] = P + r * K + ((slot % CH) ^ rswap(r)) * 8;
+            } else if (QT) {
+                const int k = s / (TN / 8);
+                src[u] = Q + k * ldq + ((s % (TN / 8)) ^ (qswap(k) << 1)) * 8;
+            } else {
+                const int r = s / CH;
+                src[u] = Q + r * K + ((s % CH) ^ rswap(r)) * 8;
+            }
+        }
+    }
+
+    __device__ __forceinline__ void load(int stage)
+    {
+#pragma unroll
+        for (int u = 0; u < LOADS; ++u) {
+            const uint32_t dst = lds0 + (uint32_t)(stage * TILE::STAGE * 2 + (u * TILE::THREADS + wave * 64) * 16);
+            load_lds16(src[u], __builtin_amdgcn_readfirstlane(dst));
+            src[u] += u * TILE::THREADS < TM * CH ? BK : qstep;
+        }
+    }
+
+    // fragments of 32 summed elements from 32 ks on
+    __device__ __forceinline__ void read(int stage, int ks, int row0, int col0, half8 (&pf)[TILE::FP],
+                                         half8 (&qf)[TILE::FQ]) const
+    {
+        const _Float16 *pb = lds + stage * TILE::STAGE, *qb = pb + TM * BK;
+#pragma unroll
+        for (int j = 0; j < TILE::FQ; ++j) {
+            const int j0 = col0 + j * 16;
+            if constexpr (!QT) {
+                const int r = j0 + fr;
+                qf[j] = *reinterpret_cast<const half8 *>(qb + r * BK + (((ks * 4 + fk) ^ rswap(r)) * 8));
+            } else {
+                // rows 8 fk + 0..3, then + 4..7
+                const int k = 32 * ks + 8 * fk + (fr >> 2), c = (fr & 3) * 4;
+                const half4 a = read_transposed(qb + k * TN + ((j0 / 16) ^ qswap(k)) * 16 + c);
+                const half4 h = read_transposed(qb + (k + 4) * TN + ((j0 / 16) ^ qswap(k + 4)) * 16 + c);
+                qf[j] = half8{a[0], a[1], a[2], a[3], h[0], h[1], h[2], h[3]};
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TILE::FP; ++i) {
+            const int r = row0 + i * 16 + fr;
+            pf[i] = *reinterpret_cast<const half8 *>(pb + r * BK + (((ks * 4 + fk) ^ rswap(r)) * 8));
+        }
+    }
+};
+
+// Q is the first operand: a lane's four results lie along j
+template <typename TILE>
+__device__ __forceinline__ void multiply(const half8 (&pf)[TILE::FP], const half8 (&qf)[TILE::FQ],
+                                         float4v (&acc)[TILE::FP][TILE::FQ])
+{
+#pragma unroll
+    for (int i = 0; i < TILE::FP; ++i)
+#pragma unroll
+        for (int j = 0; j < TILE::FQ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[j], pf[i], acc[i][j], 0, 0, 0);
+}
+
+// Stage kt is computed while NST - 1 later ones load.  One barrier per stage:
+// after it every wave has the stage, and none still reads the stage before,
+// which the next load overwrites.
+template <typename TILE, bool QT>
+__device__ __forceinline__ void run_pipeline(MuonStages<TILE, QT> &st, int end, int row0, int col0,
+                                             float4v (&acc)[TILE::FP][TILE::FQ])
+{
+    constexpr int NST = TILE::NST;
+    half8 pf[TILE::FP], qf[TILE::FQ];
+    auto compute = [&](int s) {
+#pragma unroll
+        for (int ks = 0; ks < TILE::BK / 32; ++ks) {
+            st.read(s, ks, row0, col0, pf, qf);
+            multiply<TILE>(pf, qf, acc);
+        }
+    };
+    for (int s = 0; s < NST - 1; ++s)
+        if (s < end)
+            st.load(s);
+    int now = 0, next = NST - 1, kt = 0;
+    for (; kt + NST - 1 < end; ++kt) {
+        wait_stage<(NST - 2) * TILE::LOADS>();
+        st.load(next);
+        compute(now);
+        now = now + 1 == NST ? 0 : now + 1;
+        next = next + 1 == NST ? 0 : next + 1;
+    }
+    for (; kt < end; ++kt) {
+        wait_stage<0>();
+        compute(now);
+        now = now + 1 == NST ? 0 : now + 1;
+    }
+}
+
+template <bool VM>
+__device__ __forceinline__ void phase_end()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    if (VM)
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Two groups of four waves, one wave of each on every SIMD, half a stage apart:
+// while one group's MFMAs run the other reads its fragments.  A stage takes
+// four phases with a barrier after each (group 1 is one phase behind):
+//   read 0 | multiply 0 | read 1 | multiply 1
+// The next stage's loads are issued while group 0 reads part 0 (group 1 then
+// multiplies part 1 of the stage before); both groups are done reading the
+// buffer that they overwrite, since a read phase ends with its reads returned.
+// Each wave waits for its own loads before the barrier that opens the next
+// stage.
+template <typename TILE, bool QT>
+__device__ __forceinline__ void run_alternating(MuonStages<TILE, QT> &st, int end, int row0, int col0,
+                                                float4v (&acc)[TILE::FP][TILE::FQ])
+{
+    static_assert(TILE::BK == 64 && TILE::NST == 2 && TILE::WM * TILE::WN == 8, "");
+    half8 pf[TILE::FP], qf[TILE::FQ];
+    const bool second = st.wave >= 4;
+    auto products = [&]() {
+        __builtin_amdgcn_s_setprio(1);
+        multiply<TILE>(pf, qf, acc);
+        __builtin_amdgcn_s_setprio(0);
+    };
+    st.load(0);
+    phase_end<true>();
+    if (second) {
+        if (end > 1)
+            st.load(1);
+        phase_end<false>();
+    }
+    for (int kt = 0; kt < end; ++kt) {
+        const int s = kt & 1;
+        if (!second && kt + 1 < end)
+            st.load(s ^ 1);
+        st.read(s, 0, row0, col0, pf, qf);
+        phase_end<false>();
+        products();
+        phase_end<false>();
+        st.read(s, 1, row0, col0, pf, qf);
+        if (second)
+            phase_end<true>();
+        else
+            phase_end<false>();
+        if (second && kt + 2 < end)
+            st.load(s);
+        products();
+        if (second)
+            phase_end<false>();
+        else
+            phase_end<true>();
+    }
+    if (!second)
+        phase_end<false>();
+}
 
 // C[i][j] = sum_k P[i][k] Q[k][j].
 //   kModeA    P = X, Q = X^T: off-diagonal A in two parts, diagonal d
 //   kModeB    P = Q = O (symmetric): off-diagonal B, diagonal db
 //   kModeX    P = B, Q = X: the next X in both parts
 //   kModeOut  the same, to the caller's output
-//
-// A stage holds TM rows of P, 32 elements (4 chunks of 16 bytes) each, chunk c
-// of row r at c ^ ((r >> 2) & 3); then Q, in the symmetric modes as TN rows
-// like P's, else as 32 rows of TN elements whose 32-byte chunks are exchanged
-// by row, so that the lanes of one LDS read fall on different banks.  Loads
-// into LDS are linear; the exchange is in the addresses they read.
 template <int MODE, typename TILE>
 __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuffers b, MuonStep st, uint16_t *out,
                                                                      MuonView ov)
 {
-    constexpr int TM = TILE::TM, TN = TILE::TN, THREADS = TILE::THREADS, FP = TILE::FP, FQ = TILE::FQ;
-    constexpr int NST = TILE::NST, STAGE = TILE::STAGE, LOADS = TILE::LOADS;
+    constexpr int TM = TILE::TM, TN = TILE::TN, FP = TILE::FP, FQ = TILE::FQ;
     constexpr bool SYM = MODE == kModeA || MODE == kModeB;
-    __shared__ __attribute__((aligned(16))) _Float16 lds[NST * STAGE];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    __shared__ __attribute__((aligned(16))) _Float16 lds[TILE::NST * TILE::STAGE];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave / TILE::WN, wq = wave % TILE::WN;
-
-    // tile of this workgroup.  Workgroups go to the 8 XCDs in turn: each XCD
-    // gets a contiguous run of tiles, so neighbours share operands in its L2
-    const int total = gridDim.x, xcd = blockIdx.x & 7, per = total >> 3, rem = total & 7;
-    const int id = xcd * per + min(xcd, rem) + (blockIdx.x >> 3);
-    const int tm = b.mp / TM, tn = SYM ? b.mp / TN : b.np / TN;
-    constexpr int SS = TILE::SYM_STEP;
-    const int per_matrix = SYM ? SS * (tm * (tm + 1) / 2) : tm * tn;
-    const int e = id / per_matrix;
-    const int t = id % per_matrix;
-    int bi, bj;
-    if (SYM) {
-        // row tile bi has the SS (bi + 1) column tiles up to its diagonal block
-        const int q = t / SS;
-        bi = (int)((sqrtf(8.0f * q + 1.0f) - 1.0f) * 0.5f);
-        while ((bi + 1) * (bi + 2) / 2 <= q)
-            ++bi;
-        while (bi * (bi + 1) / 2 > q)
-            --bi;
-        bj = t - SS * (bi * (bi + 1) / 2);
-    } else {
-        bi = t % tm;
-        bj = t / tm;
-    }
+    const int fr = threadIdx.x & 15, fk = (threadIdx.x & 63) >> 4;
+    int e, bi, bj;
+    muon_tile<TILE, SYM>(b.mp, b.np, e, bi, bj);
     const int64_t xo = (int64_t)e * b.mp * b.np, ao = (int64_t)e * b.mp * b.mp;
     const int K = MODE == kModeA ? b.np : b.mp;
     const _Float16 *P = MODE == kModeA ? b.xh[st.cur] + xo : MODE == kModeB ? b.oh + ao : b.bo + ao;
     const _Float16 *Q = SYM ? P + (int64_t)bj * TN * K : b.xh[st.cur] + xo + (int64_t)bj * TN;
-    P += (int64_t)bi * TM * K;
-    const int64_t ldq = SYM ? K : b.np;
-
-    // 32-byte chunk exchange of a row of Q in the transposed reads
-    auto qswap = [](int k) {
-        return TN >= 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
-    };
-    // this thread's part of a stage: one source pointer per load, moved on by
-    // a stage each time
-    const _Float16 *src[LOADS];
-#pragma unroll
-    for (int u = 0; u < LOADS; ++u) {
-        const int slot = u * THREADS + tid;  // 16-byte slot of the stage
-        if (slot < TM * 4) {
-            const int r = slot >> 2, c = (slot & 3) ^ ((r >> 2) & 3);
-            src[u] = P + (int64_t)r * K + c * 8;
-        } else if (SYM) {
-            const int s = slot - TM * 4, r = s >> 2, c = (s & 3) ^ ((r >> 2) & 3);
-            src[u] = Q + (int64_t)r * K + c * 8;
-        } else {
-            const int s = slot - TM * 4, k = s / (TN / 8), c = (s % (TN / 8)) ^ (qswap(k) << 1);
-            src[u] = Q + (int64_t)k * ldq + c * 8;
-        }
-    }
-    const int64_t qstep = SYM ? kBK : kBK * ldq;
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds;
-    auto load_stage = [&](int s) {
-#pragma unroll
-        for (int u = 0; u < LOADS; ++u) {
-            const uint32_t dst = lds0 + (uint32_t)(s * STAGE * 2 + (u * THREADS + wave * 64) * 16);
-            load_lds16(src[u], __builtin_amdgcn_readfirstlane(dst));
-            src[u] += u * THREADS < TM * 4 ? kBK : qstep;
-        }
-    };
-    static_assert(TM * 4 % THREADS == 0, "a load is of P or of Q for the whole workgroup");
+    MuonStages<TILE, !SYM> stages(lds, P + (int64_t)bi * TM * K, Q, K, b.np, wave);
 
     float4v acc[FP][FQ];
 #pragma unroll
@@ -337,68 +518,18 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
 #pragma unroll
         for (int j = 0; j < FQ; ++j)
             acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-
-    const int fr = lane & 15, fk = lane >> 4;
-    auto compute = [&](int s) {
-        const _Float16 *pb = lds + s * STAGE, *qb = pb + TM * kBK;
-        half8 pf[FP], qf[FQ];
-#pragma unroll
-        for (int j = 0; j < FQ; ++j) {
-            const int j0 = (wq * FQ + j) * 16;
-            if constexpr (SYM) {
-                const int r = j0 + fr;
-                qf[j] = *reinterpret_cast<const half8 *>(qb + r * kBK + ((fk ^ ((r >> 2) & 3)) * 8));
-            } else {
-                // rows 8 fk + 0..3, then + 4..7
-                const int k = 8 * fk + (fr >> 2), c = (j0 / 16) ^ qswap(k);
-                const half4 a = read_transposed(qb + k * TN + c * 16 + (fr & 3) * 4);
-                const half4 h = read_transposed(qb + (k + 4) * TN + ((j0 / 16) ^ qswap(k + 4)) * 16 + (fr & 3) * 4);
-                qf[j] = half8{a[0], a[1], a[2], a[3], h[0], h[1], h[2], h[3]};
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < FP; ++i) {
-            const int r = (wp * FP + i) * 16 + fr;
-            pf[i] = *reinterpret_cast<const half8 *>(pb + r * kBK + ((fk ^ ((r >> 2) & 3)) * 8));
-        }
-        // Q is the first operand: a lane's four results lie along j
-#pragma unroll
-        for (int i = 0; i < FP; ++i)
-#pragma unroll
-            for (int j = 0; j < FQ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[j], pf[i], acc[i][j], 0, 0, 0);
-    };
-
-    // Stage kt is computed while NST - 1 later ones load.  One barrier per
-    // stage: after it every wave has the stage, and none still reads the
-    // stage before, which the next load overwrites.
-    const int end = K / kBK;
-    for (int s = 0; s < NST - 1; ++s)
-        if (s < end)
-            load_stage(s);
-    int s_now = 0, s_next = NST - 1;
-    int kt = 0;
-    for (; kt + NST - 1 < end; ++kt) {
-        wait_stage<(NST - 2) * LOADS>();
-        load_stage(s_next);
-        compute(s_now);
-        s_now = s_now + 1 == NST ? 0 : s_now + 1;
-        s_next = s_next + 1 == NST ? 0 : s_next + 1;
-    }
-    for (; kt < end; ++kt) {
-        wait_stage<0>();
-        compute(s_now);
-        s_now = s_now + 1 == NST ? 0 : s_now + 1;
-    }
+    if constexpr (TILE::NST == 2)
+        run_alternating<TILE, !SYM>(stages, K / TILE::BK, wp * FP * 16, wq * FQ * 16, acc);
+    else
+        run_pipeline<TILE, !SYM>(stages, K / TILE::BK, wp * FP * 16, wq * FQ * 16, acc);
 
     // Lane l holds row l % 16, columns 4 (l / 16) + 0..3 of each fragment.
     const int wi0 = bi * TM + wp * FP * 16, wj0 = bj * TN + wq * FQ * 16;
     // Values stored a second time transposed go through LDS, RC rows of the
     // wave's part at a time, each wave in its own region.
-    constexpr int WI = FP * 16, WJ = FQ * 16, RC = WI < 64 ? WI : 64, LDT = WJ + 8;
-    static_assert(RC * LDT * THREADS / 64 <= NST * STAGE, "the transposition fits in the stages");
+    constexpr int WI = FP * 16, RC = TILE::RC, LDT = TILE::LDT;
     _Float16 *turn = lds + wave * RC * LDT;
-    const bool turned = SYM ? bj < bi * SS : MODE == kModeOut && ov.si == 1 && ov.sj != 1;
+    const bool turned = SYM ? bj < bi * TILE::SS : MODE == kModeOut && ov.si == 1 && ov.sj != 1;
     if (turned)
         wait_stage<0>();  // every wave is done with the stages
     const float *d = b.d + (int64_t)e * b.mp, *db = b.db + (int64_t)e * b.mp;
