@@ -243,9 +243,9 @@ struct MuonTile {
     static constexpr int STAGE = (TM + TN) * BK;                // f16 elements of a stage
     static constexpr int LOADS = STAGE * 2 / 16 / THREADS;      // 16-byte loads of a thread
     static constexpr int SS = TM / TN;                          // column tiles per row tile on the diagonal
-    // values turned in LDS on their way out: RC rows of a wave's part at a time
-    static constexpr int RC = FP * 16 < 64 ? FP * 16 : 64, LDT = FQ * 16 + 8;
-    static_assert(RC * LDT * WM * WN <= NST * STAGE, "the transposition fits in the stages");
+    // the results pass through LDS RC rows of a wave's part at a time
+    static constexpr int RC = FP * 16 < 64 ? FP * 16 : 64, WJ = FQ * 16;
+    static_assert(RC * WJ * 2 * WM * WN <= NST * STAGE, "the results fit in the stages");
     static_assert(TM * BK / 8 % THREADS == 0, "a load is of P or of Q for the whole workgroup");
     static_assert(TM % TN == 0, "the diagonal blocks are whole tiles");
 };
@@ -309,9 +309,14 @@ __device__ __forceinline__ void muon_tile(int mp, int np, int &e, int &bi, int &
 template <typename TILE, bool QT>
 struct MuonStages {
     static constexpr int TM = TILE::TM, TN = TILE::TN, BK = TILE::BK, LOADS = TILE::LOADS, CH = BK / 8;
-    const _Float16 *src[LOADS];  // one source pointer per load, moved on by a stage each time
-    int64_t qstep;
-    uint32_t lds0;
+    static constexpr int PL = TM * CH / TILE::THREADS;       // loads of P, then those of Q
+    static constexpr int PR = TILE::THREADS / CH;            // rows of P per load
+    static constexpr int QR = QT ? TILE::THREADS / (TN / 8) : PR;
+    static_assert(PR % 16 == 0 && QR % 16 == 0, "the chunk orders repeat with each load");
+    // a load's address: uniform base (operand, load, stage) + this thread's offset
+    const char *pbase, *qbase;
+    int64_t prow, qrow, qstep;   // bytes from load to load, and of Q from stage to stage
+    uint32_t poff, qoff, lds0;
     const _Float16 *lds;
     int wave, fr, fk;
 
@@ -321,44 +326,56 @@ struct MuonStages {
         return TN >= 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
     }
 
-    __device__ __forceinline__ MuonStages(const _Float16 *l, const _Float16 *P, const _Float16 *Q, int64_t K,
-                                          int64_t ldq, int w)
-        : qstep(QT ? BK * ldq : BK), lds0((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)l),
-          lds(l), wave(w), fr(threadIdx.x & 15), fk((threadIdx.x & 63) >> 4)
+    __device__ __forceinline__ MuonStages(const _Float16 *l, const _Float16 *P, const _Float16 *Q, int K, int ldq,
+                                          int w)
+        : pbase(reinterpret_cast<const char *>(P)), qbase(reinterpret_cast<const char *>(Q)),
+          prow((int64_t)PR * K * 2), qrow((int64_t)QR * (QT ? ldq : K) * 2), qstep(QT ? (int64_t)BK * ldq * 2 : BK * 2),
+          lds0((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)l), lds(l), wave(w),
+          fr(threadIdx.x & 15), fk((threadIdx.x & 63) >> 4)
     {
-#pragma unroll
-        for (int u = 0; u < LOADS; ++u) {
-            const int slot = u * TILE::THREADS + threadIdx.x, s = slot - TM * CH;  // 16-byte slot of the stage
-            if (s < 0) {
-                const int r = slot / CH;
-                src[u] = P + r * K + ((slot % CH) ^ rswap(r)) * 8;
-            } else if (QT) {
-                const int k = s / (TN / 8);
-                src[u] = Q + k * ldq + ((s % (TN / 8)) ^ (qswap(k) << 1)) * 8;
-            } else {
-                const int r = s / CH;
-                src[u] = Q + r * K + ((s % CH) ^ rswap(r)) * 8;
-            }
+        const int t = threadIdx.x, r = t / CH;
+        poff = (uint32_t)(r * K + ((t % CH) ^ rswap(r)) * 8) * 2;
+        if (QT) {
+            const int k = t / (TN / 8);
+            qoff = (uint32_t)(k * ldq + ((t % (TN / 8)) ^ (qswap(k) << 1)) * 8) * 2;
+        } else {
+            qoff = poff;
         }
     }
 
-    __device__ __forceinline__ void load(int stage)
+    // load u of stage kt into LDS stage s
+    __device__ __forceinline__ void load_one(int s, int u, int kt) const
+    {
+        const uint32_t dst = lds0 + (uint32_t)(s * TILE::STAGE * 2 + (u * TILE::THREADS + wave * 64) * 16);
+        const char *base = u < PL ? pbase + u * prow + (int64_t)kt * (BK * 2) : qbase + (u - PL) * qrow + kt * qstep;
+        load_lds16(base + (u < PL ? poff : qoff), __builtin_amdgcn_readfirstlane(dst));
+    }
+
+    __device__ __forceinline__ void load(int s, int kt) const
     {
 #pragma unroll
-        for (int u = 0; u < LOADS; ++u) {
-            const uint32_t dst = lds0 + (uint32_t)(stage * TILE::STAGE * 2 + (u * TILE::THREADS + wave * 64) * 16);
-            load_lds16(src[u], __builtin_amdgcn_readfirstlane(dst));
-            src[u] += u * TILE::THREADS < TM * CH ? BK : qstep;
-        }
+        for (int u = 0; u < LOADS; ++u)
+            load_one(s, u, kt);
     }
 
     // fragments of 32 summed elements from 32 ks on
-    __device__ __forceinline__ void read(int stage, int ks, int row0, int col0, half8 (&pf)[TILE::FP],
-                                         half8 (&qf)[TILE::FQ]) const
+    template <int N>
+    __device__ __forceinline__ void read_p(int stage, int ks, int row0, half8 (&pf)[N]) const
     {
-        const _Float16 *pb = lds + stage * TILE::STAGE, *qb = pb + TM * BK;
+        const _Float16 *pb = lds + stage * TILE::STAGE;
 #pragma unroll
-        for (int j = 0; j < TILE::FQ; ++j) {
+        for (int i = 0; i < N; ++i) {
+            const int r = row0 + i * 16 + fr;
+            pf[i] = *reinterpret_cast<const half8 *>(pb + r * BK + (((ks * 4 + fk) ^ rswap(r)) * 8));
+        }
+    }
+
+    template <int N>
+    __device__ __forceinline__ void read_q(int stage, int ks, int col0, half8 (&qf)[N]) const
+    {
+        const _Float16 *qb = lds + stage * TILE::STAGE + TM * BK;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
             const int j0 = col0 + j * 16;
             if constexpr (!QT) {
                 const int r = j0 + fr;
@@ -371,24 +388,18 @@ struct MuonStages {
                 qf[j] = half8{a[0], a[1], a[2], a[3], h[0], h[1], h[2], h[3]};
             }
         }
-#pragma unroll
-        for (int i = 0; i < TILE::FP; ++i) {
-            const int r = row0 + i * 16 + fr;
-            pf[i] = *reinterpret_cast<const half8 *>(pb + r * BK + (((ks * 4 + fk) ^ rswap(r)) * 8));
-        }
     }
 };
 
 // Q is the first operand: a lane's four results lie along j
-template <typename TILE>
-__device__ __forceinline__ void multiply(const half8 (&pf)[TILE::FP], const half8 (&qf)[TILE::FQ],
-                                         float4v (&acc)[TILE::FP][TILE::FQ])
+template <int I0, int N, int FQ, int FP>
+__device__ __forceinline__ void multiply(const half8 (&pf)[N], const half8 (&qf)[FQ], float4v (&acc)[FP][FQ])
 {
 #pragma unroll
-    for (int i = 0; i < TILE::FP; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < TILE::FQ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[j], pf[i], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < FQ; ++j)
+            acc[I0 + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[j], pf[i], acc[I0 + i][j], 0, 0, 0);
 }
 
 // Stage kt is computed while NST - 1 later ones load.  One barrier per stage:
@@ -403,17 +414,18 @@ __device__ __forceinline__ void run_pipeline(MuonStages<TILE, QT> &st, int end, 
     auto compute = [&](int s) {
 #pragma unroll
         for (int ks = 0; ks < TILE::BK / 32; ++ks) {
-            st.read(s, ks, row0, col0, pf, qf);
-            multiply<TILE>(pf, qf, acc);
+            st.read_q(s, ks, col0, qf);
+            st.read_p(s, ks, row0, pf);
+            multiply<0>(pf, qf, acc);
         }
     };
     for (int s = 0; s < NST - 1; ++s)
         if (s < end)
-            st.load(s);
+            st.load(s, s);
     int now = 0, next = NST - 1, kt = 0;
     for (; kt + NST - 1 < end; ++kt) {
         wait_stage<(NST - 2) * TILE::LOADS>();
-        st.load(next);
+        st.load(next, kt + NST - 1);
         compute(now);
         now = now + 1 == NST ? 0 : now + 1;
         next = next + 1 == NST ? 0 : next + 1;
@@ -425,69 +437,150 @@ __device__ __forceinline__ void run_pipeline(MuonStages<TILE, QT> &st, int end, 
     }
 }
 
-template <bool VM>
+// End of a phase: this wave's LDS reads have returned, at most PENDING of its
+// loads are still on their way (-1: whatever), and the workgroup meets.
+template <int PENDING>
 __device__ __forceinline__ void phase_end()
 {
     __builtin_amdgcn_sched_barrier(0);
-    if (VM)
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if constexpr (PENDING >= 0)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
     else
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Two groups of four waves, one wave of each on every SIMD, half a stage apart:
-// while one group's MFMAs run the other reads its fragments.  A stage takes
-// four phases with a barrier after each (group 1 is one phase behind):
-//   read 0 | multiply 0 | read 1 | multiply 1
-// The next stage's loads are issued while group 0 reads part 0 (group 1 then
-// multiplies part 1 of the stage before); both groups are done reading the
-// buffer that they overwrite, since a read phase ends with its reads returned.
-// Each wave waits for its own loads before the barrier that opens the next
-// stage.
+// Two groups of four waves, one wave of each on every SIMD, one phase apart:
+// while one group's MFMAs run the other reads its fragments.  Group 0 has the
+// upper half of the tile's rows, group 1 the lower; each half's rows are taken
+// in two quarters.  A stage takes four phases with a barrier after each:
+//   ra  read Q and the first quarter     ma  multiply
+//   rb  read the second quarter          mb  multiply
+// and group 1 is in the phase before group 0's.
+//
+// Two stages in LDS, but a stage's parts are loaded as soon as the part that
+// they overwrite has been read by both groups (a read phase ends with its
+// reads returned), two 16-byte loads per thread and phase, so that the loads
+// never queue up and every part has four to six phases (about 500 cycles
+// each) to arrive.  With group 0's phases of stage t:
+//   ra(t)  Q, quarter 0 of t + 1: the last third     (first read in ra(t + 1))
+//   ma(t)  quarters 1 and 3 of t + 1                 (first read in rb(t + 1))
+//   rb(t)  Q, quarter 0 and 2 of t + 2: first third
+//   mb(t)  the second third
+// The loads of a wave return in order: at the end of mb(t) all of Q and
+// quarters 0, 2 of t + 1 have landed when at most the 6 loads issued since are
+// pending; at the end of ma(t) quarters 1, 3 of t when at most 8 are.
 template <typename TILE, bool QT>
-__device__ __forceinline__ void run_alternating(MuonStages<TILE, QT> &st, int end, int row0, int col0,
-                                                float4v (&acc)[TILE::FP][TILE::FQ])
-{
-    static_assert(TILE::BK == 64 && TILE::NST == 2 && TILE::WM * TILE::WN == 8, "");
-    half8 pf[TILE::FP], qf[TILE::FQ];
-    const bool second = st.wave >= 4;
-    auto products = [&]() {
+struct MuonAlternating {
+    static_assert(TILE::BK == 64 && TILE::NST == 2 && TILE::WM == 2 && TILE::WN == 4 && TILE::TM == 256 &&
+                  TILE::TN == 256, "loads 0-3 are the quarters, 4-7 are Q");
+    static constexpr int H = TILE::FP / 2;
+    const MuonStages<TILE, QT> &st;
+    int row0, col0;
+    half8 p0[H], p1[H], q0[TILE::FQ], q1[TILE::FQ];
+
+    __device__ __forceinline__ void load2(int u0, int u1, int kt) const
+    {
+        st.load_one(kt & 1, u0, kt);
+        st.load_one(kt & 1, u1, kt);
+    }
+    __device__ __forceinline__ void load_first(int kt) const { load2(4, 5, kt); }
+    __device__ __forceinline__ void load_second(int kt) const { load2(6, 7, kt); }
+    __device__ __forceinline__ void load_third(int kt) const { load2(0, 2, kt); }
+    __device__ __forceinline__ void load_rest(int kt) const { load2(1, 3, kt); }
+
+    __device__ __forceinline__ void read_a(int s)
+    {
+        st.read_q(s, 0, col0, q0);
+        st.read_p(s, 0, row0, p0);
+        st.read_q(s, 1, col0, q1);
+        st.read_p(s, 1, row0, p1);
+    }
+    __device__ __forceinline__ void read_b(int s)
+    {
+        st.read_p(s, 0, row0 + H * 16, p0);
+        st.read_p(s, 1, row0 + H * 16, p1);
+    }
+    template <int I0>
+    __device__ __forceinline__ void products(float4v (&acc)[TILE::FP][TILE::FQ])
+    {
         __builtin_amdgcn_s_setprio(1);
-        multiply<TILE>(pf, qf, acc);
+        multiply<I0>(p0, q0, acc);
+        multiply<I0>(p1, q1, acc);
         __builtin_amdgcn_s_setprio(0);
-    };
-    st.load(0);
-    phase_end<true>();
-    if (second) {
-        if (end > 1)
-            st.load(1);
-        phase_end<false>();
     }
-    for (int kt = 0; kt < end; ++kt) {
+
+    // one stage; MORE: how many stages follow (0, 1, or 2 for two and more)
+    template <bool SECOND, int MORE>
+    __device__ __forceinline__ void stage(int kt, float4v (&acc)[TILE::FP][TILE::FQ])
+    {
+        constexpr int kQuarters = MORE >= 1 ? 8 : 0, kNext = MORE >= 2 ? 6 : MORE == 1 ? 2 : -1;
         const int s = kt & 1;
-        if (!second && kt + 1 < end)
-            st.load(s ^ 1);
-        st.read(s, 0, row0, col0, pf, qf);
-        phase_end<false>();
-        products();
-        phase_end<false>();
-        st.read(s, 1, row0, col0, pf, qf);
-        if (second)
-            phase_end<true>();
-        else
-            phase_end<false>();
-        if (second && kt + 2 < end)
-            st.load(s);
-        products();
-        if (second)
-            phase_end<false>();
-        else
-            phase_end<true>();
+        if constexpr (!SECOND) {
+            read_a(s);
+            if (MORE >= 1) load_third(kt + 1);
+            phase_end<-1>();
+            if (MORE >= 1) load_rest(kt + 1);
+            products<0>(acc);
+            phase_end<kQuarters>();
+            read_b(s);
+            if (MORE >= 2) load_first(kt + 2);
+            phase_end<-1>();
+            if (MORE >= 2) load_second(kt + 2);
+            products<H>(acc);
+            phase_end<kNext>();
+        } else {
+            read_a(s);
+            if (MORE >= 1) load_rest(kt + 1);
+            phase_end<kQuarters>();
+            if (MORE >= 2) load_first(kt + 2);
+            products<0>(acc);
+            phase_end<-1>();
+            read_b(s);
+            if (MORE >= 2) load_second(kt + 2);
+            phase_end<kNext>();
+            if (MORE >= 2) load_third(kt + 2);
+            products<H>(acc);
+            phase_end<-1>();
+        }
     }
-    if (!second)
-        phase_end<false>();
-}
+
+    template <bool SECOND>
+    __device__ __forceinline__ void run_group(int end, float4v (&acc)[TILE::FP][TILE::FQ])
+    {
+        if (SECOND) {
+            if (end > 1)
+                load_third(1);
+            phase_end<-1>();
+        }
+        int kt = 0;
+        for (; kt + 2 < end; ++kt)
+            stage<SECOND, 2>(kt, acc);
+        if (kt + 1 < end) {
+            stage<SECOND, 1>(kt, acc);
+            ++kt;
+        }
+        stage<SECOND, 0>(kt, acc);
+        if (!SECOND)
+            phase_end<-1>();
+    }
+
+    __device__ __forceinline__ void run(int end, float4v (&acc)[TILE::FP][TILE::FQ])
+    {
+        st.load(0, 0);
+        if (end > 1) {
+            load_first(1);
+            load_second(1);
+            phase_end<4>();
+        } else {
+            phase_end<0>();
+        }
+        if (st.wave >= 4)
+            run_group<true>(end, acc);
+        else
+            run_group<false>(end, acc);
+    }
+};
 
 // C[i][j] = sum_k P[i][k] Q[k][j].
 //   kModeA    P = X, Q = X^T: off-diagonal A in two parts, diagonal d
@@ -519,112 +612,141 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
         for (int j = 0; j < FQ; ++j)
             acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (TILE::NST == 2)
-        run_alternating<TILE, !SYM>(stages, K / TILE::BK, wp * FP * 16, wq * FQ * 16, acc);
+        MuonAlternating<TILE, !SYM>{stages, wp * FP * 16, wq * FQ * 16}.run(K / TILE::BK, acc);
     else
         run_pipeline<TILE, !SYM>(stages, K / TILE::BK, wp * FP * 16, wq * FQ * 16, acc);
 
-    // Lane l holds row l % 16, columns 4 (l / 16) + 0..3 of each fragment.
-    const int wi0 = bi * TM + wp * FP * 16, wj0 = bj * TN + wq * FQ * 16;
-    // Values stored a second time transposed go through LDS, RC rows of the
-    // wave's part at a time, each wave in its own region.
-    constexpr int WI = FP * 16, RC = TILE::RC, LDT = TILE::LDT;
-    _Float16 *turn = lds + wave * RC * LDT;
+    // Results.  A lane holds row l % 16, columns 4 (l / 16) + 0..3 of each
+    // fragment; through LDS (each wave in its own region, RC rows at a time)
+    // it gets 8 consecutive columns of one row instead, so that everything
+    // below is read and written in 16-byte pieces of whole 128-byte lines.
+    constexpr int RC = TILE::RC, WJ = TILE::WJ, LPR = WJ / 8, RPP = 64 / LPR, PASSES = RC / RPP;
+    const int lane = threadIdx.x & 63, pr = lane / LPR, pc = lane % LPR;
+    const int wi0 = bi * TM + wp * FP * 16, wj0 = bj * TN + wq * WJ;
+    // stored a second time (or only) transposed: the mirror of an off-diagonal
+    // tile, and the output of a tall matrix
     const bool turned = SYM ? bj < bi * TILE::SS : MODE == kModeOut && ov.si == 1 && ov.sj != 1;
-    if (turned)
-        wait_stage<0>();  // every wave is done with the stages
-    const float *d = b.d + (int64_t)e * b.mp, *db = b.db + (int64_t)e * b.mp;
+    float *wide = reinterpret_cast<float *>(lds) + wave * RC * WJ;
+    _Float16 *turn = reinterpret_cast<_Float16 *>(wide);
+    // chunk orders of the two uses of the region: 16-byte chunks of fp32 rows,
+    // 32-byte chunks of f16 rows
+    auto wswap = [](int r) { return WJ == 64 ? r & 15 : (r >> 1) & 7; };
+    auto tswap = [](int r) { return WJ == 64 ? ((r >> 1) & 1) | ((r >> 3) & 1) << 1 : (r >> 3) & 1; };
+    float *d = b.d + (int64_t)e * b.mp, *db = b.db + (int64_t)e * b.mp;
+    wait_stage<0>();  // every wave is done with the stages
 #pragma unroll
-    for (int ic = 0; ic < WI; ic += RC) {
+    for (int ic = 0; ic < FP * 16; ic += RC) {
+        // what the results are combined with, on its way while they turn
+        half8 oldh[PASSES], oldl[PASSES];
+        if constexpr (MODE != kModeA) {
 #pragma unroll
-        for (int i = ic / 16; i < (ic + RC) / 16; ++i)
+            for (int p = 0; p < PASSES; ++p) {
+                const int gi = wi0 + ic + p * RPP + pr, gj = wj0 + pc * 8;
+                const int64_t at = MODE == kModeB ? ao + (int64_t)gi * b.mp + gj : xo + (int64_t)gi * b.np + gj;
+                oldh[p] = *reinterpret_cast<const half8 *>((MODE == kModeB ? b.oh : b.xh[st.cur]) + at);
+                oldl[p] = *reinterpret_cast<const half8 *>((MODE == kModeB ? b.ol : b.xl) + at);
+            }
+        }
 #pragma unroll
-            for (int j = 0; j < FQ; ++j) {
-                const int gi = wi0 + 16 * i + fr, gj = wj0 + 16 * j + 4 * fk;
-                half4 h4;
-                if constexpr (MODE == kModeA) {
-                    half4 l4;
+        for (int i = 0; i < RC / 16; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float v = acc[i][j][r] * (1.0f / (kScaleX * kScaleX));
-                        const bool diag = gi == gj + r;
-                        if (diag)
-                            b.d[(int64_t)e * b.mp + gi] = v;
-                        _Float16 h, l;
-                        split_half(diag ? 0.0f : v * kScaleA, h, l);
-                        h4[r] = h;
-                        l4[r] = l;
-                    }
-                    const int64_t at = ao + (int64_t)gi * b.mp + gj;
-                    *reinterpret_cast<half4 *>(b.oh + at) = h4;
-                    *reinterpret_cast<half4 *>(b.ol + at) = l4;
-                } else if constexpr (MODE == kModeB) {
-                    const int64_t at = ao + (int64_t)gi * b.mp + gj;
-                    const half4 oh = *reinterpret_cast<const half4 *>(b.oh + at);
-                    const half4 ol = *reinterpret_cast<const half4 *>(b.ol + at);
-                    const float di = d[gi];
-                    const float4v dj = *reinterpret_cast<const float4v *>(d + gj);
+            for (int j = 0; j < FQ; ++j)
+                *reinterpret_cast<float4v *>(wide + (i * 16 + fr) * WJ + ((4 * j + fk) ^ wswap(i * 16 + fr)) * 4) =
+                    acc[ic / 16 + i][j];
+        __builtin_amdgcn_wave_barrier();
+        half8 h8[PASSES];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float oo = acc[i][j][r] * (1.0f / (kScaleA * kScaleA));
-                        const float o = join_half(oh[r], ol[r]) * (1.0f / kScaleA);
-                        const bool diag = gi == gj + r;
-                        const float aij = diag ? di : o;
-                        const float a2 = oo + (diag ? di * di : (di + dj[r]) * o);
-                        const float v = st.b * aij + st.c * a2;
-                        if (diag)
-                            b.db[(int64_t)e * b.mp + gi] = v;
-                        h4[r] = (_Float16)(diag ? 0.0f : v * kScaleB);
-                    }
-                    *reinterpret_cast<half4 *>(b.bo + at) = h4;
-                } else {
-                    const int64_t at = xo + (int64_t)gi * b.np + gj;
-                    const half4 xh = *reinterpret_cast<const half4 *>(b.xh[st.cur] + at);
-                    const half4 xl = *reinterpret_cast<const half4 *>(b.xl + at);
-                    const float own = st.a + db[gi];
-                    half4 l4;
-                    float v[4];
+        for (int p = 0; p < PASSES; ++p) {
+            const int r = p * RPP + pr, gi = wi0 + ic + r, gj = wj0 + pc * 8;
+            float v[8];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        v[r] = own * join_half(xh[r], xl[r]) + acc[i][j][r] * (1.0f / kScaleB);
-                        if constexpr (MODE == kModeX) {
-                            _Float16 h, l;
-                            split_half(v[r], h, l);
-                            h4[r] = h;
-                            l4[r] = l;
-                        } else {
-                            h4[r] = __builtin_bit_cast(_Float16, (__bf16)(v[r] * st.out_scale));
-                        }
-                    }
+            for (int q = 0; q < 2; ++q) {
+                const float4v x = *reinterpret_cast<const float4v *>(wide + r * WJ + ((2 * pc + q) ^ wswap(r)) * 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[4 * q + k] = x[k];
+            }
+            if constexpr (MODE == kModeA) {
+                half8 l8;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float x = v[k] * (1.0f / (kScaleX * kScaleX));
+                    const bool diag = gi == gj + k;
+                    if (diag)
+                        d[gi] = x;
+                    _Float16 h, l;
+                    split_half(diag ? 0.0f : x * kScaleA, h, l);
+                    h8[p][k] = h;
+                    l8[k] = l;
+                }
+                const int64_t at = ao + (int64_t)gi * b.mp + gj;
+                *reinterpret_cast<half8 *>(b.oh + at) = h8[p];
+                *reinterpret_cast<half8 *>(b.ol + at) = l8;
+            } else if constexpr (MODE == kModeB) {
+                const float di = d[gi];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float oo = v[k] * (1.0f / (kScaleA * kScaleA));
+                    const float o = join_half(oldh[p][k], oldl[p][k]) * (1.0f / kScaleA);
+                    const bool diag = gi == gj + k;
+                    const float aij = diag ? di : o;
+                    const float a2 = oo + (diag ? di * di : (di + d[gj + k]) * o);
+                    const float x = st.b * aij + st.c * a2;
+                    if (diag)
+                        db[gi] = x;
+                    h8[p][k] = (_Float16)(diag ? 0.0f : x * kScaleB);
+                }
+                *reinterpret_cast<half8 *>(b.bo + ao + (int64_t)gi * b.mp + gj) = h8[p];
+            } else {
+                const float own = st.a + db[gi];
+                half8 l8;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float x = own * join_half(oldh[p][k], oldl[p][k]) + v[k] * (1.0f / kScaleB);
                     if constexpr (MODE == kModeX) {
-                        *reinterpret_cast<half4 *>(b.xh[st.cur ^ 1] + at) = h4;
-                        *reinterpret_cast<half4 *>(b.xl + at) = l4;
-                    } else if (!turned && gi < ov.m) {
-                        typedef _Float16 Out4 __attribute__((ext_vector_type(4), aligned(2)));
-                        _Float16 *o = reinterpret_cast<_Float16 *>(out) + e * ov.se + (int64_t)gi * ov.si;
-                        if (ov.sj == 1 && gj + 4 <= ov.n) {
-                            *reinterpret_cast<Out4 *>(o + gj) = h4;
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (gj + r < ov.n)
-                                    o[(int64_t)(gj + r) * ov.sj] = h4[r];
-                        }
+                        _Float16 h, l;
+                        split_half(x, h, l);
+                        h8[p][k] = h;
+                        l8[k] = l;
+                    } else {
+                        h8[p][k] = __builtin_bit_cast(_Float16, (__bf16)(x * st.out_scale));
                     }
                 }
-                if (MODE != kModeX && turned)
-                    *reinterpret_cast<half4 *>(turn + ((i * 16 - ic) + fr) * LDT + j * 16 + 4 * fk) = h4;
+                if constexpr (MODE == kModeX) {
+                    const int64_t at = xo + (int64_t)gi * b.np + gj;
+                    *reinterpret_cast<half8 *>(b.xh[st.cur ^ 1] + at) = h8[p];
+                    *reinterpret_cast<half8 *>(b.xl + at) = l8;
+                } else if (!turned && gi < ov.m) {
+                    typedef _Float16 Out8 __attribute__((ext_vector_type(8), aligned(2)));
+                    _Float16 *o = reinterpret_cast<_Float16 *>(out) + e * ov.se + (int64_t)gi * ov.si;
+                    if (ov.sj == 1 && gj + 8 <= ov.n) {
+                        *reinterpret_cast<Out8 *>(o + gj) = h8[p];
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (gj + k < ov.n)
+                                o[(int64_t)(gj + k) * ov.sj] = h8[p][k];
+                    }
+                }
             }
+        }
+        __builtin_amdgcn_wave_barrier();
         if (MODE == kModeX || !turned)
             continue;
-        // lane l reads column l % 16 of rows 8 (l / 16) + 0..7 of a block of 32
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+            const int r = p * RPP + pr;
+            *reinterpret_cast<half8 *>(turn + r * WJ + (((pc >> 1) ^ tswap(r)) * 2 + (pc & 1)) * 8) = h8[p];
+        }
         __builtin_amdgcn_wave_barrier();
+        // lane l reads column l % 16 of rows 8 (l / 16) + 0..7 of a block of 32
 #pragma unroll
         for (int i = 0; i < RC; i += 32)
 #pragma unroll
             for (int j = 0; j < FQ; ++j) {
-                const int row = i + 8 * fk + (fr >> 2), col = j * 16 + (fr & 3) * 4;
-                const half4 a = read_transposed(turn + row * LDT + col);
-                const half4 h = read_transposed(turn + (row + 4) * LDT + col);
+                const int r = i + 8 * fk + (fr >> 2), c = (fr & 3) * 4;
+                const half4 a = read_transposed(turn + r * WJ + (j ^ tswap(r)) * 16 + c);
+                const half4 h = read_transposed(turn + (r + 4) * WJ + (j ^ tswap(r + 4)) * 16 + c);
                 const half8 w = {a[0], a[1], a[2], a[3], h[0], h[1], h[2], h[3]};
                 const int gi = wi0 + ic + i + 8 * fk, gj = wj0 + 16 * j + fr;
                 if constexpr (SYM) {
@@ -637,9 +759,9 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
                         *reinterpret_cast<Out8 *>(o) = w;
                     } else {
 #pragma unroll
-                        for (int r = 0; r < 8; ++r)
-                            if (gi + r < ov.m)
-                                o[r] = w[r];
+                        for (int k = 0; k < 8; ++k)
+                            if (gi + k < ov.m)
+                                o[k] = w[k];
                     }
                 }
             }
