@@ -633,15 +633,22 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
     auto wswap = [](int r) { return WJ == 64 ? r & 15 : (r >> 1) & 7; };
     auto tswap = [](int r) { return WJ == 64 ? ((r >> 1) & 1) | ((r >> 3) & 1) << 1 : (r >> 3) & 1; };
     float *d = b.d + (int64_t)e * b.mp, *db = b.db + (int64_t)e * b.mp;
+    float dj[8];
+    if constexpr (MODE == kModeB)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            dj[k] = d[wj0 + pc * 8 + k];
     wait_stage<0>();  // every wave is done with the stages
 #pragma unroll
     for (int ic = 0; ic < FP * 16; ic += RC) {
         // what the results are combined with, on its way while they turn
         half8 oldh[PASSES], oldl[PASSES];
+        float di[PASSES];
         if constexpr (MODE != kModeA) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
                 const int gi = wi0 + ic + p * RPP + pr, gj = wj0 + pc * 8;
+                di[p] = MODE == kModeB ? d[gi] : db[gi];
                 const int64_t at = MODE == kModeB ? ao + (int64_t)gi * b.mp + gj : xo + (int64_t)gi * b.np + gj;
                 oldh[p] = *reinterpret_cast<const half8 *>((MODE == kModeB ? b.oh : b.xh[st.cur]) + at);
                 oldl[p] = *reinterpret_cast<const half8 *>((MODE == kModeB ? b.ol : b.xl) + at);
@@ -683,14 +690,13 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
                 *reinterpret_cast<half8 *>(b.oh + at) = h8[p];
                 *reinterpret_cast<half8 *>(b.ol + at) = l8;
             } else if constexpr (MODE == kModeB) {
-                const float di = d[gi];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float oo = v[k] * (1.0f / (kScaleA * kScaleA));
                     const float o = join_half(oldh[p][k], oldl[p][k]) * (1.0f / kScaleA);
                     const bool diag = gi == gj + k;
-                    const float aij = diag ? di : o;
-                    const float a2 = oo + (diag ? di * di : (di + d[gj + k]) * o);
+                    const float aij = diag ? di[p] : o;
+                    const float a2 = oo + (diag ? di[p] * di[p] : (di[p] + dj[k]) * o);
                     const float x = st.b * aij + st.c * a2;
                     if (diag)
                         db[gi] = x;
@@ -698,7 +704,7 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
                 }
                 *reinterpret_cast<half8 *>(b.bo + ao + (int64_t)gi * b.mp + gj) = h8[p];
             } else {
-                const float own = st.a + db[gi];
+                const float own = st.a + di[p];
                 half8 l8;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
