@@ -15,9 +15,11 @@ using namespace mxq;
 
 constexpr int64_t kMaxDim = 65536;
 
+// large: 128 KB of LDS, one workgroup of eight alternating waves per CU;
+// medium: 72 KB, two per CU; small: 48 KB, three per CU
 using TileLarge = MuonTile<256, 256, 2, 4, 64, 2>;
-using TileMedium = MuonTile<128, 128, 2, 2, 32, 4>;
-using TileSmall = MuonTile<64, 64, 2, 2, 32, 8>;
+using TileMedium = MuonTile<128, 64, 4, 2, 64, 3>;
+using TileSmall = MuonTile<64, 64, 2, 2, 64, 3>;
 
 struct MuonPlan {
     int tile;            // 2 large, 1 medium, 0 small
@@ -27,21 +29,28 @@ struct MuonPlan {
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-// Larger tiles reuse each operand byte more and are taken when they still
-// fill the machine.
+// Larger tiles do more per loaded byte, smaller ones fill the machine from
+// fewer rows and pad less.  Measured, the three products of one step: one
+// 512 x 512 matrix 16 / 19 / 64 us with small / medium / large tiles, one
+// 2048 x 2048 83 / 70 / 148 us, four of 1024 x 2048 70 / 64 / 115 us, four of
+// 2048 x 2048 233 / 204 / 174 us, one 4096 x 4096 437 / 374 / 280 us.  So a
+// size is taken from the number of tiles on that gives every CU one, unless
+// its padding costs more than its rate gains (1.33 times medium over large,
+// 1.17 small over medium).
 MuonPlan muon_plan(int64_t count, int64_t rows, int64_t cols)
 {
     const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
+    auto tiles = [&](int64_t t) { return count * ((m + t - 1) / t) * ((n + t - 1) / t); };
+    auto volume = [&](int64_t tm, int64_t tn) { return (double)round_up(m, tm) * round_up(m, tm) * round_up(n, tn); };
     MuonPlan p;
-    auto tiles = [&](int64_t tm, int64_t tn) { return count * ((m + tm - 1) / tm) * ((n + tn - 1) / tn); };
-#ifdef MXQ_MUON_TILE
-    p.tile = MXQ_MUON_TILE;
-#else
-    p.tile = tiles(256, 256) >= 192 ? 2 : tiles(128, 128) >= 256 ? 1 : 0;
-#endif
-    const int64_t edge = p.tile == 2 ? 256 : p.tile == 1 ? 128 : 64;
-    p.mp = round_up(m, edge);
-    p.np = round_up(n, edge);
+    if (tiles(256) >= 192 && volume(256, 256) <= 1.33 * volume(128, 64))
+        p.tile = 2;
+    else if (tiles(128) >= 256 && volume(128, 64) <= 1.17 * volume(64, 64))
+        p.tile = 1;
+    else
+        p.tile = 0;
+    p.mp = round_up(m, p.tile == 2 ? 256 : p.tile == 1 ? 128 : 64);
+    p.np = round_up(n, p.tile == 2 ? 256 : 64);
     p.bytes = count * (6 * p.mp * p.np + 6 * p.mp * p.mp + 8 * p.mp + 8 * kNormParts);
     return p;
 }

@@ -402,39 +402,48 @@ __device__ __forceinline__ void multiply(const half8 (&pf)[N], const half8 (&qf)
             acc[I0 + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(qf[j], pf[i], acc[I0 + i][j], 0, 0, 0);
 }
 
-// Stage kt is computed while NST - 1 later ones load.  One barrier per stage:
-// after it every wave has the stage, and none still reads the stage before,
-// which the next load overwrites.
+// Fragments are read one half stage ahead of their MFMAs: the second half of
+// stage kt beside the products of its first, then, past the stage's one
+// barrier, the first half of stage kt + 1 beside the products of the second.
+// At the barrier every wave has read stage kt and has stage kt + 1; the load
+// of stage kt + NST overwrites stage kt.
 template <typename TILE, bool QT>
-__device__ __forceinline__ void run_pipeline(MuonStages<TILE, QT> &st, int end, int row0, int col0,
+__device__ __forceinline__ void run_pipeline(const MuonStages<TILE, QT> &st, int end, int row0, int col0,
                                              float4v (&acc)[TILE::FP][TILE::FQ])
 {
+    static_assert(TILE::BK == 64, "a stage has two halves");
     constexpr int NST = TILE::NST;
-    half8 pf[TILE::FP], qf[TILE::FQ];
-    auto compute = [&](int s) {
-#pragma unroll
-        for (int ks = 0; ks < TILE::BK / 32; ++ks) {
-            st.read_q(s, ks, col0, qf);
-            st.read_p(s, ks, row0, pf);
-            multiply<0>(pf, qf, acc);
-        }
-    };
-    for (int s = 0; s < NST - 1; ++s)
+    half8 p0[TILE::FP], q0[TILE::FQ], p1[TILE::FP], q1[TILE::FQ];
+    for (int s = 0; s < NST; ++s)
         if (s < end)
             st.load(s, s);
-    int now = 0, next = NST - 1, kt = 0;
-    for (; kt + NST - 1 < end; ++kt) {
-        wait_stage<(NST - 2) * TILE::LOADS>();
-        st.load(next, kt + NST - 1);
-        compute(now);
-        now = now + 1 == NST ? 0 : now + 1;
-        next = next + 1 == NST ? 0 : next + 1;
-    }
-    for (; kt < end; ++kt) {
+    if (end >= NST)
+        wait_stage<(NST - 1) * TILE::LOADS>();
+    else
         wait_stage<0>();
-        compute(now);
-        now = now + 1 == NST ? 0 : now + 1;
+    st.read_q(0, 0, col0, q0);
+    st.read_p(0, 0, row0, p0);
+    int now = 0, kt = 0;
+    for (; kt + 1 < end; ++kt) {
+        const int next = now + 1 == NST ? 0 : now + 1;
+        st.read_q(now, 1, col0, q1);
+        st.read_p(now, 1, row0, p1);
+        multiply<0>(p0, q0, acc);
+        if (kt + NST <= end)
+            wait_stage<(NST - 2) * TILE::LOADS>();
+        else
+            wait_stage<0>();
+        if (kt + NST < end)
+            st.load(now, kt + NST);
+        st.read_q(next, 0, col0, q0);
+        st.read_p(next, 0, row0, p0);
+        multiply<0>(p1, q1, acc);
+        now = next;
     }
+    st.read_q(now, 1, col0, q1);
+    st.read_p(now, 1, row0, p1);
+    multiply<0>(p0, q0, acc);
+    multiply<0>(p1, q1, acc);
 }
 
 // End of a phase: this wave's LDS reads have returned, at most PENDING of its
@@ -611,7 +620,7 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
 #pragma unroll
         for (int j = 0; j < FQ; ++j)
             acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (TILE::NST == 2)
+    if constexpr (TILE::TM == 256)
         MuonAlternating<TILE, !SYM>{stages, wp * FP * 16, wq * FQ * 16}.run(K / TILE::BK, acc);
     else
         run_pipeline<TILE, !SYM>(stages, K / TILE::BK, wp * FP * 16, wq * FQ * 16, acc);
