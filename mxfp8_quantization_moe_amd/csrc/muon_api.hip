@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "mxq.h"
 #include "api_common.hpp"
@@ -18,6 +19,7 @@ constexpr int64_t kMaxDim = 65536;
 // large: 128 KB of LDS, one workgroup of eight alternating waves per CU;
 // medium: 72 KB, two per CU; small: 48 KB, three per CU
 using TileLarge = MuonTile<256, 256, 2, 4, 64, 2>;
+using TileHalf = MuonTile<256, 128, 2, 4, 64, 2>;
 using TileMedium = MuonTile<128, 64, 4, 2, 64, 3>;
 using TileSmall = MuonTile<64, 64, 2, 2, 64, 3>;
 
@@ -60,27 +62,33 @@ bool sizes_ok(int64_t count, int64_t rows, int64_t cols)
     return count >= 0 && rows >= 0 && cols >= 0 && rows <= kMaxDim && cols <= kMaxDim && count <= 65535;
 }
 
-template <int MODE, typename TILE>
+// A grid of large tiles runs in rounds of one tile per CU.  A last round of at
+// most half the CUs is taken as half tiles instead, by all of them.
+constexpr int64_t kCUs = 256;
+
+template <int MODE, typename TILE, typename HALF>
 void launch_product(const MuonBuffers &b, const MuonStep &st, int64_t count, uint16_t *out, const MuonView &ov,
                     hipStream_t s)
 {
     constexpr bool SYM = MODE == kModeA || MODE == kModeB;
     const int64_t tm = b.mp / TILE::TM, tn = b.np / TILE::TN;
-    const int64_t blocks = count * (SYM ? TILE::SS * (tm * (tm + 1) / 2) : tm * tn);
-    muon_product_kernel<MODE, TILE><<<dim3((unsigned)blocks), dim3(TILE::THREADS), 0, s>>>(b, st, out, ov);
+    const int64_t tiles = count * (SYM ? TILE::SS * (tm * (tm + 1) / 2) : tm * tn);
+    const int64_t rest = std::is_same<TILE, HALF>::value || tiles % kCUs > kCUs / 2 ? 0 : tiles % kCUs;
+    muon_product_kernel<MODE, TILE, HALF><<<dim3((unsigned)(tiles + rest)), dim3(TILE::THREADS), 0, s>>>(
+        b, st, out, ov, (int)(tiles - rest));
 }
 
-template <typename TILE>
+template <typename TILE, typename HALF>
 void launch_steps(MuonBuffers &b, MuonStep st, int steps, int64_t count, uint16_t *out, const MuonView &ov,
                   hipStream_t s)
 {
     for (int k = 0; k < steps; ++k) {
-        launch_product<kModeA, TILE>(b, st, count, out, ov, s);
-        launch_product<kModeB, TILE>(b, st, count, out, ov, s);
+        launch_product<kModeA, TILE, HALF>(b, st, count, out, ov, s);
+        launch_product<kModeB, TILE, HALF>(b, st, count, out, ov, s);
         if (k + 1 < steps)
-            launch_product<kModeX, TILE>(b, st, count, out, ov, s);
+            launch_product<kModeX, TILE, HALF>(b, st, count, out, ov, s);
         else
-            launch_product<kModeOut, TILE>(b, st, count, out, ov, s);
+            launch_product<kModeOut, TILE, HALF>(b, st, count, out, ov, s);
         st.cur ^= 1;
     }
 }
@@ -161,11 +169,11 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
         muon_copy_kernel<<<dim3((unsigned)((gv.n + 255) / 256), (unsigned)gv.m, (unsigned)count), dim3(256), 0, s>>>(
             buf, st.out_scale, out, ov);
     else if (p.tile == 2)
-        launch_steps<TileLarge>(buf, st, steps, count, out, ov, s);
+        launch_steps<TileLarge, TileHalf>(buf, st, steps, count, out, ov, s);
     else if (p.tile == 1)
-        launch_steps<TileMedium>(buf, st, steps, count, out, ov, s);
+        launch_steps<TileMedium, TileMedium>(buf, st, steps, count, out, ov, s);
     else
-        launch_steps<TileSmall>(buf, st, steps, count, out, ov, s);
+        launch_steps<TileSmall, TileSmall>(buf, st, steps, count, out, ov, s);
     return launch_status();
 }
 

@@ -34,6 +34,8 @@
 #include <hip/hip_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "moe_rows_kernels.hpp"
 #include "mxq_device.hpp"
 
@@ -250,15 +252,20 @@ struct MuonTile {
     static_assert(TM % TN == 0, "the diagonal blocks are whole tiles");
 };
 
-// Matrix e and tile (bi, bj) of a workgroup.  Workgroups go to the 8 XCDs in
-// turn: each XCD gets a contiguous run of the order below.  Bands of kBand row
-// tiles, columns outermost in a band: the tiles that an XCD works on at a time
-// form a block and share their operands in its L2.
-template <typename TILE, bool SYM>
-__device__ __forceinline__ void muon_tile(int mp, int np, int &e, int &bi, int &bj)
+// Workgroups go to the 8 XCDs in turn; this numbering gives each XCD a
+// contiguous run of 0..total-1.
+__device__ __forceinline__ int xcd_run(int block, int total)
 {
-    const int total = gridDim.x, xcd = blockIdx.x & 7, per = total >> 3, rem = total & 7;
-    const int id = xcd * per + min(xcd, rem) + (blockIdx.x >> 3);
+    const int xcd = block & 7;
+    return xcd * (total >> 3) + min(xcd, total & 7) + (block >> 3);
+}
+
+// Matrix e and tile (bi, bj) number id.  Bands of kBand row tiles, columns
+// outermost in a band: the tiles that an XCD works on at a time form a block
+// and share their operands in its L2.
+template <typename TILE, bool SYM>
+__device__ __forceinline__ void muon_tile(int id, int mp, int np, int &e, int &bi, int &bj)
+{
     constexpr int SS = TILE::SS;
     const int tm = mp / TILE::TM, tn = SYM ? mp / TILE::TN : np / TILE::TN;
     const int per_matrix = SYM ? SS * (tm * (tm + 1) / 2) : tm * tn;
@@ -478,12 +485,14 @@ __device__ __forceinline__ void phase_end()
 //   mb(t)  the second third
 // The loads of a wave return in order: at the end of mb(t) all of Q and
 // quarters 0, 2 of t + 1 have landed when at most the 6 loads issued since are
-// pending; at the end of ma(t) quarters 1, 3 of t when at most 8 are.
+// pending; at the end of ma(t) quarters 1, 3 of t when at most 8 are.  (A tile
+// of 128 columns has two loads of Q, none in the second third, and 4 and 6.)
 template <typename TILE, bool QT>
 struct MuonAlternating {
-    static_assert(TILE::BK == 64 && TILE::NST == 2 && TILE::WM == 2 && TILE::WN == 4 && TILE::TM == 256 &&
-                  TILE::TN == 256, "loads 0-3 are the quarters, 4-7 are Q");
+    static_assert(TILE::BK == 64 && TILE::NST == 2 && TILE::WM == 2 && TILE::WN == 4 && TILE::TM == 256,
+                  "loads 0-3 are the quarters, the rest Q");
     static constexpr int H = TILE::FP / 2;
+    static constexpr int SECOND = TILE::LOADS - 6;  // loads of the second third
     const MuonStages<TILE, QT> &st;
     int row0, col0;
     half8 p0[H], p1[H], q0[TILE::FQ], q1[TILE::FQ];
@@ -494,7 +503,11 @@ struct MuonAlternating {
         st.load_one(kt & 1, u1, kt);
     }
     __device__ __forceinline__ void load_first(int kt) const { load2(4, 5, kt); }
-    __device__ __forceinline__ void load_second(int kt) const { load2(6, 7, kt); }
+    __device__ __forceinline__ void load_second(int kt) const
+    {
+        if constexpr (SECOND == 2)
+            load2(6, 7, kt);
+    }
     __device__ __forceinline__ void load_third(int kt) const { load2(0, 2, kt); }
     __device__ __forceinline__ void load_rest(int kt) const { load2(1, 3, kt); }
 
@@ -520,12 +533,13 @@ struct MuonAlternating {
     }
 
     // one stage; MORE: how many stages follow (0, 1, or 2 for two and more)
-    template <bool SECOND, int MORE>
+    template <bool LATER, int MORE>
     __device__ __forceinline__ void stage(int kt, float4v (&acc)[TILE::FP][TILE::FQ])
     {
-        constexpr int kQuarters = MORE >= 1 ? 8 : 0, kNext = MORE >= 2 ? 6 : MORE == 1 ? 2 : -1;
+        constexpr int kQuarters = MORE >= 1 ? 6 + SECOND : 0;
+        constexpr int kNext = MORE >= 2 ? 4 + SECOND : MORE == 1 ? 2 : -1;
         const int s = kt & 1;
-        if constexpr (!SECOND) {
+        if constexpr (!LATER) {
             read_a(s);
             if (MORE >= 1) load_third(kt + 1);
             phase_end<-1>();
@@ -554,23 +568,23 @@ struct MuonAlternating {
         }
     }
 
-    template <bool SECOND>
+    template <bool LATER>
     __device__ __forceinline__ void run_group(int end, float4v (&acc)[TILE::FP][TILE::FQ])
     {
-        if (SECOND) {
+        if (LATER) {
             if (end > 1)
                 load_third(1);
             phase_end<-1>();
         }
         int kt = 0;
         for (; kt + 2 < end; ++kt)
-            stage<SECOND, 2>(kt, acc);
+            stage<LATER, 2>(kt, acc);
         if (kt + 1 < end) {
-            stage<SECOND, 1>(kt, acc);
+            stage<LATER, 1>(kt, acc);
             ++kt;
         }
-        stage<SECOND, 0>(kt, acc);
-        if (!SECOND)
+        stage<LATER, 0>(kt, acc);
+        if (!LATER)
             phase_end<-1>();
     }
 
@@ -580,7 +594,7 @@ struct MuonAlternating {
         if (end > 1) {
             load_first(1);
             load_second(1);
-            phase_end<4>();
+            phase_end<2 + SECOND>();
         } else {
             phase_end<0>();
         }
@@ -597,22 +611,19 @@ struct MuonAlternating {
 //   kModeX    P = B, Q = X: the next X in both parts
 //   kModeOut  the same, to the caller's output
 template <int MODE, typename TILE>
-__global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuffers b, MuonStep st, uint16_t *out,
-                                                                     MuonView ov)
+__device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b, const MuonStep &st, uint16_t *out,
+                                             const MuonView &ov, int e, int i0, int j0, bool mirror)
 {
-    constexpr int TM = TILE::TM, TN = TILE::TN, FP = TILE::FP, FQ = TILE::FQ;
+    constexpr int FP = TILE::FP, FQ = TILE::FQ;
     constexpr bool SYM = MODE == kModeA || MODE == kModeB;
-    __shared__ __attribute__((aligned(16))) _Float16 lds[TILE::NST * TILE::STAGE];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave / TILE::WN, wq = wave % TILE::WN;
     const int fr = threadIdx.x & 15, fk = (threadIdx.x & 63) >> 4;
-    int e, bi, bj;
-    muon_tile<TILE, SYM>(b.mp, b.np, e, bi, bj);
     const int64_t xo = (int64_t)e * b.mp * b.np, ao = (int64_t)e * b.mp * b.mp;
     const int K = MODE == kModeA ? b.np : b.mp;
     const _Float16 *P = MODE == kModeA ? b.xh[st.cur] + xo : MODE == kModeB ? b.oh + ao : b.bo + ao;
-    const _Float16 *Q = SYM ? P + (int64_t)bj * TN * K : b.xh[st.cur] + xo + (int64_t)bj * TN;
-    MuonStages<TILE, !SYM> stages(lds, P + (int64_t)bi * TM * K, Q, K, b.np, wave);
+    const _Float16 *Q = SYM ? P + (int64_t)j0 * K : b.xh[st.cur] + xo + j0;
+    MuonStages<TILE, !SYM> stages(lds, P + (int64_t)i0 * K, Q, K, b.np, wave);
 
     float4v acc[FP][FQ];
 #pragma unroll
@@ -631,10 +642,10 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
     // below is read and written in 16-byte pieces of whole 128-byte lines.
     constexpr int RC = TILE::RC, WJ = TILE::WJ, LPR = WJ / 8, RPP = 64 / LPR, PASSES = RC / RPP;
     const int lane = threadIdx.x & 63, pr = lane / LPR, pc = lane % LPR;
-    const int wi0 = bi * TM + wp * FP * 16, wj0 = bj * TN + wq * WJ;
+    const int wi0 = i0 + wp * FP * 16, wj0 = j0 + wq * WJ;
     // stored a second time (or only) transposed: the mirror of an off-diagonal
     // tile, and the output of a tall matrix
-    const bool turned = SYM ? bj < bi * TILE::SS : MODE == kModeOut && ov.si == 1 && ov.sj != 1;
+    const bool turned = SYM ? mirror : MODE == kModeOut && ov.si == 1 && ov.sj != 1;
     float *wide = reinterpret_cast<float *>(lds) + wave * RC * WJ;
     _Float16 *turn = reinterpret_cast<_Float16 *>(wide);
     // chunk orders of the two uses of the region: 16-byte chunks of fp32 rows,
@@ -781,6 +792,26 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
                 }
             }
         __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// `whole` workgroups take a tile each; of the tiles after those, two
+// workgroups take the column halves.
+template <int MODE, typename TILE, typename HALF>
+__global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuffers b, MuonStep st, uint16_t *out,
+                                                                     MuonView ov, int whole)
+{
+    constexpr bool SYM = MODE == kModeA || MODE == kModeB;
+    __shared__ __attribute__((aligned(16))) _Float16 lds[TILE::NST * TILE::STAGE];
+    int e, bi, bj;
+    if ((int)blockIdx.x < whole) {
+        muon_tile<TILE, SYM>(xcd_run(blockIdx.x, whole), b.mp, b.np, e, bi, bj);
+        muon_product<MODE, TILE>(lds, b, st, out, ov, e, bi * TILE::TM, bj * TILE::TN, bj < bi * TILE::SS);
+    } else if constexpr (!std::is_same<TILE, HALF>::value) {
+        const int id = xcd_run(blockIdx.x - whole, gridDim.x - whole);
+        muon_tile<TILE, SYM>(whole + (id >> 1), b.mp, b.np, e, bi, bj);
+        muon_product<MODE, HALF>(lds, b, st, out, ov, e, bi * TILE::TM, bj * TILE::TN + (id & 1) * HALF::TN,
+                                 bj < bi * TILE::SS);
     }
 }
 
