@@ -402,8 +402,9 @@ int64_t mxq_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts, int32
  *             f_e = counts_e / (live * top_k), and z = mean of lse^2; both 0
  *             when no token is live.
  * live        1 int32: number of live tokens.
- * workspace   mxq_moe_route_workspace_bytes bytes, 4-byte aligned, contents
- *             arbitrary before and after; too small -> MXQ_ERR_WORKSPACE.
+ * workspace   mxq_moe_route_workspace_bytes bytes (none for up to 64 tokens),
+ *             8-byte aligned, contents arbitrary before and after; too small
+ *             -> MXQ_ERR_WORKSPACE.
  * A NaN logit is never taken and makes the token's probabilities, and the
  * losses, NaN.
  */

@@ -45,64 +45,78 @@ int64_t route_runs(int64_t tokens)
     return tokens > 0 ? (tokens + route_run(tokens) - 1) / route_run(tokens) : 0;
 }
 
+// a single run needs no workspace
 int64_t route_bytes(int64_t tokens, int64_t experts)
 {
-    return route_runs(tokens) * (2 * experts + 2) * 4;
+    const int64_t runs = route_runs(tokens);
+    return runs <= 1 ? 0 : experts * 8 + runs * (2 * experts + 2) * 4;
 }
 
-template <typename T, int L, int V, int THREADS>
-void launch_route(const T *logits, int64_t sl, int tokens, int experts, const uint8_t *mask, int k, int renorm,
-                  int run, int nruns, int32_t *ids, float *weights, int32_t *rows, float *lse,
-                  const RouteWorkspace &ws, hipStream_t st)
-{
-    const size_t lds = (size_t)experts * 12 + (size_t)kRouteTile * (4 + 6 * k);
-    moe_route_kernel<T, L, V, THREADS><<<dim3((unsigned)nruns), dim3(THREADS), lds, st>>>(
-        logits, sl, tokens, experts, mask, k, renorm, run, ids, weights, rows, lse, ws);
-}
-
-// Lanes per token and experts per lane by the number of experts: a lane's
-// logits are one load of up to 16 bytes (32 in fp32), and the fewer lanes a
-// token has the fewer cross-lane steps its reductions take.
-template <typename T, typename F>
+// Lanes per token, experts per lane and threads by the number of experts.
+// Sixteen lanes reduce within a DPP row, without LDS permutes; more experts
+// per lane share those steps among more tokens of a wave.
+template <typename F>
 void by_experts(int experts, F &&f)
 {
+    auto go = [&](auto l, auto v, auto t) { f(l, v, t); };
+#define MXQ_CONFIG(L, V, THREADS)                                                                              \
+    go(std::integral_constant<int, L>(), std::integral_constant<int, V>(), std::integral_constant<int, THREADS>())
     if (experts <= 8)
-        f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>(), std::integral_constant<int, 512>());
+        MXQ_CONFIG(8, 1, 512);
     else if (experts <= 32)
-        f(std::integral_constant<int, 8>(), std::integral_constant<int, 4>(), std::integral_constant<int, 512>());
+        MXQ_CONFIG(8, 4, 512);
+    else if (experts <= 64)
+        MXQ_CONFIG(16, 4, 1024);
     else if (experts <= 128)
-        f(std::integral_constant<int, 16>(), std::integral_constant<int, 8>(), std::integral_constant<int, 1024>());
+        MXQ_CONFIG(16, 8, 1024);
     else if (experts <= 256)
-        f(std::integral_constant<int, 32>(), std::integral_constant<int, 8>(), std::integral_constant<int, 1024>());
+        MXQ_CONFIG(16, 16, 1024);
     else if (experts <= 512)
-        f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>(), std::integral_constant<int, 1024>());
+        MXQ_CONFIG(32, 16, 1024);
     else if (experts <= 1024)
-        f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>(), std::integral_constant<int, 512>());
+        MXQ_CONFIG(64, 16, 1024);
     else
-        f(std::integral_constant<int, 64>(), std::integral_constant<int, 64>(), std::integral_constant<int, 256>());
+        MXQ_CONFIG(64, 64, 256);
+#undef MXQ_CONFIG
 }
 
 template <typename T>
 mxq_status run_route(const void *logits, int64_t sl, int tokens, int experts, const uint8_t *mask, int k,
                      int renorm, int align, int32_t *ids, float *weights, int32_t *rows, float *lse,
-                     int32_t *counts, int32_t *offs, float *mean_prob, float *losses, int32_t *live,
-                     void *workspace, hipStream_t st)
+                     const RouteResults &out, void *workspace, hipStream_t st)
 {
-    const int run = (int)route_run(tokens), nruns = (int)route_runs(tokens);
-    RouteWorkspace ws;
-    ws.counts = reinterpret_cast<int32_t *>(workspace);
-    ws.probs = reinterpret_cast<float *>(ws.counts + (int64_t)nruns * experts);
-    ws.z = ws.probs + (int64_t)nruns * experts;
-    ws.live = reinterpret_cast<int32_t *>(ws.z + nruns);
-    if (nruns > 0)
-        by_experts<T>(experts, [&](auto L, auto V, auto THREADS) {
-            launch_route<T, L(), V(), THREADS()>(reinterpret_cast<const T *>(logits), sl, tokens, experts, mask, k,
-                                                 renorm, run, nruns, ids, weights, rows, lse, ws, st);
-        });
-    const int group = 8;
-    const int blocks = (nruns + group - 1) / group + 1;
-    moe_rank_kernel<<<dim3((unsigned)blocks), dim3(kRankThreads), (size_t)experts * 8, st>>>(
-        tokens, experts, k, align, run, nruns, group, ids, rows, counts, offs, mean_prob, losses, live, ws);
+    const int run = (int)std::max<int64_t>(route_run(tokens), kRouteTile), nruns = (int)route_runs(tokens);
+    RouteWorkspace ws = {};
+    if (nruns > 1) {
+        ws.balance = reinterpret_cast<double *>(workspace);
+        ws.counts = reinterpret_cast<int32_t *>(ws.balance + experts);
+        ws.probs = reinterpret_cast<float *>(ws.counts + (int64_t)nruns * experts);
+        ws.z = ws.probs + (int64_t)nruns * experts;
+        ws.live = reinterpret_cast<int32_t *>(ws.z + nruns);
+    }
+    const size_t lds = (size_t)experts * 12 + (size_t)kRouteTile * (8 + 6 * k);
+    by_experts(experts, [&](auto l, auto v, auto t) {
+        constexpr int L = decltype(l)::value, V = decltype(v)::value, THREADS = decltype(t)::value;
+        constexpr int D8 = V < 8 ? V : 8;
+        auto go = [&](auto kernel) {
+            kernel<<<dim3((unsigned)std::max(nruns, 1)), dim3(THREADS), lds, st>>>(
+                reinterpret_cast<const T *>(logits), sl, tokens, experts, mask, k, renorm, align, run, ids, weights,
+                rows, lse, ws, out);
+        };
+        // a token takes at most k keys from one lane: 8 positions of its list move
+        if (k <= 8)
+            nruns <= 1 ? go(moe_route_kernel<T, L, V, D8, THREADS, true>)
+                       : go(moe_route_kernel<T, L, V, D8, THREADS, false>);
+        else
+            nruns <= 1 ? go(moe_route_kernel<T, L, V, V, THREADS, true>)
+                       : go(moe_route_kernel<T, L, V, V, THREADS, false>);
+    });
+    if (nruns > 1) {
+        moe_scan_kernel<<<dim3((unsigned)((experts + kScanExperts - 1) / kScanExperts)), dim3(kScanThreads), 0, st>>>(
+            experts, nruns, ws, out);
+        moe_place_kernel<<<dim3((unsigned)(nruns + 1)), dim3(kPlaceThreads), (size_t)experts * 4, st>>>(
+            tokens, experts, k, align, run, nruns, ids, rows, ws, out);
+    }
     return launch_status();
 }
 
@@ -112,10 +126,11 @@ mxq_status run_route_backward(const void *logits, int64_t sl, int tokens, int ex
                               const int32_t *live, const float *gw, const float *gl, void *dl, int64_t sd,
                               hipStream_t st)
 {
-    by_experts<T>(experts, [&](auto L, auto V, auto) {
-        const int per = 256 / L();
+    by_experts(experts, [&](auto l, auto v, auto) {
+        constexpr int L = decltype(l)::value, V = decltype(v)::value;
+        const int per = 256 / L;
         const int64_t blocks = std::min<int64_t>(((int64_t)tokens + per - 1) / per, 1 << 20);
-        moe_route_backward_kernel<T, L(), V()><<<dim3((unsigned)blocks), dim3(256), 0, st>>>(
+        moe_route_backward_kernel<T, L, V><<<dim3((unsigned)blocks), dim3(256), 0, st>>>(
             reinterpret_cast<const T *>(logits), sl, tokens, experts, k, renorm, ids, weights, lse, counts, live,
             gw, gl, reinterpret_cast<T *>(dl), sd);
     });
@@ -225,7 +240,7 @@ mxq_status mxq_moe_route(const void *logits, int32_t dtype, int64_t tokens, int3
         return MXQ_ERR_INVALID_ARG;
     if (num_experts > 1 && sl_e != 1)
         return MXQ_ERR_UNSUPPORTED;
-    if (sl_t < 0 || !aligned_to(logits, dtype_size(dtype)) || !aligned_to(workspace, 4))
+    if (sl_t < 0 || !aligned_to(logits, dtype_size(dtype)) || !aligned_to(workspace, 8))
         return MXQ_ERR_INVALID_ARG;
     const int64_t need = route_bytes(tokens, num_experts);
     if (workspace_bytes < need || (need > 0 && !workspace))
@@ -233,7 +248,7 @@ mxq_status mxq_moe_route(const void *logits, int32_t dtype, int64_t tokens, int3
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     return (dtype == MXQ_BF16 ? run_route<uint16_t> : run_route<float>)(
         logits, sl_t, (int)tokens, num_experts, token_mask, top_k, renormalize, align, ids, weights, rows, lse,
-        counts, offs, mean_prob, losses, live, workspace, st);
+        RouteResults{counts, offs, mean_prob, losses, live}, workspace, st);
 }
 
 mxq_status mxq_moe_route_backward(const void *logits, int32_t dtype, int64_t tokens, int32_t num_experts,

@@ -14,18 +14,29 @@
 //   P_e = 1/n sum_t p_te     balance = E sum_e c_e/(n k) P_e
 //   z = 1/n sum_t lse_t^2
 //
-// Two kernels.  The first gives each workgroup a run of tokens (at most
-// kRouteMaxBlocks runs): L lanes hold a token's logits, V consecutive ones
-// per lane, so the whole row stays in registers and every reduction is a few
-// cross-lane steps.  64 tokens at a time set their bits in one 64-bit mask
-// per expert in LDS; a slot's rank among the run's slots of its expert is
-// then a population count, whatever order the lanes ran in, and no atomic
-// result depends on an order.  The second kernel turns the runs' counts into
-// ranks over all tokens and into the per-expert results.
+// Three kernels.  The first gives each workgroup a run of tokens (at most
+// kRouteMaxBlocks runs): L lanes hold a token's logits, V consecutive ones per
+// lane, so the whole row stays in registers.  64 tokens at a time set their
+// bits in one 64-bit mask per expert in LDS; a slot's rank among the run's
+// slots of its expert is then a population count, whatever order the lanes ran
+// in, and no atomic result depends on an order.  The second kernel scans the
+// runs' counts and adds up their probabilities, the third adds the group
+// starts to the ranks.  A single run (serving) does all of it in the first.
+//
+// The selection is bound by vector instructions, so it works on one unique
+// key per logit: its order-preserving bits above the complement of its index.
+// Equal logits then compare by index, and a key names its logit and expert: a
+// bf16 logit's key has 32 bits, an fp32 logit's is the bit pattern of a
+// positive double (numerical order = order of the bits), and minima and maxima
+// need no comparison flags.  Each lane sorts its V keys once in a network;
+// every slot takes the largest head over the token's lanes and moves the
+// winner's list up.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "moe_rows_kernels.hpp"
 #include "mxq_device.hpp"
@@ -36,42 +47,128 @@ namespace mxq {
 constexpr int kRouteTile = 64;        // tokens that share one round of bit masks
 constexpr int kRouteMaxBlocks = 256;  // runs of tokens (workgroups of the first kernel)
 constexpr int kNoExpert = 0xffff;
-constexpr int kRankThreads = 1024;    // workgroups of the second kernel
+constexpr int kScanThreads = 1024;    // workgroups of the second kernel: 32 experts x 32 parts of the runs
+constexpr int kScanExperts = 32;
+constexpr int kPlaceThreads = 256;    // workgroups of the third kernel
 
-// fp32 -> uint32 whose unsigned order is the float order (-0 equals +0: adding
-// zero makes it +0); NaN and -inf -> 0
-__device__ __forceinline__ uint32_t route_key(float v)
+// order-preserving bits of fp32 (-0 equals +0: adding zero makes it +0)
+__device__ __forceinline__ uint32_t ordered_bits(float v)
 {
     const uint32_t b = __float_as_uint(v + 0.0f);
-    return v > -INFINITY ? b ^ (b >> 31 ? 0xffffffffu : 0x80000000u) : 0u;
+    return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t b)
+{
+    return __uint_as_float(b ^ (b >> 31 ? 0x80000000u : 0xffffffffu));
+}
+
+// Unique keys of the logits of type T (-inf and NaN: 0, the least key).
+template <typename T>
+struct RouteKey;
+template <>
+struct RouteKey<uint16_t> {
+    typedef uint32_t K;
+    static __device__ __forceinline__ K make(float v, int e)
+    {
+        return v > -INFINITY ? (ordered_bits(v) & 0xffff0000u) | (uint32_t)(0xffff - e) : 0u;
+    }
+    static __device__ __forceinline__ K big(K a, K b) { return a > b ? a : b; }
+    static __device__ __forceinline__ K small(K a, K b) { return a < b ? a : b; }
+    static __device__ __forceinline__ int expert(K k) { return 0xffff - (int)(k & 0xffffu); }
+    // the low half of a negative value's order-preserving bits was ones
+    static __device__ __forceinline__ float logit(K k)
+    {
+        return from_ordered(k >> 31 ? k & 0xffff0000u : k | 0xffffu);
+    }
+    template <int CTRL>
+    static __device__ __forceinline__ K move(K k) { return dpp<CTRL>(k); }
+    static __device__ __forceinline__ K xor_lane(K k, int m) { return (K)__shfl_xor((int)k, m, 64); }
+};
+template <>
+struct RouteKey<float> {
+    typedef double K;
+    // bits 61..30: the logit's, 29..18: the index's (below 4096); the top two
+    // bits are 0, so every key is a positive finite double
+    static __device__ __forceinline__ K make(float v, int e)
+    {
+        const uint64_t b = (uint64_t)ordered_bits(v) << 30 | (uint64_t)(uint32_t)(4095 - e) << 18;
+        return __longlong_as_double(v > -INFINITY ? (long long)b : 0);
+    }
+    static __device__ __forceinline__ K big(K a, K b) { return __builtin_fmax(a, b); }
+    static __device__ __forceinline__ K small(K a, K b) { return __builtin_fmin(a, b); }
+    static __device__ __forceinline__ int expert(K k)
+    {
+        return 4095 - (int)((uint64_t)__double_as_longlong(k) >> 18 & 4095u);
+    }
+    static __device__ __forceinline__ float logit(K k)
+    {
+        return from_ordered((uint32_t)((uint64_t)__double_as_longlong(k) >> 30));
+    }
+    template <int CTRL>
+    static __device__ __forceinline__ K move(K k)
+    {
+        const uint64_t b = (uint64_t)__double_as_longlong(k);
+        return __longlong_as_double((long long)((uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32 | dpp<CTRL>((uint32_t)b)));
+    }
+    static __device__ __forceinline__ K xor_lane(K k, int m) { return __shfl_xor(k, m, 64); }
+};
+
+// reductions over aligned groups of L lanes; every lane gets the result
+template <int L, typename F, typename M, typename X>
+__device__ __forceinline__ F lanes_reduce(F v, M &&op, X &&xor_lane)
+{
+    if constexpr (L >= 2) v = op(v, std::integral_constant<int, kDppQuadXor1>());
+    if constexpr (L >= 4) v = op(v, std::integral_constant<int, kDppQuadXor2>());
+    if constexpr (L >= 8) v = op(v, std::integral_constant<int, kDppHalfMirror>());
+    if constexpr (L >= 16) v = op(v, std::integral_constant<int, kDppRowMirror>());
+    if constexpr (L >= 32) v = xor_lane(v, 16);
+    if constexpr (L >= 64) v = xor_lane(v, 32);
+    return v;
 }
 
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v)
 {
-#pragma unroll
-    for (int m = 1; m < L; m <<= 1)
-        v += __shfl_xor(v, m, 64);
-    return v;
+    return lanes_reduce<L>(
+        v, [](float x, auto c) { return x + __uint_as_float(dpp<c()>(__float_as_uint(x))); },
+        [](float x, int m) { return x + __shfl_xor(x, m, 64); });
 }
 
 template <int L>
 __device__ __forceinline__ float lanes_max(float v)
 {
-#pragma unroll
-    for (int m = 1; m < L; m <<= 1)
-        v = fmaxf(v, __shfl_xor(v, m, 64));
-    return v;
+    return lanes_reduce<L>(
+        v, [](float x, auto c) { return fmaxf(x, __uint_as_float(dpp<c()>(__float_as_uint(x)))); },
+        [](float x, int m) { return fmaxf(x, __shfl_xor(x, m, 64)); });
 }
 
-template <int L>
-__device__ __forceinline__ uint32_t lanes_umax(uint32_t v)
+template <int L, typename T>
+__device__ __forceinline__ typename RouteKey<T>::K lanes_best(typename RouteKey<T>::K v)
 {
-    v = group_max<(L < 16 ? L : 16)>(v);
+    typedef RouteKey<T> R;
+    return lanes_reduce<L>(
+        v, [](typename R::K x, auto c) { return R::big(x, R::template move<c()>(x)); },
+        [](typename R::K x, int m) { return R::big(x, R::xor_lane(x, m)); });
+}
+
+// Batcher's odd-even merge sort of N keys (a power of two), largest first
+template <typename T, int N>
+__device__ __forceinline__ void sort_keys(typename RouteKey<T>::K (&k)[N])
+{
+    typedef RouteKey<T> R;
 #pragma unroll
-    for (int m = 16; m < L; m <<= 1)
-        v = umax(v, (uint32_t)__shfl_xor((int)v, m, 64));
-    return v;
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const typename R::K a = k[i + j], b = k[i + j + q];
+                        k[i + j] = R::big(a, b);
+                        k[i + j + q] = R::small(a, b);
+                    }
 }
 
 // V consecutive elements of a row from element e0 on; those at or past
@@ -99,33 +196,87 @@ __device__ __forceinline__ void load_row(const T *row, int e0, int width, bool w
         v[i] = e0 + i < width ? Piece<T>::to_f32(row[e0 + i]) : fill;
 }
 
-// Workspace of a call: per run, the counts and probability sums of every
-// expert and the run's sum of lse^2 and number of live tokens.
+// Workspace of a call.  Per run, the counts of every expert (after the second
+// kernel: those of the runs before), their probability sums, the sum of lse^2
+// and the number of live tokens; per expert its share of the balance loss.
 struct RouteWorkspace {
     int32_t *counts;  // [runs][experts]
     float *probs;     // [runs][experts]
     float *z;         // [runs]
     int32_t *live;    // [runs]
+    double *balance;  // [experts]
 };
 
-// One run of tokens per workgroup.  L lanes per token, V experts per lane.
-template <typename T, int L, int V, int THREADS>
+struct RouteResults {
+    int32_t *counts, *offs;
+    float *mean_prob, *losses;
+    int32_t *live;
+};
+
+// Group ends and starts from the counts: wave 0 scans 64 experts at a time.
+__device__ __forceinline__ void group_ends(const int32_t *count, int32_t *start, int32_t *offs, int experts, int align)
+{
+    const int lane = threadIdx.x;
+    int base = 0;
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+        const int e = e0 + lane;
+        const int padded = e < experts ? (count[e] + align - 1) / align * align : 0;
+        int sum = padded;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int up = __shfl_up(sum, m, 64);
+            sum += lane >= m ? up : 0;
+        }
+        if (e < experts) {
+            if (offs)
+                offs[e] = base + sum;
+            start[e] = base + sum - padded;
+        }
+        base += __shfl(sum, 63, 64);
+    }
+}
+
+// sum over the workgroup's N threads in a fixed order; part: N / 64 entries
+template <int N>
+__device__ __forceinline__ double block_sum(double *part, double v)
+{
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1)
+        v += __shfl_xor(v, m, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int w = 0; w < N / 64; ++w)
+        s += part[w];
+    return s;
+}
+
+// One run of tokens per workgroup.  L lanes per token, V experts per lane, at
+// most D slots of a token (D = V: any number).  ONE: the only run.
+template <typename T, int L, int V, int D, int THREADS, bool ONE>
 __global__ __launch_bounds__(THREADS) void moe_route_kernel(
     const T *__restrict__ logits, int64_t sl, int tokens, int experts, const uint8_t *__restrict__ mask, int k,
-    int renorm, int run, int32_t *__restrict__ ids, float *__restrict__ weights, int32_t *__restrict__ rows,
-    float *__restrict__ lse_out, RouteWorkspace ws)
+    int renorm, int align, int run, int32_t *__restrict__ ids, float *__restrict__ weights,
+    int32_t *__restrict__ rows, float *__restrict__ lse_out, RouteWorkspace ws, RouteResults out)
 {
+    typedef RouteKey<T> R;
+    typedef typename R::K K;
     constexpr int G = THREADS / L;  // tokens in flight
     constexpr int WAVES = THREADS / 64;
     // per expert the 64-token mask and the run's count so far; per slot of the
-    // round its probability and expert, per token 1 / (sum of its slots)
+    // round its logit and expert, per token log-sum-exp and the factor of its
+    // weights
     extern __shared__ uint64_t lds[];
     uint64_t *bits = lds;
     int32_t *count = reinterpret_cast<int32_t *>(bits + experts);
-    float *norm = reinterpret_cast<float *>(count + experts);
-    float *slot_p = norm + kRouteTile;
-    uint16_t *slot_e = reinterpret_cast<uint16_t *>(slot_p + kRouteTile * k);
-    const int tid = threadIdx.x, sub = tid % L, grp = tid / L;
+    float *slse = reinterpret_cast<float *>(count + experts);
+    float *norm = slse + kRouteTile;
+    float *slot_l = norm + kRouteTile;
+    uint16_t *slot_e = reinterpret_cast<uint16_t *>(slot_l + kRouteTile * k);
+    const int tid = threadIdx.x, sub = tid % L, wave = tid >> 6, lane = tid & 63;
     const int e0 = sub * V;
     const bool whole = experts % V == 0;
     for (int e = tid; e < experts; e += THREADS) {
@@ -139,21 +290,19 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
         acc[i] = 0.0f;
     __syncthreads();
     const int first = blockIdx.x * run, last = min(first + run, tokens);
-    for (int t0 = first; t0 < last; t0 += kRouteTile) {
-        for (int s = grp; s < kRouteTile; s += G) {
-            const int t = t0 + s;
+    for (int t0 = first; ONE ? t0 == first : t0 < last; t0 += kRouteTile) {
+        // s0: the wave's first token, so that the wave leaves together
+        for (int s0 = wave * (64 / L); s0 < kRouteTile && t0 + s0 < last; s0 += G) {
+            const int s = s0 + lane / L, t = t0 + s;
             const bool in = t < last;
-            float v[V];
             const int tl = in ? t : first;
+            float v[V];
             load_row<T, V>(logits + (int64_t)tl * sl, e0, experts, whole, -INFINITY, v);
             bool live = in && (!mask || mask[tl] != 0);
             float top = v[0];
-            bool bad = false;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = 1; i < V; ++i)
                 top = fmaxf(top, v[i]);
-                bad |= v[i] != v[i];
-            }
             top = lanes_max<L>(top);
             // fmax drops NaN: a row of -inf and NaN alone has no logit either
             live = live && top > -INFINITY;
@@ -169,55 +318,66 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
             if (live) {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    acc[i] += p[i] * inv;
+                    acc[i] = fmaf(p[i], inv, acc[i]);
                 if (sub == 0) {
                     zsum = fmaf(lse, lse, zsum);
                     ++nlive;
                 }
             }
-            if (in && sub == 0)
-                lse_out[t] = lse;
-            // the k largest: a lane offers its best, the largest offer wins,
-            // the lowest lane among equals (its experts come first)
-            uint32_t key[V];
+            K key[V];
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                key[i] = live ? route_key(v[i]) : 0u;
+                key[i] = live ? R::make(v[i], e0 + i) : (K)0;
+            if constexpr (V <= 16)
+                sort_keys<T, V>(key);
             float total = 0.0f;
             for (int j = 0; j < k; ++j) {
-                uint32_t best = 0;
-                int at = 0;
+                K best = key[0];
+                if constexpr (V > 16) {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (key[i] > best) {
-                        best = key[i];
-                        at = i;
-                    }
-                const uint32_t win = lanes_umax<L>(best);
-                const uint64_t same = __ballot(best == win) >> ((tid & 63) / L * L);
-                const bool owner = sub == __builtin_ctzll(same);
-                if (owner) {
-                    float pw = 0.0f;
+                    for (int i = 1; i < V; ++i)
+                        best = R::big(best, key[i]);
+                }
+                const K win = lanes_best<L, T>(best);
+                if constexpr (V > 16) {
 #pragma unroll
                     for (int i = 0; i < V; ++i)
-                        if (i == at) {
-                            pw = p[i] * inv;
-                            key[i] = 0;
-                        }
-                    const bool taken = win != 0;
-                    slot_p[s * k + j] = taken ? pw : 0.0f;
-                    slot_e[s * k + j] = taken ? (uint16_t)(e0 + at) : kNoExpert;
-                    if (taken) {
-                        atomicOr(reinterpret_cast<unsigned long long *>(bits + e0 + at), 1ull << s);
-                        total += pw;
-                    }
+                        key[i] = key[i] == win ? (K)0 : key[i];
+                } else {
+                    const bool mine = key[0] == win;
+#pragma unroll
+                    for (int i = 0; i < D; ++i)
+                        key[i] = mine ? (i + 1 < V ? key[i + 1 < V ? i + 1 : i] : (K)0) : key[i];
+                }
+                const bool taken = win != (K)0;
+                const float l = taken ? R::logit(win) : -INFINITY;
+                total += __expf(l - top) * inv;
+                if (sub == 0) {
+                    slot_l[s * k + j] = l;
+                    slot_e[s * k + j] = taken ? (uint16_t)R::expert(win) : kNoExpert;
+                    if (taken)
+                        atomicOr(reinterpret_cast<unsigned long long *>(bits + R::expert(win)), 1ull << s);
                 }
             }
-            total = lanes_sum<L>(total);
-            if (sub == 0)
-                norm[s] = renorm && total > 0.0f ? 1.0f / total : 1.0f;
+            if (sub == 0) {
+                slse[s] = lse;
+                norm[s] = renorm && live ? 1.0f / total : 1.0f;
+                if (in)
+                    lse_out[t] = lse;
+            }
         }
         __syncthreads();
+        if constexpr (ONE) {
+            for (int e = tid; e < experts; e += THREADS) {
+                const int c = __popcll(bits[e]);
+                count[e] = c;
+                out.counts[e] = c;
+            }
+            __syncthreads();
+            if (tid < 64)
+                group_ends(count, count, out.offs, experts, align);
+            __syncthreads();
+        }
         // rank of each slot among the run's slots of its expert
         const int n = min(kRouteTile, last - t0) * k;
         for (int i = tid; i < n; i += THREADS) {
@@ -226,31 +386,34 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
             const int e = slot_e[i];
             const bool taken = e != kNoExpert;
             ids[at] = taken ? e : -1;
-            weights[at] = slot_p[i] * norm[s];
+            weights[at] = taken ? __expf(slot_l[i] - slse[s]) * norm[s] : 0.0f;
             rows[at] = taken ? count[e] + __popcll(bits[e] & ((1ull << s) - 1)) : -1;
         }
         __syncthreads();
-        for (int e = tid; e < experts; e += THREADS) {
-            count[e] += __popcll(bits[e]);
-            bits[e] = 0;
+        if constexpr (!ONE) {
+            for (int e = tid; e < experts; e += THREADS) {
+                count[e] += __popcll(bits[e]);
+                bits[e] = 0;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
-    // the run's sums, wave after wave so that their order is fixed
-    float *psum = reinterpret_cast<float *>(bits);
-    const int wave = tid >> 6, lane = tid & 63;
+    // the run's sums: lanes that hold the same experts, then wave after wave,
+    // so that their order is fixed
+    float *psum = ONE ? reinterpret_cast<float *>(count) : reinterpret_cast<float *>(bits);
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int m = L; m < 64; m <<= 1)
             acc[i] += __shfl_xor(acc[i], m, 64);
     zsum = lanes_sum<64>(zsum);
-    nlive = (int)lanes_sum<64>((float)nlive);
+    const float fl = lanes_sum<64>((float)nlive);
     if (lane == 0) {
-        norm[wave] = zsum;
-        norm[WAVES + wave] = (float)nlive;
+        slse[wave] = zsum;
+        norm[wave] = fl;
     }
-    for (int w = 0; w < WAVES; ++w) {
+    const int waves = min(WAVES, (min(last - first, kRouteTile) + 64 / L - 1) / (64 / L));  // that had a token
+    for (int w = 0; w < max(waves, 1); ++w) {
         if (wave == w && lane < L)
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -258,136 +421,133 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
                     psum[e0 + i] = (w ? psum[e0 + i] : 0.0f) + acc[i];
         __syncthreads();
     }
-    for (int e = tid; e < experts; e += THREADS) {
-        ws.counts[(int64_t)blockIdx.x * experts + e] = count[e];
-        ws.probs[(int64_t)blockIdx.x * experts + e] = psum[e];
+    float z = 0.0f, nl = 0.0f;
+    for (int w = 0; w < WAVES; ++w) {
+        z += slse[w];
+        nl += norm[w];
     }
-    if (tid == 0) {
-        float z = 0.0f, n = 0.0f;
-        for (int w = 0; w < WAVES; ++w) {
-            z += norm[w];
-            n += norm[WAVES + w];
+    if constexpr (!ONE) {
+        for (int e = tid; e < experts; e += THREADS) {
+            ws.counts[(int64_t)blockIdx.x * experts + e] = count[e];
+            ws.probs[(int64_t)blockIdx.x * experts + e] = psum[e];
         }
-        ws.z[blockIdx.x] = z;
-        ws.live[blockIdx.x] = (int)n;
+        if (tid == 0) {
+            ws.z[blockIdx.x] = z;
+            ws.live[blockIdx.x] = (int)nl;
+        }
+    } else {
+        const double inv = nl > 0.0f ? 1.0 / (double)nl : 0.0;
+        double b = 0.0;
+        for (int e = tid; e < experts; e += THREADS) {
+            const double p = (double)psum[e] * inv;
+            out.mean_prob[e] = (float)p;
+            b += (double)__popcll(bits[e]) * p;
+        }
+        __shared__ double part[WAVES];
+        b = block_sum<THREADS>(part, b);
+        if (tid == 0) {
+            out.losses[0] = (float)(b * (double)experts * inv / (double)k);
+            out.losses[1] = (float)((double)z * inv);
+            out.live[0] = (int)nl;
+        }
     }
 }
 
-// sum over the workgroup's kRankThreads values in a fixed order
-__device__ __forceinline__ double tree_sum(double *part, double v)
+// 32 experts per workgroup, 32 threads each, every thread a contiguous part of
+// the runs: counts of the runs before each run (in place), totals, mean
+// probabilities (64-bit sums in a fixed order).
+__global__ __launch_bounds__(kScanThreads) void moe_scan_kernel(int experts, int nruns, RouteWorkspace ws,
+                                                                RouteResults out)
 {
-    const int tid = threadIdx.x;
-    part[tid] = v;
+    constexpr int PARTS = kScanThreads / kScanExperts, MOST = kRouteMaxBlocks / PARTS;
+    __shared__ int32_t psum[PARTS][kScanExperts];
+    __shared__ double qsum[PARTS][kScanExperts];
+    __shared__ int32_t alive;
+    const int tid = threadIdx.x, part = tid / kScanExperts, x = tid % kScanExperts;
+    const int e = blockIdx.x * kScanExperts + x;
+    const int per = (nruns + PARTS - 1) / PARTS, r0 = min(part * per, nruns), r1 = min(r0 + per, nruns);
+    if (tid == 0)
+        alive = 0;
     __syncthreads();
-    for (int m = kRankThreads / 2; m > 0; m >>= 1) {
-        if (tid < m)
-            part[tid] += part[tid + m];
-        __syncthreads();
+    if (tid < nruns)
+        atomicAdd(&alive, ws.live[tid]);
+    int c[MOST], sum = 0;
+    double p = 0.0;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+        const bool on = r0 + i < r1 && e < experts;
+        const int64_t at = (int64_t)(r0 + i) * experts + e;
+        c[i] = on ? ws.counts[at] : 0;
+        p += on ? (double)ws.probs[at] : 0.0;
     }
-    const double s = part[0];
+#pragma unroll
+    for (int i = 0; i < MOST; ++i)
+        sum += c[i];
+    psum[part][x] = sum;
+    qsum[part][x] = p;
     __syncthreads();
-    return s;
+    int before = 0;
+    for (int q = 0; q < part; ++q)
+        before += psum[q][x];
+#pragma unroll
+    for (int i = 0; i < MOST; ++i)
+        if (r0 + i < r1 && e < experts) {
+            ws.counts[(int64_t)(r0 + i) * experts + e] = before;
+            before += c[i];
+        }
+    if (part == PARTS - 1 && e < experts) {
+        double q = 0.0;
+        for (int i = 0; i < PARTS; ++i)
+            q += qsum[i][x];
+        const double inv = alive > 0 ? 1.0 / (double)alive : 0.0;
+        out.counts[e] = before;
+        out.mean_prob[e] = (float)(q * inv);
+        ws.balance[e] = (double)before * (q * inv);
+    }
 }
 
-// Ranks over all tokens.  Workgroup b < gridDim.x - 1 takes the slots of
-// `group` runs; the last one writes the per-expert results.  Every workgroup
-// adds up the runs' counts itself (they are small and in cache), each expert
-// by several threads, then lays the groups out.
-__global__ __launch_bounds__(kRankThreads) void moe_rank_kernel(
-    int tokens, int experts, int k, int align, int run, int nruns, int group, const int32_t *__restrict__ ids,
-    int32_t *__restrict__ rows, int32_t *__restrict__ counts, int32_t *__restrict__ offs,
-    float *__restrict__ mean_prob, float *__restrict__ losses, int32_t *__restrict__ live, RouteWorkspace ws)
+// A run per workgroup: its slots' ranks become rows.  The last workgroup
+// writes the group ends and the losses.
+__global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(int tokens, int experts, int k, int align, int run,
+                                                                  int nruns, const int32_t *__restrict__ ids,
+                                                                  int32_t *__restrict__ rows, RouteWorkspace ws,
+                                                                  RouteResults out)
 {
     extern __shared__ uint64_t lds[];
-    int32_t *total = reinterpret_cast<int32_t *>(lds);    // [experts] counts, then group starts
-    int32_t *before = total + experts;                     // [experts] in the runs before this workgroup's
-    const int tid = threadIdx.x;
-    const bool final = blockIdx.x == gridDim.x - 1;
-    const int run0 = blockIdx.x * group, run1 = min(run0 + group, nruns);
-    for (int e = tid; e < 2 * experts; e += kRankThreads)
-        total[e] = 0;
+    int32_t *start = reinterpret_cast<int32_t *>(lds);  // [experts]
+    const int tid = threadIdx.x, r = blockIdx.x;
+    const bool final = r == nruns;
+    for (int e = tid; e < experts; e += kPlaceThreads)
+        start[e] = out.counts[e];
     __syncthreads();
-    // integer sums: their order does not matter
-    const int parts = max(1, kRankThreads / experts);
-    for (int i = tid; i < parts * experts; i += kRankThreads) {
-        const int e = i % experts, part = i / experts;
-        int all = 0, prior = 0;
-#pragma unroll 8
-        for (int r = part; r < nruns; r += parts) {
-            const int c = ws.counts[(int64_t)r * experts + e];
-            all += c;
-            prior += r < run0 ? c : 0;
-        }
-        atomicAdd(&total[e], all);
-        if (!final)
-            atomicAdd(&before[e], prior);
-    }
+    if (tid < 64)
+        group_ends(start, start, final ? out.offs : nullptr, experts, align);
     __syncthreads();
     if (final) {
-        // per-expert results, and the losses in 64 bits in a fixed order
-        __shared__ double part[kRankThreads];
-        __shared__ int alive;
-        if (tid == 0)
-            alive = 0;
-        __syncthreads();
-        if (tid < nruns)
-            atomicAdd(&alive, ws.live[tid]);
-        const double z = tree_sum(part, tid < nruns ? (double)ws.z[tid] : 0.0);
-        const int n = alive;
-        const double inv = n > 0 ? 1.0 / (double)n : 0.0;
-        double s = 0.0;
-        for (int e = tid; e < experts; e += kRankThreads) {
-            double p = 0.0;
-#pragma unroll 8
-            for (int r = 0; r < nruns; ++r)
-                p += (double)ws.probs[(int64_t)r * experts + e];
-            p *= inv;
-            mean_prob[e] = (float)p;
-            counts[e] = total[e];
-            s += (double)total[e] * p;
+        __shared__ double part[kPlaceThreads / 64];
+        double z = 0.0, b = 0.0, n = 0.0;
+        for (int i = tid; i < nruns; i += kPlaceThreads) {
+            z += (double)ws.z[i];
+            n += (double)ws.live[i];
         }
-        s = tree_sum(part, s);
+        for (int e = tid; e < experts; e += kPlaceThreads)
+            b += ws.balance[e];
+        z = block_sum<kPlaceThreads>(part, z);
+        n = block_sum<kPlaceThreads>(part, n);
+        b = block_sum<kPlaceThreads>(part, b);
         if (tid == 0) {
-            losses[0] = (float)(s * (double)experts * inv / (double)k);
-            losses[1] = (float)(z * inv);
-            live[0] = n;
+            const double inv = n > 0.0 ? 1.0 / n : 0.0;
+            out.losses[0] = (float)(b * (double)experts * inv / (double)k);
+            out.losses[1] = (float)(z * inv);
+            out.live[0] = (int)n;
         }
-    }
-    // group starts: wave 0 scans 64 experts at a time
-    if (tid < 64) {
-        int base = 0;
-        for (int e0 = 0; e0 < experts; e0 += 64) {
-            const int e = e0 + tid;
-            const int c = e < experts ? total[e] : 0;
-            const int padded = (c + align - 1) / align * align;
-            int sum = padded;
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const int up = __shfl_up(sum, m, 64);
-                sum += tid >= m ? up : 0;
-            }
-            if (e < experts) {
-                if (final)
-                    offs[e] = base + sum;
-                total[e] = base + sum - padded;
-            }
-            base += __shfl(sum, 63, 64);
-        }
-    }
-    __syncthreads();
-    if (final)
         return;
-    for (int r = run0; r < run1; ++r) {
-        const int64_t first = (int64_t)r * run * k, last = min((int64_t)(r + 1) * run, (int64_t)tokens) * k;
-        for (int64_t i = first + tid; i < last; i += kRankThreads) {
-            const int e = ids[i];
-            if (e >= 0)
-                rows[i] += total[e] + before[e];
-        }
-        __syncthreads();
-        for (int e = tid; e < experts; e += kRankThreads)
-            before[e] += ws.counts[(int64_t)r * experts + e];
-        __syncthreads();
+    }
+    const int64_t first = (int64_t)r * run * k, last = min((int64_t)(r + 1) * run, (int64_t)tokens) * k;
+    for (int64_t i = first + tid; i < last; i += kPlaceThreads) {
+        const int e = ids[i];
+        if (e >= 0)
+            rows[i] += start[e] + ws.counts[(int64_t)r * experts + e];
     }
 }
 
