@@ -94,22 +94,20 @@ mxq_status run_route(const void *logits, int64_t sl, int tokens, int experts, co
         ws.z = ws.probs + (int64_t)nruns * experts;
         ws.live = reinterpret_cast<int32_t *>(ws.z + nruns);
     }
-    const size_t lds = (size_t)experts * 12 + (size_t)kRouteTile * (8 + 6 * k);
+    const size_t lds = (size_t)experts * 12 + (size_t)kRouteTile * 6 * k;
     by_experts(experts, [&](auto l, auto v, auto t) {
         constexpr int L = decltype(l)::value, V = decltype(v)::value, THREADS = decltype(t)::value;
-        constexpr int D8 = V < 8 ? V : 8;
         auto go = [&](auto kernel) {
             kernel<<<dim3((unsigned)std::max(nruns, 1)), dim3(THREADS), lds, st>>>(
                 reinterpret_cast<const T *>(logits), sl, tokens, experts, mask, k, renorm, align, run, ids, weights,
                 rows, lse, ws, out);
         };
-        // a token takes at most k keys from one lane: 8 positions of its list move
         if (k <= 8)
-            nruns <= 1 ? go(moe_route_kernel<T, L, V, D8, THREADS, true>)
-                       : go(moe_route_kernel<T, L, V, D8, THREADS, false>);
+            nruns <= 1 ? go(moe_route_kernel<T, L, V, true, THREADS, true>)
+                       : go(moe_route_kernel<T, L, V, true, THREADS, false>);
         else
-            nruns <= 1 ? go(moe_route_kernel<T, L, V, V, THREADS, true>)
-                       : go(moe_route_kernel<T, L, V, V, THREADS, false>);
+            nruns <= 1 ? go(moe_route_kernel<T, L, V, false, THREADS, true>)
+                       : go(moe_route_kernel<T, L, V, false, THREADS, false>);
     });
     if (nruns > 1) {
         moe_scan_kernel<<<dim3((unsigned)((experts + kScanExperts - 1) / kScanExperts)), dim3(kScanThreads), 0, st>>>(
@@ -130,7 +128,7 @@ mxq_status run_route_backward(const void *logits, int64_t sl, int tokens, int ex
         constexpr int L = decltype(l)::value, V = decltype(v)::value;
         const int per = 256 / L;
         const int64_t blocks = std::min<int64_t>(((int64_t)tokens + per - 1) / per, 1 << 20);
-        moe_route_backward_kernel<T, L, V><<<dim3((unsigned)blocks), dim3(256), 0, st>>>(
+        moe_route_backward_kernel<T, L, V><<<dim3((unsigned)blocks), dim3(256), (size_t)256 * V * 4, st>>>(
             reinterpret_cast<const T *>(logits), sl, tokens, experts, k, renorm, ids, weights, lse, counts, live,
             gw, gl, reinterpret_cast<T *>(dl), sd);
     });

@@ -47,6 +47,7 @@ namespace mxq {
 constexpr int kRouteTile = 64;        // tokens that share one round of bit masks
 constexpr int kRouteMaxBlocks = 256;  // runs of tokens (workgroups of the first kernel)
 constexpr int kNoExpert = 0xffff;
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr int kScanThreads = 1024;    // workgroups of the second kernel: 32 experts x 32 parts of the runs
 constexpr int kScanExperts = 32;
 constexpr int kPlaceThreads = 256;    // workgroups of the third kernel
@@ -55,22 +56,23 @@ constexpr int kPlaceThreads = 256;    // workgroups of the third kernel
 __device__ __forceinline__ uint32_t ordered_bits(float v)
 {
     const uint32_t b = __float_as_uint(v + 0.0f);
-    return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float from_ordered(uint32_t b)
 {
     return __uint_as_float(b ^ (b >> 31 ? 0x80000000u : 0xffffffffu));
 }
 
-// Unique keys of the logits of type T (-inf and NaN: 0, the least key).
+// Unique keys of the logits of type T, NaN as -inf.  Keys below kFirst are -inf's.
 template <typename T>
 struct RouteKey;
 template <>
 struct RouteKey<uint16_t> {
     typedef uint32_t K;
+    static constexpr K kFirst = 0x00800000u;  // -inf: 0x007f....
     static __device__ __forceinline__ K make(float v, int e)
     {
-        return v > -INFINITY ? (ordered_bits(v) & 0xffff0000u) | (uint32_t)(0xffff - e) : 0u;
+        return (ordered_bits(fmaxf(v, -INFINITY)) & 0xffff0000u) | (uint32_t)(0xffff - e);
     }
     static __device__ __forceinline__ K big(K a, K b) { return a > b ? a : b; }
     static __device__ __forceinline__ K small(K a, K b) { return a < b ? a : b; }
@@ -89,10 +91,12 @@ struct RouteKey<float> {
     typedef double K;
     // bits 61..30: the logit's, 29..18: the index's (below 4096); the top two
     // bits are 0, so every key is a positive finite double
+    static constexpr K kFirst = 0x1p-1021;    // bits of 0x00800000 << 30 (-inf: 0x007fffff << 30)
     static __device__ __forceinline__ K make(float v, int e)
     {
-        const uint64_t b = (uint64_t)ordered_bits(v) << 30 | (uint64_t)(uint32_t)(4095 - e) << 18;
-        return __longlong_as_double(v > -INFINITY ? (long long)b : 0);
+        const uint64_t b =
+            (uint64_t)ordered_bits(fmaxf(v, -INFINITY)) << 30 | (uint64_t)(uint32_t)(4095 - e) << 18;
+        return __longlong_as_double((long long)b);
     }
     static __device__ __forceinline__ K big(K a, K b) { return __builtin_fmax(a, b); }
     static __device__ __forceinline__ K small(K a, K b) { return __builtin_fmin(a, b); }
@@ -213,26 +217,28 @@ struct RouteResults {
     int32_t *live;
 };
 
-// Group ends and starts from the counts: wave 0 scans 64 experts at a time.
+// Group ends and starts from the counts (start may be count), by one wave:
+// consecutive experts per lane, one scan of the lanes' sums.
 __device__ __forceinline__ void group_ends(const int32_t *count, int32_t *start, int32_t *offs, int experts, int align)
 {
-    const int lane = threadIdx.x;
-    int base = 0;
-    for (int e0 = 0; e0 < experts; e0 += 64) {
-        const int e = e0 + lane;
-        const int padded = e < experts ? (count[e] + align - 1) / align * align : 0;
-        int sum = padded;
+    const int lane = threadIdx.x & 63, per = (experts + 63) / 64;
+    const int e0 = min(lane * per, experts), e1 = min(e0 + per, experts);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e)
+        sum += (count[e] + align - 1) / align * align;
+    int upto = sum;
 #pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const int up = __shfl_up(sum, m, 64);
-            sum += lane >= m ? up : 0;
-        }
-        if (e < experts) {
-            if (offs)
-                offs[e] = base + sum;
-            start[e] = base + sum - padded;
-        }
-        base += __shfl(sum, 63, 64);
+    for (int m = 1; m < 64; m <<= 1) {
+        const int up = __shfl_up(upto, m, 64);
+        upto += lane >= m ? up : 0;
+    }
+    int at = upto - sum;
+    for (int e = e0; e < e1; ++e) {
+        const int next = at + (count[e] + align - 1) / align * align;
+        start[e] = at;
+        if (offs)
+            offs[e] = next;
+        at = next;
     }
 }
 
@@ -254,9 +260,10 @@ __device__ __forceinline__ double block_sum(double *part, double v)
     return s;
 }
 
-// One run of tokens per workgroup.  L lanes per token, V experts per lane, at
-// most D slots of a token (D = V: any number).  ONE: the only run.
-template <typename T, int L, int V, int D, int THREADS, bool ONE>
+// One run of tokens per workgroup.  L lanes per token, V experts per lane.
+// FEW: at most 8 slots, so only the first 8 of a lane's sorted keys can be
+// taken.  ONE: the only run.
+template <typename T, int L, int V, bool FEW, int THREADS, bool ONE>
 __global__ __launch_bounds__(THREADS) void moe_route_kernel(
     const T *__restrict__ logits, int64_t sl, int tokens, int experts, const uint8_t *__restrict__ mask, int k,
     int renorm, int align, int run, int32_t *__restrict__ ids, float *__restrict__ weights,
@@ -266,16 +273,16 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
     typedef typename R::K K;
     constexpr int G = THREADS / L;  // tokens in flight
     constexpr int WAVES = THREADS / 64;
+    // slots a lane keeps: slot j stays with lane j % L of its token
+    constexpr int KEEP = FEW || L >= 32 ? 1 : 32 / L, D = FEW && V > 8 ? 8 : V;
     // per expert the 64-token mask and the run's count so far; per slot of the
-    // round its logit and expert, per token log-sum-exp and the factor of its
-    // weights
+    // round its weight and expert
     extern __shared__ uint64_t lds[];
     uint64_t *bits = lds;
     int32_t *count = reinterpret_cast<int32_t *>(bits + experts);
-    float *slse = reinterpret_cast<float *>(count + experts);
-    float *norm = slse + kRouteTile;
-    float *slot_l = norm + kRouteTile;
-    uint16_t *slot_e = reinterpret_cast<uint16_t *>(slot_l + kRouteTile * k);
+    float *slot_w = reinterpret_cast<float *>(count + experts);
+    uint16_t *slot_e = reinterpret_cast<uint16_t *>(slot_w + kRouteTile * k);
+    __shared__ float zpart[WAVES], npart[WAVES];
     const int tid = threadIdx.x, sub = tid % L, wave = tid >> 6, lane = tid & 63;
     const int e0 = sub * V;
     const bool whole = experts % V == 0;
@@ -306,15 +313,18 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
             top = lanes_max<L>(top);
             // fmax drops NaN: a row of -inf and NaN alone has no logit either
             live = live && top > -INFINITY;
+            // exp(v - top) as 2^(v log2 e - top log2 e), one rounding of the
+            // difference; the rounding of top log2 e is common to the row
+            const float ltop = top * kLog2E;
             float p[V], sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                p[i] = __expf(v[i] - top);
+                p[i] = __builtin_amdgcn_exp2f(fmaf(v[i], kLog2E, -ltop));
                 sum += p[i];
             }
             sum = lanes_sum<L>(sum);
             const float lse = live ? logf(sum) + top : INFINITY;
-            const float inv = 1.0f / sum;
+            const float inv = live ? 1.0f / sum : 0.0f;
             if (live) {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
@@ -324,46 +334,59 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
                     ++nlive;
                 }
             }
+            if (sub == 0 && in)
+                lse_out[t] = lse;
             K key[V];
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                key[i] = live ? R::make(v[i], e0 + i) : (K)0;
+                key[i] = R::make(v[i], e0 + i);
             if constexpr (V <= 16)
                 sort_keys<T, V>(key);
-            float total = 0.0f;
-            for (int j = 0; j < k; ++j) {
-                K best = key[0];
-                if constexpr (V > 16) {
+            K kept[KEEP];
 #pragma unroll
-                    for (int i = 1; i < V; ++i)
-                        best = R::big(best, key[i]);
-                }
-                const K win = lanes_best<L, T>(best);
-                if constexpr (V > 16) {
+            for (int q = 0; q < KEEP; ++q)
+                kept[q] = (K)0;
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        key[i] = key[i] == win ? (K)0 : key[i];
-                } else {
-                    const bool mine = key[0] == win;
+            for (int q = 0; q < KEEP; ++q)
+                for (int j = q * L; j < min(k, (q + 1) * L); ++j) {
+                    K best = key[0];
+                    if constexpr (V > 16) {
 #pragma unroll
-                    for (int i = 0; i < D; ++i)
-                        key[i] = mine ? (i + 1 < V ? key[i + 1 < V ? i + 1 : i] : (K)0) : key[i];
+                        for (int i = 1; i < V; ++i)
+                            best = R::big(best, key[i]);
+                    }
+                    const K win = lanes_best<L, T>(best);
+                    if constexpr (V > 16) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            key[i] = key[i] == win ? (K)0 : key[i];
+                    } else {
+                        const bool mine = key[0] == win;
+#pragma unroll
+                        for (int i = 0; i < D; ++i)
+                            key[i] = mine ? (i + 1 < V ? key[i + 1 < V ? i + 1 : i] : (K)0) : key[i];
+                    }
+                    kept[q] = sub + q * L == j ? win : kept[q];
                 }
-                const bool taken = win != (K)0;
-                const float l = taken ? R::logit(win) : -INFINITY;
-                total += __expf(l - top) * inv;
-                if (sub == 0) {
-                    slot_l[s * k + j] = l;
-                    slot_e[s * k + j] = taken ? (uint16_t)R::expert(win) : kNoExpert;
-                    if (taken)
-                        atomicOr(reinterpret_cast<unsigned long long *>(bits + R::expert(win)), 1ull << s);
-                }
+            float w[KEEP], total = 0.0f;
+#pragma unroll
+            for (int q = 0; q < KEEP; ++q) {
+                const bool taken = live && kept[q] >= R::kFirst;
+                w[q] = taken ? __builtin_amdgcn_exp2f(fmaf(R::logit(kept[q]), kLog2E, -ltop)) * inv : 0.0f;
+                total += w[q];
             }
-            if (sub == 0) {
-                slse[s] = lse;
-                norm[s] = renorm && live ? 1.0f / total : 1.0f;
-                if (in)
-                    lse_out[t] = lse;
+            const float norm = renorm ? 1.0f / lanes_sum<L>(total) : 1.0f;
+#pragma unroll
+            for (int q = 0; q < KEEP; ++q) {
+                const int j = sub + q * L;
+                if (j < k) {
+                    const bool taken = live && kept[q] >= R::kFirst;
+                    const int e = R::expert(kept[q]);
+                    slot_w[s * k + j] = taken ? w[q] * norm : 0.0f;
+                    slot_e[s * k + j] = taken ? (uint16_t)e : (uint16_t)kNoExpert;
+                    if (taken)
+                        atomicOr(reinterpret_cast<unsigned long long *>(bits + e), 1ull << s);
+                }
             }
         }
         __syncthreads();
@@ -386,7 +409,7 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
             const int e = slot_e[i];
             const bool taken = e != kNoExpert;
             ids[at] = taken ? e : -1;
-            weights[at] = taken ? __expf(slot_l[i] - slse[s]) * norm[s] : 0.0f;
+            weights[at] = slot_w[i];
             rows[at] = taken ? count[e] + __popcll(bits[e] & ((1ull << s) - 1)) : -1;
         }
         __syncthreads();
@@ -398,9 +421,9 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
             __syncthreads();
         }
     }
-    // the run's sums: lanes that hold the same experts, then wave after wave,
-    // so that their order is fixed
-    float *psum = ONE ? reinterpret_cast<float *>(count) : reinterpret_cast<float *>(bits);
+    // the run's sums: lanes that hold the same experts, then the waves two by
+    // two, so that their order is fixed
+    float *psum = reinterpret_cast<float *>(bits);  // two sets
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -409,27 +432,30 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
     zsum = lanes_sum<64>(zsum);
     const float fl = lanes_sum<64>((float)nlive);
     if (lane == 0) {
-        slse[wave] = zsum;
-        norm[wave] = fl;
+        zpart[wave] = zsum;
+        npart[wave] = fl;
     }
     const int waves = min(WAVES, (min(last - first, kRouteTile) + 64 / L - 1) / (64 / L));  // that had a token
-    for (int w = 0; w < max(waves, 1); ++w) {
-        if (wave == w && lane < L)
+    for (int w = 0; w < max(waves, 2); w += 2) {
+        if (wave >> 1 == w >> 1 && lane < L) {
+            float *set = psum + (wave & 1) * experts;
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (e0 + i < experts)
-                    psum[e0 + i] = (w ? psum[e0 + i] : 0.0f) + acc[i];
+                    set[e0 + i] = (w ? set[e0 + i] : 0.0f) + acc[i];
+        }
         __syncthreads();
     }
     float z = 0.0f, nl = 0.0f;
+#pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-        z += slse[w];
-        nl += norm[w];
+        z += zpart[w];
+        nl += npart[w];
     }
     if constexpr (!ONE) {
         for (int e = tid; e < experts; e += THREADS) {
             ws.counts[(int64_t)blockIdx.x * experts + e] = count[e];
-            ws.probs[(int64_t)blockIdx.x * experts + e] = psum[e];
+            ws.probs[(int64_t)blockIdx.x * experts + e] = psum[e] + psum[experts + e];
         }
         if (tid == 0) {
             ws.z[blockIdx.x] = z;
@@ -439,9 +465,9 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
         const double inv = nl > 0.0f ? 1.0 / (double)nl : 0.0;
         double b = 0.0;
         for (int e = tid; e < experts; e += THREADS) {
-            const double p = (double)psum[e] * inv;
+            const double p = (double)(psum[e] + psum[experts + e]) * inv;
             out.mean_prob[e] = (float)p;
-            b += (double)__popcll(bits[e]) * p;
+            b += (double)out.counts[e] * p;  // this thread's own store
         }
         __shared__ double part[WAVES];
         b = block_sum<THREADS>(part, b);
@@ -460,8 +486,8 @@ __global__ __launch_bounds__(kScanThreads) void moe_scan_kernel(int experts, int
                                                                 RouteResults out)
 {
     constexpr int PARTS = kScanThreads / kScanExperts, MOST = kRouteMaxBlocks / PARTS;
-    __shared__ int32_t psum[PARTS][kScanExperts];
-    __shared__ double qsum[PARTS][kScanExperts];
+    __shared__ int32_t psum[PARTS][kScanExperts + 1];
+    __shared__ double qsum[PARTS][kScanExperts + 1];
     __shared__ int32_t alive;
     const int tid = threadIdx.x, part = tid / kScanExperts, x = tid % kScanExperts;
     const int e = blockIdx.x * kScanExperts + x;
@@ -486,24 +512,35 @@ __global__ __launch_bounds__(kScanThreads) void moe_scan_kernel(int experts, int
     psum[part][x] = sum;
     qsum[part][x] = p;
     __syncthreads();
-    int before = 0;
-    for (int q = 0; q < part; ++q)
-        before += psum[q][x];
+    {
+        // the parts of one expert in consecutive lanes: one scan
+        const int q = tid % PARTS, y = tid / PARTS;
+        const int own = psum[q][y];
+        double all = qsum[q][y];
+        int upto = own;
+#pragma unroll
+        for (int m = 1; m < PARTS; m <<= 1) {
+            const int up = __shfl_up(upto, m, PARTS);
+            upto += q >= m ? up : 0;
+            all += __shfl_xor(all, m, PARTS);
+        }
+        psum[q][y] = upto - own;
+        const int f = blockIdx.x * kScanExperts + y;
+        if (q == PARTS - 1 && f < experts) {
+            const double inv = alive > 0 ? 1.0 / (double)alive : 0.0;
+            out.counts[f] = upto;
+            out.mean_prob[f] = (float)(all * inv);
+            ws.balance[f] = (double)upto * (all * inv);
+        }
+    }
+    __syncthreads();
+    int before = psum[part][x];
 #pragma unroll
     for (int i = 0; i < MOST; ++i)
         if (r0 + i < r1 && e < experts) {
             ws.counts[(int64_t)(r0 + i) * experts + e] = before;
             before += c[i];
         }
-    if (part == PARTS - 1 && e < experts) {
-        double q = 0.0;
-        for (int i = 0; i < PARTS; ++i)
-            q += qsum[i][x];
-        const double inv = alive > 0 ? 1.0 / (double)alive : 0.0;
-        out.counts[e] = before;
-        out.mean_prob[e] = (float)(q * inv);
-        ws.balance[e] = (double)before * (q * inv);
-    }
 }
 
 // A run per workgroup: its slots' ranks become rows.  The last workgroup
@@ -554,6 +591,9 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(int tokens, in
 // dl_te = p_te (g_te - sum_e' p_te' g_te') + 2 g_z lse_t p_te / n with
 // g_te = g_b E c_e / (n^2 k) + [e = ids_tj] q_tj, where q is the gradient of
 // the selected probabilities (through the renormalisation when there is one).
+// A slot's part is worked out by one lane and reaches the lane that holds its
+// expert through a row of zeros in LDS (comparing every expert with every slot
+// took three times as long).
 template <typename T, int L, int V>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(
     const T *__restrict__ logits, int64_t sl, int tokens, int experts, int k, int renorm,
@@ -561,55 +601,74 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(
     const int32_t *__restrict__ counts, const int32_t *__restrict__ live, const float *__restrict__ gw,
     const float *__restrict__ gl, T *__restrict__ dl, int64_t sd)
 {
+    extern __shared__ uint64_t lds[];
     const int tid = threadIdx.x, sub = tid % L, e0 = sub * V;
     const bool whole = experts % V == 0;
+    // this token's row: L * V entries, V of them per lane, in pieces of 4
+    float *row = reinterpret_cast<float *>(lds) + tid / L * (L * V);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        row[e0 + i] = 0.0f;
     const float n = (float)max(live ? live[0] : 1, 1);
     const float gb = gl ? gl[0] * (float)experts / (n * (float)k) / n : 0.0f;
     const float gz = gl ? 2.0f * gl[1] / n : 0.0f;
     float bal[V];
+    if (gl && whole && e0 < experts) {
+        typedef int32_t Ints __attribute__((ext_vector_type(V), aligned(4)));
+        const Ints c = *reinterpret_cast<const Ints *>(counts + e0);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        bal[i] = gl && e0 + i < experts ? gb * (float)counts[e0 + i] : 0.0f;
+        for (int i = 0; i < V; ++i)
+            bal[i] = gb * (float)c[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            bal[i] = gl && e0 + i < experts ? gb * (float)counts[e0 + i] : 0.0f;
+    }
     const int64_t per_grid = (int64_t)gridDim.x * (256 / L);
     for (int64_t t = (int64_t)blockIdx.x * (256 / L) + tid / L; t < tokens; t += per_grid) {
         float v[V];
         load_row<T, V>(logits + t * sl, e0, experts, whole, -INFINITY, v);
         const float lse = lse_in[t];
         const bool dead = lse == INFINITY;
-        float p[V], g[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            p[i] = dead || v[i] == -INFINITY ? 0.0f : __expf(v[i] - lse);
-            g[i] = bal[i];
-        }
         if (gw) {
-            float total = 1.0f, wg = 0.0f;
+            float total = 0.0f, wg = 0.0f;
             if (renorm) {
-                total = 0.0f;
-                for (int j = 0; j < k; ++j) {
+                for (int j = sub; j < k; j += L) {
                     const int e = ids[t * k + j];
-                    if (e >= 0)
+                    if (e >= 0 && e < experts) {
+                        total += __expf(Piece<T>::to_f32(logits[t * sl + e]) - lse);
                         wg = fmaf(weights[t * k + j], gw[t * k + j], wg);
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        total += e == e0 + i ? p[i] : 0.0f;
+                    }
                 }
                 total = lanes_sum<L>(total);
+                wg = lanes_sum<L>(wg);
             }
-            const float inv = 1.0f / total;
-            for (int j = 0; j < k; ++j) {
+            const float inv = renorm ? 1.0f / total : 1.0f;
+            for (int j = sub; j < k; j += L) {
                 const int e = ids[t * k + j];
-                const float q = (gw[t * k + j] - wg) * inv;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    g[i] += e == e0 + i ? q : 0.0f;
+                if (e >= 0 && e < experts)
+                    row[e] = (gw[t * k + j] - wg) * inv;
             }
+            // lanes of one wave: LDS runs its instructions in order
+            __builtin_amdgcn_wave_barrier();
         }
-        float dot = 0.0f;
+        float p[V], g[V], dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+            g[i] = bal[i] + (gw ? row[e0 + i] : 0.0f);
+            p[i] = __expf(v[i] - lse);  // 0 for -inf; a dead token's is not used
             dot = fmaf(p[i], g[i], dot);
+        }
         dot = lanes_sum<L>(dot) - gz * lse;
+        if (gw) {
+            __builtin_amdgcn_wave_barrier();
+            for (int j = sub; j < k; j += L) {
+                const int e = ids[t * k + j];
+                if (e >= 0 && e < experts)
+                    row[e] = 0.0f;
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
         typedef T Vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
         T *out = dl + t * sd + e0;
         Vec o;

@@ -81,7 +81,7 @@ def test_token_counts(T, E, k):
     check(T, E, k, masked=T > 64, align=16)
 
 
-@pytest.mark.parametrize("E,k", [(1, 1), (2, 2), (3, 2), (7, 7), (9, 3), (13, 13), (32, 32), (33, 8), (64, 6), (128, 8),
+@pytest.mark.parametrize("E,k", [(1, 1), (2, 2), (3, 2), (7, 7), (9, 3), (13, 13), (32, 32), (33, 8), (64, 6), (40, 20), (64, 32), (100, 17), (128, 32), (500, 32), (128, 8),
                                  (129, 32), (200, 5), (256, 8), (257, 1), (384, 6), (512, 10), (700, 4), (1024, 8),
                                  (1500, 3), (4096, 32)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -105,6 +105,19 @@ def test_unavailable_experts_and_masked_tokens(E, k, renorm):
 def test_strided_and_unaligned_logits(pad, shift, dtype):
     check(100, 64, 4, dtype=dtype, pad=pad, shift=shift)
     check(100, 30, 4, dtype=dtype, pad=pad, shift=shift)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_extreme_logits(dtype):
+    """The largest and smallest finite logits, infinitesimal ones and signed
+    zeros are ordered and taken like any others."""
+    top = torch.finfo(dtype).max
+    vals = [top, -top, 0.0, -0.0, 1e-40, -1e-40, 3.0, -float("inf"), -top, 88.0, -88.0, 3.0]
+    l = torch.tensor([vals, vals[::-1], [-top] * 12, [-float("inf")] * 11 + [-top]], dtype=dtype)
+    want = ref.route(l.double().numpy(), 12)
+    for k in (3, 12):
+        r = mxq.moe_route(l.to(DEV), k)
+        assert np.array_equal(r.ids.cpu().numpy(), want["ids"][:, :k])
 
 
 def test_many_tokens_take_longer_runs():
