@@ -150,6 +150,15 @@ int pieces_per_lane(int64_t width, int most)
     return u;
 }
 
+// from here on a call's loads carry the nontemporal hint (see ld_piece): between
+// the 100 MB that lose by it and the 235 MB that gain
+constexpr int64_t kStreamBytes = 160 << 20;
+template <typename T>
+bool streams(int64_t tokens, int64_t width, int k)
+{
+    return tokens * width * (k + 1) * (int64_t)sizeof(T) >= kStreamBytes;
+}
+
 template <typename T, int U>
 mxq_status run_dispatch(const void *x, int64_t sx, int tokens, int width, const int32_t *rows, int k,
                         const int32_t *counts, const int32_t *offs, int experts, void *out, int64_t ld,
@@ -159,7 +168,8 @@ mxq_status run_dispatch(const void *x, int64_t sx, int tokens, int width, const 
     const int64_t items = tokens * chunks, work = (items + 3) / 4, clear = clear_blocks(capacity);
     if (items > INT32_MAX - 4096)
         return MXQ_ERR_INVALID_ARG;
-    moe_dispatch_kernel<T, U><<<dim3((unsigned)(work + clear)), dim3(kRowsThreads), 0, st>>>(
+    auto kernel = streams<T>(tokens, width, k) ? moe_dispatch_kernel<T, U, true> : moe_dispatch_kernel<T, U, false>;
+    kernel<<<dim3((unsigned)(work + clear)), dim3(kRowsThreads), 0, st>>>(
         reinterpret_cast<const T *>(x), sx, tokens, width, rows, k, counts, offs, experts,
         reinterpret_cast<T *>(out), ld, capacity, (int)chunks, (int)work);
     return launch_status();
@@ -174,7 +184,8 @@ mxq_status run_combine(const void *in, int64_t ld, int capacity, int width, cons
     const int64_t items = tokens * chunks, work = (items + 3) / 4;
     if (items > INT32_MAX - 4096)
         return MXQ_ERR_INVALID_ARG;
-    moe_combine_kernel<T, U, KB><<<dim3((unsigned)work), dim3(kRowsThreads), 0, st>>>(
+    auto kernel = streams<T>(tokens, width, k) ? moe_combine_kernel<T, U, KB, true> : moe_combine_kernel<T, U, KB, false>;
+    kernel<<<dim3((unsigned)work), dim3(kRowsThreads), 0, st>>>(
         reinterpret_cast<const T *>(in), ld, capacity, width, rows, weights, k, reinterpret_cast<const T *>(resid),
         sr, reinterpret_cast<T *>(y), sy, tokens, (int)chunks);
     return launch_status();
@@ -190,7 +201,10 @@ mxq_status run_combine_backward(const void *dy, int64_t sy, int tokens, int widt
     const int64_t work = ((int64_t)tokens + TPB - 1) / TPB, clear = clear_blocks(capacity);
     if (work > INT32_MAX - 4096)
         return MXQ_ERR_INVALID_ARG;
-    moe_combine_backward_kernel<T, NW, KB><<<dim3((unsigned)(work + clear)), dim3(kRowsThreads), 0, st>>>(
+    // rows read and written
+    auto kernel = streams<T>(tokens, width, 2 * k) ? moe_combine_backward_kernel<T, NW, KB, true>
+                                                   : moe_combine_backward_kernel<T, NW, KB, false>;
+    kernel<<<dim3((unsigned)(work + clear)), dim3(kRowsThreads), 0, st>>>(
         reinterpret_cast<const T *>(dy), sy, tokens, width, reinterpret_cast<const T *>(in), ld, rows, weights, k,
         counts, offs, experts, capacity, reinterpret_cast<T *>(out), ldo, dw, (int)work);
     return launch_status();

@@ -64,11 +64,19 @@ __device__ __forceinline__ int piece_start(int p, int width)
     return c + Piece<T>::N <= width ? c : width - Piece<T>::N;
 }
 
-template <typename T>
+// STREAM: with the nontemporal hint, for calls that move more than the caches
+// hold.  16384 tokens of 4096 bf16 over 2 slots (402 MB): dispatch 75 -> 61 us,
+// combine 76 -> 65, its gradient 130 -> 104; 4096 tokens (100 MB) lose: 16.2
+// -> 18.8, 19.7 -> 19.8, 30.8 -> 30.0.  The hint on the stores as well, or on
+// them alone, is slower (70 and 72 us for the first).
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ Piece<T> ld_piece(const T *p)
 {
     Piece<T> r;
-    r.v = *reinterpret_cast<const typename Piece<T>::V *>(p);
+    if constexpr (STREAM)
+        r.v = __builtin_nontemporal_load(reinterpret_cast<const typename Piece<T>::V *>(p));
+    else
+        r.v = *reinterpret_cast<const typename Piece<T>::V *>(p);
     return r;
 }
 template <typename T>
@@ -116,7 +124,7 @@ __device__ __forceinline__ void zero_rows(int z, int nz, const int32_t *__restri
 
 // One wave per (token, chunk of 64 * U pieces); the workgroups past
 // `work` blocks clear the rows without a slot.
-template <typename T, int U>
+template <typename T, int U, bool STREAM>
 __global__ __launch_bounds__(kRowsThreads) void moe_dispatch_kernel(
     const T *__restrict__ x, int64_t sx, int tokens, int width, const int32_t *__restrict__ rows, int k,
     const int32_t *__restrict__ counts, const int32_t *__restrict__ offs, int experts, T *__restrict__ out,
@@ -148,7 +156,7 @@ __global__ __launch_bounds__(kRowsThreads) void moe_dispatch_kernel(
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         c[u] = piece_start<T>(min(p0 + 64 * u, pieces - 1), width);
-        v[u] = ld_piece<T>(src + c[u]);
+        v[u] = ld_piece<T, STREAM>(src + c[u]);
     }
     for (int j = 0; j < k; ++j) {
         const int r = slots[j];
@@ -164,7 +172,7 @@ __global__ __launch_bounds__(kRowsThreads) void moe_dispatch_kernel(
 
 // One wave per (token, chunk of 64 * U pieces), KB slots' loads in flight at
 // a time.  Loads of empty slots go to row 0 and are not used.
-template <typename T, int U, int KB>
+template <typename T, int U, int KB, bool STREAM>
 __global__ __launch_bounds__(kRowsThreads) void moe_combine_kernel(
     const T *__restrict__ in, int64_t ld, int capacity, int width, const int32_t *__restrict__ rows,
     const float *__restrict__ weights, int k, const T *__restrict__ resid, int64_t sr, T *__restrict__ y,
@@ -203,7 +211,7 @@ __global__ __launch_bounds__(kRowsThreads) void moe_combine_kernel(
     if (resid) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const Piece<T> v = ld_piece<T>(resid + (int64_t)t * sr + c[u]);
+            const Piece<T> v = ld_piece<T, STREAM>(resid + (int64_t)t * sr + c[u]);
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 acc[u][i] = v.get(i);
@@ -223,7 +231,7 @@ __global__ __launch_bounds__(kRowsThreads) void moe_combine_kernel(
             const T *src = in + (int64_t)max(r[j], 0) * ld;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                v[j][u] = ld_piece<T>(src + c[u]);
+                v[j][u] = ld_piece<T, STREAM>(src + c[u]);
         }
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
@@ -258,7 +266,7 @@ __device__ __forceinline__ float wave_sum(float v)
 
 // NW waves per token; each lane holds its piece of dy while KB slots' rows
 // pass, and the dot products meet in a fixed order (lane tree, then waves).
-template <typename T, int NW, int KB>
+template <typename T, int NW, int KB, bool STREAM>
 __global__ __launch_bounds__(kRowsThreads) void moe_combine_backward_kernel(
     const T *__restrict__ dy, int64_t sy, int tokens, int width, const T *__restrict__ in, int64_t ld,
     const int32_t *__restrict__ rows, const float *__restrict__ weights, int k,
@@ -307,11 +315,11 @@ __global__ __launch_bounds__(kRowsThreads) void moe_combine_backward_kernel(
             for (int p = wt * 64 + lane; p < pieces; p += NW * 64) {
                 const int c = piece_start<T>(p, width);
                 const int skip = p * N - c;  // elements that the piece before has
-                const Piece<T> d = ld_piece<T>(g + c);
+                const Piece<T> d = ld_piece<T, STREAM>(g + c);
                 Piece<T> v[KB];
 #pragma unroll
                 for (int j = 0; j < KB; ++j)
-                    v[j] = ld_piece<T>(in + (int64_t)max(r[j], 0) * ld + c);
+                    v[j] = ld_piece<T, STREAM>(in + (int64_t)max(r[j], 0) * ld + c);
 #pragma unroll
                 for (int j = 0; j < KB; ++j) {
                     if (r[j] < 0)
