@@ -53,7 +53,7 @@ MuonPlan muon_plan(int64_t count, int64_t rows, int64_t cols)
         p.tile = 0;
     p.mp = round_up(m, p.tile == 2 ? 256 : p.tile == 1 ? 128 : 64);
     p.np = round_up(n, p.tile == 2 ? 256 : 64);
-    p.bytes = count * (6 * p.mp * p.np + 6 * p.mp * p.mp + 8 * p.mp + 8 * kNormParts);
+    p.bytes = count * (5 * p.mp * p.np + 5 * p.mp * p.mp + 8 * p.mp + 8 * kNormParts);
     return p;
 }
 
@@ -147,12 +147,12 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
     const int64_t nx = count * p.mp * p.np, na = count * p.mp * p.mp;
     buf.xh[0] = reinterpret_cast<_Float16 *>(buf.part + count * kNormParts);
     buf.xh[1] = buf.xh[0] + nx;
-    buf.xl = buf.xh[1] + nx;
-    buf.oh = buf.xl + nx;
-    buf.ol = buf.oh + na;
-    buf.bo = buf.ol + na;
+    buf.oh = buf.xh[1] + nx;
+    buf.bo = buf.oh + na;
     buf.d = reinterpret_cast<float *>(buf.bo + na);
     buf.db = buf.d + count * p.mp;
+    buf.xl = reinterpret_cast<uint8_t *>(buf.db + count * p.mp);
+    buf.ol = buf.xl + nx;
 
     // X is G, or G transposed when G is tall
     const bool tall = rows > cols;

@@ -15,13 +15,14 @@
 // cost 1.4e-3 to 3e-3 of the result (relative 2-norm, simulated), more than
 // the final bf16 rounding (1.65e-3).  Two exact rearrangements bring it to
 // 3e-4 to 7e-4 without another product:
-//   - X is carried in two f16 parts (22 bits), and a X + diag(B) X is added in
-//     fp32 from both parts; only the product with the rest of B sees the high
-//     part alone;
+//   - X is carried in two parts, f16 and the difference in e4m3 (about 15
+//     bits; 22 bits of f16 + f16 measured no better and cost a byte per element
+//     each way), and a X + diag(B) X is added in fp32 from both parts; only the
+//     product with the rest of B sees the f16 part alone;
 //   - the diagonals d of A and of B, which are the large entries when the
 //     singular values are near one another, never enter an f16 operand: with
 //     A = diag(d) + O,  A^2 = O O + d_i O_ij + O_ij d_j + diag(d^2), and the
-//     last three terms are fp32 in the epilogue (O there from two f16 parts).
+//     last three terms are fp32 in the epilogue (O there from two parts).
 //
 // Layout.  X is row-major.  X X^T and O O sum along rows; B X sums along X's
 // columns and reads its operand through the transposing LDS read, so X is
@@ -48,14 +49,16 @@ typedef float float4v __attribute__((ext_vector_type(4)));
 constexpr float kScaleX = 8192.0f;   // |x| <= 1.3: up to 10650; room to 8
 constexpr float kScaleA = 2048.0f;   // |o| <= 1.7; room to 32
 constexpr float kScaleB = 2048.0f;   // |b| <= 3; room to 32
-constexpr float kLow = 2048.0f;      // the low parts are stored times 2^11
+constexpr float kLow = 64.0f;        // low parts are stored times this: half an f16 ulp of 10650 is 4, e4m3 ends at 448
 constexpr int kBand = 8;              // row tiles of a band (order of the tiles)
 constexpr int kNormParts = 256;      // partial sums of a matrix's squared norm
 
 // Buffers of one call; matrix e's parts are `e` strides further.
 struct MuonBuffers {
-    _Float16 *xh[2], *xl;   // [mp][np] high parts of X, this step's and the next; low part
-    _Float16 *oh, *ol, *bo; // [mp][mp] off-diagonal A (two parts) and B
+    _Float16 *xh[2];        // [mp][np] X, this step's and the next
+    uint8_t *xl;            // [mp][np] its low part
+    _Float16 *oh, *bo;      // [mp][mp] off-diagonal A and B
+    uint8_t *ol;            // [mp][mp] A's low part
     float *d, *db;          // [mp] diagonals of A and B
     double *part;           // [kNormParts] partial sums of squares
     int mp, np;             // padded extents
@@ -66,13 +69,32 @@ struct MuonView {           // x(i, j) = p[e * se + i * si + j * sj], i < m, j <
     int m, n;
 };
 
-__device__ __forceinline__ void split_half(float v, _Float16 &hi, _Float16 &lo)
+// eight values as f16 and the e4m3 codes of what f16 left of them
+__device__ __forceinline__ void split8(const float (&v)[8], half8 &hi, uint2 &lo)
 {
-    hi = (_Float16)v;
-    lo = (_Float16)((v - (float)hi) * kLow);
+    float r[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        hi[k] = (_Float16)v[k];
+        r[k] = (v[k] - (float)hi[k]) * kLow;
+    }
+    lo.x = cvt4(r[0], r[1], r[2], r[3]);
+    lo.y = cvt4(r[4], r[5], r[6], r[7]);
 }
 
-__device__ __forceinline__ float join_half(_Float16 hi, _Float16 lo) { return (float)hi + (float)lo * (1.0f / kLow); }
+__device__ __forceinline__ void join8(const half8 &hi, const uint2 &lo, float (&v)[8])
+{
+    typedef float float2v __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const float2v a = __builtin_amdgcn_cvt_pk_f32_fp8((int)(q ? lo.y : lo.x), false);
+        const float2v b = __builtin_amdgcn_cvt_pk_f32_fp8((int)(q ? lo.y : lo.x), true);
+        v[4 * q] = fmaf(a[0], 1.0f / kLow, (float)hi[4 * q]);
+        v[4 * q + 1] = fmaf(a[1], 1.0f / kLow, (float)hi[4 * q + 1]);
+        v[4 * q + 2] = fmaf(b[0], 1.0f / kLow, (float)hi[4 * q + 2]);
+        v[4 * q + 3] = fmaf(b[1], 1.0f / kLow, (float)hi[4 * q + 3]);
+    }
+}
 
 // ---------------------------------------------------------------- norm, load
 
@@ -182,17 +204,16 @@ __global__ __launch_bounds__(256) void muon_load_kernel(const T *__restrict__ g,
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = (tid >> 3) + 32 * h, j = (tid & 7) * 8;
-        half8 hi, lo;
+        half8 hi;
+        uint2 lo;
+        float x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            _Float16 a, c;
-            split_half(tile[i][j + k], a, c);
-            hi[k] = a;
-            lo[k] = c;
-        }
+        for (int k = 0; k < 8; ++k)
+            x[k] = tile[i][j + k];
+        split8(x, hi, lo);
         const int64_t at = xo + (int64_t)(i0 + i) * b.np + j0 + j;
         *reinterpret_cast<half8 *>(b.xh[0] + at) = hi;
-        *reinterpret_cast<half8 *>(b.xl + at) = lo;
+        *reinterpret_cast<uint2 *>(b.xl + at) = lo;
     }
 }
 
@@ -220,12 +241,16 @@ __device__ __forceinline__ void wait_stage()
 
 // four rows (summed dim) by 16 columns of f16, one column per lane: lane i of
 // 16 points at row i / 4, columns 4 (i % 4) and receives column i of all four
-__device__ __forceinline__ half4 read_transposed(const _Float16 *p)
+__device__ __forceinline__ half4 read_transposed(uint32_t a)
 {
     typedef short short4v __attribute__((ext_vector_type(4)));
-    const uint32_t a = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
     return __builtin_bit_cast(half4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                                          (__attribute__((address_space(3))) short4v *)(uintptr_t)a));
+}
+
+__device__ __forceinline__ half8 read_lds(uint32_t a)
+{
+    return *(__attribute__((address_space(3))) const half8 *)(uintptr_t)a;
 }
 
 enum MuonMode { kModeA, kModeB, kModeX, kModeOut };
@@ -324,30 +349,44 @@ struct MuonStages {
     const char *pbase, *qbase;
     int64_t prow, qrow, qstep;   // bytes from load to load, and of Q from stage to stage
     uint32_t poff, qoff, lds0;
-    const _Float16 *lds;
-    int wave, fr, fk;
+    // LDS addresses of this lane's fragment reads in stage 0: by half of the
+    // stage, or (transposed Q) by column fragment.  The rest of an address is
+    // a constant of the instruction.
+    uint32_t pread[2], qread[QT ? TILE::FQ : 2];
+    int wave;
 
-    static __device__ __forceinline__ int rswap(int r) { return BK == 64 ? (r >> 1) & 7 : -(r >> 2) & 3; }
+    // both depend on the row's low four bits alone
+    static __device__ __forceinline__ int rswap(int r) { return (r >> 1) & 7; }
     static __device__ __forceinline__ int qswap(int k)
     {
         return TN >= 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
     }
 
+    // row0, col0: the wave's part of the tile
     __device__ __forceinline__ MuonStages(const _Float16 *l, const _Float16 *P, const _Float16 *Q, int K, int ldq,
-                                          int w)
+                                          int w, int row0, int col0)
         : pbase(reinterpret_cast<const char *>(P)), qbase(reinterpret_cast<const char *>(Q)),
           prow((int64_t)PR * K * 2), qrow((int64_t)QR * (QT ? ldq : K) * 2), qstep(QT ? (int64_t)BK * ldq * 2 : BK * 2),
-          lds0((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)l), lds(l), wave(w),
-          fr(threadIdx.x & 15), fk((threadIdx.x & 63) >> 4)
+          lds0((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)l), wave(w)
     {
-        const int t = threadIdx.x, r = t / CH;
+        const int t = threadIdx.x, r = t / CH, fr = t & 15, fk = (t & 63) >> 4;
         poff = (uint32_t)(r * K + ((t % CH) ^ rswap(r)) * 8) * 2;
         if (QT) {
             const int k = t / (TN / 8);
             qoff = (uint32_t)(k * ldq + ((t % (TN / 8)) ^ (qswap(k) << 1)) * 8) * 2;
+            const int kr = 8 * fk + (fr >> 2);  // and the four rows after
+#pragma unroll
+            for (int j = 0; j < TILE::FQ; ++j)
+                qread[j] = lds0 + (uint32_t)(TM * BK + kr * TN + ((col0 / 16 + j) ^ qswap(kr)) * 16 + (fr & 3) * 4) * 2;
         } else {
             qoff = poff;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                qread[h] = lds0 + (uint32_t)((TM + col0 + fr) * BK + ((h * 4 + fk) ^ rswap(fr)) * 8) * 2;
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            pread[h] = lds0 + (uint32_t)((row0 + fr) * BK + ((h * 4 + fk) ^ rswap(fr)) * 8) * 2;
     }
 
     // load u of stage kt into LDS stage s
@@ -365,34 +404,27 @@ struct MuonStages {
             load_one(s, u, kt);
     }
 
-    // fragments of 32 summed elements from 32 ks on
-    template <int N>
-    __device__ __forceinline__ void read_p(int stage, int ks, int row0, half8 (&pf)[N]) const
+    // fragments I0.. of P, and of Q, in half `ks` of a stage
+    template <int I0, int N>
+    __device__ __forceinline__ void read_p(int stage, int ks, half8 (&pf)[N]) const
     {
-        const _Float16 *pb = lds + stage * TILE::STAGE;
+        const uint32_t a = pread[ks] + (uint32_t)(stage * TILE::STAGE * 2);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int r = row0 + i * 16 + fr;
-            pf[i] = *reinterpret_cast<const half8 *>(pb + r * BK + (((ks * 4 + fk) ^ rswap(r)) * 8));
-        }
+        for (int i = 0; i < N; ++i)
+            pf[i] = read_lds(a + (I0 + i) * 16 * BK * 2);
     }
 
-    template <int N>
-    __device__ __forceinline__ void read_q(int stage, int ks, int col0, half8 (&qf)[N]) const
+    __device__ __forceinline__ void read_q(int stage, int ks, half8 (&qf)[TILE::FQ]) const
     {
-        const _Float16 *qb = lds + stage * TILE::STAGE + TM * BK;
+        const uint32_t off = (uint32_t)(stage * TILE::STAGE * 2);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int j0 = col0 + j * 16;
+        for (int j = 0; j < TILE::FQ; ++j) {
             if constexpr (!QT) {
-                const int r = j0 + fr;
-                qf[j] = *reinterpret_cast<const half8 *>(qb + r * BK + (((ks * 4 + fk) ^ rswap(r)) * 8));
+                qf[j] = read_lds(qread[ks] + off + j * 16 * BK * 2);
             } else {
-                // rows 8 fk + 0..3, then + 4..7
-                const int k = 32 * ks + 8 * fk + (fr >> 2), c = (fr & 3) * 4;
-                const half4 a = read_transposed(qb + k * TN + ((j0 / 16) ^ qswap(k)) * 16 + c);
-                const half4 h = read_transposed(qb + (k + 4) * TN + ((j0 / 16) ^ qswap(k + 4)) * 16 + c);
-                qf[j] = half8{a[0], a[1], a[2], a[3], h[0], h[1], h[2], h[3]};
+                const uint32_t a = qread[j] + off + ks * 32 * TN * 2;
+                const half4 x = read_transposed(a), y = read_transposed(a + 4 * TN * 2);
+                qf[j] = half8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
             }
         }
     }
@@ -415,7 +447,7 @@ __device__ __forceinline__ void multiply(const half8 (&pf)[N], const half8 (&qf)
 // At the barrier every wave has read stage kt and has stage kt + 1; the load
 // of stage kt + NST overwrites stage kt.
 template <typename TILE, bool QT>
-__device__ __forceinline__ void run_pipeline(const MuonStages<TILE, QT> &st, int end, int row0, int col0,
+__device__ __forceinline__ void run_pipeline(const MuonStages<TILE, QT> &st, int end,
                                              float4v (&acc)[TILE::FP][TILE::FQ])
 {
     static_assert(TILE::BK == 64, "a stage has two halves");
@@ -428,13 +460,13 @@ __device__ __forceinline__ void run_pipeline(const MuonStages<TILE, QT> &st, int
         wait_stage<(NST - 1) * TILE::LOADS>();
     else
         wait_stage<0>();
-    st.read_q(0, 0, col0, q0);
-    st.read_p(0, 0, row0, p0);
+    st.read_q(0, 0, q0);
+    st.template read_p<0>(0, 0, p0);
     int now = 0, kt = 0;
     for (; kt + 1 < end; ++kt) {
         const int next = now + 1 == NST ? 0 : now + 1;
-        st.read_q(now, 1, col0, q1);
-        st.read_p(now, 1, row0, p1);
+        st.read_q(now, 1, q1);
+        st.template read_p<0>(now, 1, p1);
         multiply<0>(p0, q0, acc);
         if (kt + NST <= end)
             wait_stage<(NST - 2) * TILE::LOADS>();
@@ -442,13 +474,13 @@ __device__ __forceinline__ void run_pipeline(const MuonStages<TILE, QT> &st, int
             wait_stage<0>();
         if (kt + NST < end)
             st.load(now, kt + NST);
-        st.read_q(next, 0, col0, q0);
-        st.read_p(next, 0, row0, p0);
+        st.read_q(next, 0, q0);
+        st.template read_p<0>(next, 0, p0);
         multiply<0>(p1, q1, acc);
         now = next;
     }
-    st.read_q(now, 1, col0, q1);
-    st.read_p(now, 1, row0, p1);
+    st.read_q(now, 1, q1);
+    st.template read_p<0>(now, 1, p1);
     multiply<0>(p0, q0, acc);
     multiply<0>(p1, q1, acc);
 }
@@ -494,7 +526,6 @@ struct MuonAlternating {
     static constexpr int H = TILE::FP / 2;
     static constexpr int SECOND = TILE::LOADS - 6;  // loads of the second third
     const MuonStages<TILE, QT> &st;
-    int row0, col0;
     half8 p0[H], p1[H], q0[TILE::FQ], q1[TILE::FQ];
 
     __device__ __forceinline__ void load2(int u0, int u1, int kt) const
@@ -513,15 +544,15 @@ struct MuonAlternating {
 
     __device__ __forceinline__ void read_a(int s)
     {
-        st.read_q(s, 0, col0, q0);
-        st.read_p(s, 0, row0, p0);
-        st.read_q(s, 1, col0, q1);
-        st.read_p(s, 1, row0, p1);
+        st.read_q(s, 0, q0);
+        st.template read_p<0>(s, 0, p0);
+        st.read_q(s, 1, q1);
+        st.template read_p<0>(s, 1, p1);
     }
     __device__ __forceinline__ void read_b(int s)
     {
-        st.read_p(s, 0, row0 + H * 16, p0);
-        st.read_p(s, 1, row0 + H * 16, p1);
+        st.template read_p<H>(s, 0, p0);
+        st.template read_p<H>(s, 1, p1);
     }
     template <int I0>
     __device__ __forceinline__ void products(float4v (&acc)[TILE::FP][TILE::FQ])
@@ -623,7 +654,34 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
     const int K = MODE == kModeA ? b.np : b.mp;
     const _Float16 *P = MODE == kModeA ? b.xh[st.cur] + xo : MODE == kModeB ? b.oh + ao : b.bo + ao;
     const _Float16 *Q = SYM ? P + (int64_t)j0 * K : b.xh[st.cur] + xo + j0;
-    MuonStages<TILE, !SYM> stages(lds, P + (int64_t)i0 * K, Q, K, b.np, wave);
+    MuonStages<TILE, !SYM> stages(lds, P + (int64_t)i0 * K, Q, K, b.np, wave, wp * FP * 16, wq * FQ * 16);
+
+    // What the results are combined with, for RC rows of the wave's part.  With
+    // few registers per thread it is read before the products, so that it costs
+    // no wait after them.
+    constexpr int RC = TILE::RC, WJ = TILE::WJ, LPR = WJ / 8, RPP = 64 / LPR, PASSES = RC / RPP;
+    constexpr int CHUNKS = FP * 16 / RC;
+    constexpr bool EARLY = CHUNKS == 1 && PASSES <= 2;
+    const int lane = threadIdx.x & 63, pr = lane / LPR, pc = lane % LPR;
+    const int wi0 = i0 + wp * FP * 16, wj0 = j0 + wq * WJ, gj = wj0 + pc * 8;
+    float *d = b.d + (int64_t)e * b.mp, *db = b.db + (int64_t)e * b.mp;
+    half8 oldh[2][PASSES];
+    uint2 oldl[2][PASSES];
+    float di[2][PASSES];
+    auto load_old = [&](int ic, int set) {
+        if constexpr (MODE != kModeA) {
+#pragma unroll
+            for (int p = 0; p < PASSES; ++p) {
+                const int gi = wi0 + ic + p * RPP + pr;
+                di[set][p] = MODE == kModeB ? d[gi] : db[gi];
+                const int64_t at = MODE == kModeB ? ao + (int64_t)gi * b.mp + gj : xo + (int64_t)gi * b.np + gj;
+                oldh[set][p] = *reinterpret_cast<const half8 *>((MODE == kModeB ? b.oh : b.xh[st.cur]) + at);
+                oldl[set][p] = *reinterpret_cast<const uint2 *>((MODE == kModeB ? b.ol : b.xl) + at);
+            }
+        }
+    };
+    if constexpr (EARLY)
+        load_old(0, 0);
 
     float4v acc[FP][FQ];
 #pragma unroll
@@ -632,17 +690,14 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
         for (int j = 0; j < FQ; ++j)
             acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (TILE::TM == 256)
-        MuonAlternating<TILE, !SYM>{stages, wp * FP * 16, wq * FQ * 16}.run(K / TILE::BK, acc);
+        MuonAlternating<TILE, !SYM>{stages}.run(K / TILE::BK, acc);
     else
-        run_pipeline<TILE, !SYM>(stages, K / TILE::BK, wp * FP * 16, wq * FQ * 16, acc);
+        run_pipeline<TILE, !SYM>(stages, K / TILE::BK, acc);
 
     // Results.  A lane holds row l % 16, columns 4 (l / 16) + 0..3 of each
     // fragment; through LDS (each wave in its own region, RC rows at a time)
     // it gets 8 consecutive columns of one row instead, so that everything
     // below is read and written in 16-byte pieces of whole 128-byte lines.
-    constexpr int RC = TILE::RC, WJ = TILE::WJ, LPR = WJ / 8, RPP = 64 / LPR, PASSES = RC / RPP;
-    const int lane = threadIdx.x & 63, pr = lane / LPR, pc = lane % LPR;
-    const int wi0 = i0 + wp * FP * 16, wj0 = j0 + wq * WJ;
     // stored a second time (or only) transposed: the mirror of an off-diagonal
     // tile, and the output of a tall matrix
     const bool turned = SYM ? mirror : MODE == kModeOut && ov.si == 1 && ov.sj != 1;
@@ -652,39 +707,30 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
     // 32-byte chunks of f16 rows
     auto wswap = [](int r) { return WJ == 64 ? r & 15 : (r >> 1) & 7; };
     auto tswap = [](int r) { return WJ == 64 ? ((r >> 1) & 1) | ((r >> 3) & 1) << 1 : (r >> 3) & 1; };
-    float *d = b.d + (int64_t)e * b.mp, *db = b.db + (int64_t)e * b.mp;
+    if constexpr (!EARLY)
+        load_old(0, 0);
     float dj[8];
     if constexpr (MODE == kModeB)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            dj[k] = d[wj0 + pc * 8 + k];
+            dj[k] = d[gj + k];
     wait_stage<0>();  // every wave is done with the stages
 #pragma unroll
-    for (int ic = 0; ic < FP * 16; ic += RC) {
-        // what the results are combined with, on its way while they turn
-        half8 oldh[PASSES], oldl[PASSES];
-        float di[PASSES];
-        if constexpr (MODE != kModeA) {
-#pragma unroll
-            for (int p = 0; p < PASSES; ++p) {
-                const int gi = wi0 + ic + p * RPP + pr, gj = wj0 + pc * 8;
-                di[p] = MODE == kModeB ? d[gi] : db[gi];
-                const int64_t at = MODE == kModeB ? ao + (int64_t)gi * b.mp + gj : xo + (int64_t)gi * b.np + gj;
-                oldh[p] = *reinterpret_cast<const half8 *>((MODE == kModeB ? b.oh : b.xh[st.cur]) + at);
-                oldl[p] = *reinterpret_cast<const half8 *>((MODE == kModeB ? b.ol : b.xl) + at);
-            }
-        }
+    for (int ch = 0; ch < CHUNKS; ++ch) {
+        const int ic = ch * RC, set = ch & 1;
 #pragma unroll
         for (int i = 0; i < RC / 16; ++i)
 #pragma unroll
             for (int j = 0; j < FQ; ++j)
                 *reinterpret_cast<float4v *>(wide + (i * 16 + fr) * WJ + ((4 * j + fk) ^ wswap(i * 16 + fr)) * 4) =
                     acc[ic / 16 + i][j];
+        if (ch + 1 < CHUNKS)
+            load_old(ic + RC, set ^ 1);
         __builtin_amdgcn_wave_barrier();
         half8 h8[PASSES];
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
-            const int r = p * RPP + pr, gi = wi0 + ic + r, gj = wj0 + pc * 8;
+            const int r = p * RPP + pr, gi = wi0 + ic + r;
             float v[8];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -693,30 +739,30 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
                 for (int k = 0; k < 4; ++k)
                     v[4 * q + k] = x[k];
             }
+            uint2 low;
             if constexpr (MODE == kModeA) {
-                half8 l8;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float x = v[k] * (1.0f / (kScaleX * kScaleX));
+                    v[k] *= 1.0f / (kScaleX * kScaleX);
                     const bool diag = gi == gj + k;
                     if (diag)
-                        d[gi] = x;
-                    _Float16 h, l;
-                    split_half(diag ? 0.0f : x * kScaleA, h, l);
-                    h8[p][k] = h;
-                    l8[k] = l;
+                        d[gi] = v[k];
+                    v[k] = diag ? 0.0f : v[k] * kScaleA;
                 }
+                split8(v, h8[p], low);
                 const int64_t at = ao + (int64_t)gi * b.mp + gj;
                 *reinterpret_cast<half8 *>(b.oh + at) = h8[p];
-                *reinterpret_cast<half8 *>(b.ol + at) = l8;
+                *reinterpret_cast<uint2 *>(b.ol + at) = low;
             } else if constexpr (MODE == kModeB) {
+                const float dg = di[set][p];
+                float o[8];
+                join8(oldh[set][p], oldl[set][p], o);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float oo = v[k] * (1.0f / (kScaleA * kScaleA));
-                    const float o = join_half(oldh[p][k], oldl[p][k]) * (1.0f / kScaleA);
+                    const float oo = v[k] * (1.0f / (kScaleA * kScaleA)), ok = o[k] * (1.0f / kScaleA);
                     const bool diag = gi == gj + k;
-                    const float aij = diag ? di[p] : o;
-                    const float a2 = oo + (diag ? di[p] * di[p] : (di[p] + dj[k]) * o);
+                    const float aij = diag ? dg : ok;
+                    const float a2 = oo + (diag ? dg * dg : (dg + dj[k]) * ok);
                     const float x = st.b * aij + st.c * a2;
                     if (diag)
                         db[gi] = x;
@@ -724,34 +770,32 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
                 }
                 *reinterpret_cast<half8 *>(b.bo + ao + (int64_t)gi * b.mp + gj) = h8[p];
             } else {
-                const float own = st.a + di[p];
-                half8 l8;
+                const float own = st.a + di[set][p];
+                float x[8];
+                join8(oldh[set][p], oldl[set][p], x);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float x = own * join_half(oldh[p][k], oldl[p][k]) + v[k] * (1.0f / kScaleB);
-                    if constexpr (MODE == kModeX) {
-                        _Float16 h, l;
-                        split_half(x, h, l);
-                        h8[p][k] = h;
-                        l8[k] = l;
-                    } else {
-                        h8[p][k] = __builtin_bit_cast(_Float16, (__bf16)(x * st.out_scale));
-                    }
-                }
+                for (int k = 0; k < 8; ++k)
+                    x[k] = fmaf(own, x[k], v[k] * (1.0f / kScaleB));
                 if constexpr (MODE == kModeX) {
+                    split8(x, h8[p], low);
                     const int64_t at = xo + (int64_t)gi * b.np + gj;
                     *reinterpret_cast<half8 *>(b.xh[st.cur ^ 1] + at) = h8[p];
-                    *reinterpret_cast<half8 *>(b.xl + at) = l8;
-                } else if (!turned && gi < ov.m) {
-                    typedef _Float16 Out8 __attribute__((ext_vector_type(8), aligned(2)));
-                    _Float16 *o = reinterpret_cast<_Float16 *>(out) + e * ov.se + (int64_t)gi * ov.si;
-                    if (ov.sj == 1 && gj + 8 <= ov.n) {
-                        *reinterpret_cast<Out8 *>(o + gj) = h8[p];
-                    } else {
+                    *reinterpret_cast<uint2 *>(b.xl + at) = low;
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (gj + k < ov.n)
-                                o[(int64_t)(gj + k) * ov.sj] = h8[p][k];
+                    for (int k = 0; k < 8; ++k)
+                        h8[p][k] = __builtin_bit_cast(_Float16, (__bf16)(x[k] * st.out_scale));
+                    if (!turned && gi < ov.m) {
+                        typedef _Float16 Out8 __attribute__((ext_vector_type(8), aligned(2)));
+                        _Float16 *o = reinterpret_cast<_Float16 *>(out) + e * ov.se + (int64_t)gi * ov.si;
+                        if (ov.sj == 1 && gj + 8 <= ov.n) {
+                            *reinterpret_cast<Out8 *>(o + gj) = h8[p];
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (gj + k < ov.n)
+                                    o[(int64_t)(gj + k) * ov.sj] = h8[p][k];
+                        }
                     }
                 }
             }
@@ -766,15 +810,16 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
         }
         __builtin_amdgcn_wave_barrier();
         // lane l reads column l % 16 of rows 8 (l / 16) + 0..7 of a block of 32
+        const uint32_t turn0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)turn;
 #pragma unroll
         for (int i = 0; i < RC; i += 32)
 #pragma unroll
             for (int j = 0; j < FQ; ++j) {
                 const int r = i + 8 * fk + (fr >> 2), c = (fr & 3) * 4;
-                const half4 a = read_transposed(turn + r * WJ + (j ^ tswap(r)) * 16 + c);
-                const half4 h = read_transposed(turn + (r + 4) * WJ + (j ^ tswap(r + 4)) * 16 + c);
+                const half4 a = read_transposed(turn0 + (r * WJ + (j ^ tswap(r)) * 16 + c) * 2);
+                const half4 h = read_transposed(turn0 + ((r + 4) * WJ + (j ^ tswap(r + 4)) * 16 + c) * 2);
                 const half8 w = {a[0], a[1], a[2], a[3], h[0], h[1], h[2], h[3]};
-                const int gi = wi0 + ic + i + 8 * fk, gj = wj0 + 16 * j + fr;
+                const int gi = wi0 + ic + i + 8 * fk, gj = wj0 + 16 * j + fr;  // of this lane's column
                 if constexpr (SYM) {
                     _Float16 *o = (MODE == kModeA ? b.oh : b.bo) + ao + (int64_t)gj * b.mp + gi;
                     *reinterpret_cast<half8 *>(o) = w;
@@ -822,7 +867,9 @@ __global__ __launch_bounds__(256) void muon_copy_kernel(MuonBuffers b, float mul
     if (i >= ov.m || j >= ov.n)
         return;
     const int64_t at = (int64_t)e * b.mp * b.np + (int64_t)i * b.np + j;
-    out[e * ov.se + i * ov.si + j * ov.sj] = __builtin_bit_cast(uint16_t, (__bf16)(join_half(b.xh[0][at], b.xl[at]) * mul));
+    const float low = __builtin_amdgcn_cvt_f32_fp8((int)b.xl[at], 0);
+    out[e * ov.se + i * ov.si + j * ov.sj] =
+        __builtin_bit_cast(uint16_t, (__bf16)(fmaf(low, 1.0f / kLow, (float)b.xh[0][at]) * mul));
 }
 
 }  // namespace mxq
