@@ -508,39 +508,38 @@ __device__ __forceinline__ void phase_end()
 //
 // Two stages in LDS, but a stage's parts are loaded as soon as the part that
 // they overwrite has been read by both groups (a read phase ends with its
-// reads returned), two 16-byte loads per thread and phase, so that the loads
-// never queue up and every part has four to six phases (about 500 cycles
-// each) to arrive.  With group 0's phases of stage t:
-//   ra(t)  Q, quarter 0 of t + 1: the last third     (first read in ra(t + 1))
-//   ma(t)  quarters 1 and 3 of t + 1                 (first read in rb(t + 1))
-//   rb(t)  Q, quarter 0 and 2 of t + 2: first third
-//   mb(t)  the second third
-// The loads of a wave return in order: at the end of mb(t) all of Q and
-// quarters 0, 2 of t + 1 have landed when at most the 6 loads issued since are
-// pending; at the end of ma(t) quarters 1, 3 of t when at most 8 are.  (A tile
-// of 128 columns has two loads of Q, none in the second third, and 4 and 6.)
+// reads returned), so every part has five phases (about 500 cycles each) to
+// arrive.  Loads are issued in the read phases alone, after the LDS reads: in
+// front of a phase's MFMAs they held those up.  In either group's phases of
+// stage t:
+//   ra(t)  quarters 1 and 3 of t + 1      (first read in rb(t + 1))
+//   rb(t)  Q, quarters 0 and 2 of t + 2   (first read in ra(t + 2))
+// The loads of a wave return in order: at the end of group 0's mb(t) the parts
+// for ra(t + 1) have landed when only the 8 loads issued since are pending
+// (2 of t + 1 and 6 of t + 2), at the end of its ma(t) those for rb(t) when
+// again 8 are.  (A tile of 128 columns has two loads of Q, and 6 pending.)
 template <typename TILE, bool QT>
 struct MuonAlternating {
     static_assert(TILE::BK == 64 && TILE::NST == 2 && TILE::WM == 2 && TILE::WN == 4 && TILE::TM == 256,
                   "loads 0-3 are the quarters, the rest Q");
     static constexpr int H = TILE::FP / 2;
-    static constexpr int SECOND = TILE::LOADS - 6;  // loads of the second third
+    static constexpr int FIRST = TILE::LOADS - 2;  // loads for ra
     const MuonStages<TILE, QT> &st;
     half8 p0[H], p1[H], q0[TILE::FQ], q1[TILE::FQ];
 
-    __device__ __forceinline__ void load2(int u0, int u1, int kt) const
+    __device__ __forceinline__ void load_a(int kt) const
     {
-        st.load_one(kt & 1, u0, kt);
-        st.load_one(kt & 1, u1, kt);
+#pragma unroll
+        for (int u = 4; u < TILE::LOADS; ++u)
+            st.load_one(kt & 1, u, kt);
+        st.load_one(kt & 1, 0, kt);
+        st.load_one(kt & 1, 2, kt);
     }
-    __device__ __forceinline__ void load_first(int kt) const { load2(4, 5, kt); }
-    __device__ __forceinline__ void load_second(int kt) const
+    __device__ __forceinline__ void load_b(int kt) const
     {
-        if constexpr (SECOND == 2)
-            load2(6, 7, kt);
+        st.load_one(kt & 1, 1, kt);
+        st.load_one(kt & 1, 3, kt);
     }
-    __device__ __forceinline__ void load_third(int kt) const { load2(0, 2, kt); }
-    __device__ __forceinline__ void load_rest(int kt) const { load2(1, 3, kt); }
 
     __device__ __forceinline__ void read_a(int s)
     {
@@ -567,46 +566,28 @@ struct MuonAlternating {
     template <bool LATER, int MORE>
     __device__ __forceinline__ void stage(int kt, float4v (&acc)[TILE::FP][TILE::FQ])
     {
-        constexpr int kQuarters = MORE >= 1 ? 6 + SECOND : 0;
-        constexpr int kNext = MORE >= 2 ? 4 + SECOND : MORE == 1 ? 2 : -1;
+        constexpr int kB = MORE >= 1 ? 2 + FIRST : 0;                         // pending when rb may begin
+        constexpr int kNext = MORE >= 2 ? 2 + FIRST : MORE == 1 ? 2 : -1;     // when the next ra may
         const int s = kt & 1;
-        if constexpr (!LATER) {
-            read_a(s);
-            if (MORE >= 1) load_third(kt + 1);
-            phase_end<-1>();
-            if (MORE >= 1) load_rest(kt + 1);
-            products<0>(acc);
-            phase_end<kQuarters>();
-            read_b(s);
-            if (MORE >= 2) load_first(kt + 2);
-            phase_end<-1>();
-            if (MORE >= 2) load_second(kt + 2);
-            products<H>(acc);
-            phase_end<kNext>();
-        } else {
-            read_a(s);
-            if (MORE >= 1) load_rest(kt + 1);
-            phase_end<kQuarters>();
-            if (MORE >= 2) load_first(kt + 2);
-            products<0>(acc);
-            phase_end<-1>();
-            read_b(s);
-            if (MORE >= 2) load_second(kt + 2);
-            phase_end<kNext>();
-            if (MORE >= 2) load_third(kt + 2);
-            products<H>(acc);
-            phase_end<-1>();
-        }
+        read_a(s);
+        if (MORE >= 1)
+            load_b(kt + 1);
+        phase_end<LATER ? kB : -1>();
+        products<0>(acc);
+        phase_end<LATER ? -1 : kB>();
+        read_b(s);
+        if (MORE >= 2)
+            load_a(kt + 2);
+        phase_end<LATER ? kNext : -1>();
+        products<H>(acc);
+        phase_end<LATER ? -1 : kNext>();
     }
 
     template <bool LATER>
     __device__ __forceinline__ void run_group(int end, float4v (&acc)[TILE::FP][TILE::FQ])
     {
-        if (LATER) {
-            if (end > 1)
-                load_third(1);
+        if (LATER)
             phase_end<-1>();
-        }
         int kt = 0;
         for (; kt + 2 < end; ++kt)
             stage<LATER, 2>(kt, acc);
@@ -623,9 +604,8 @@ struct MuonAlternating {
     {
         st.load(0, 0);
         if (end > 1) {
-            load_first(1);
-            load_second(1);
-            phase_end<2 + SECOND>();
+            load_a(1);
+            phase_end<FIRST>();
         } else {
             phase_end<0>();
         }
