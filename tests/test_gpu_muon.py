@@ -156,6 +156,15 @@ def test_workspace_streams_and_repeats():
         mxq.muon_orthogonalize(g, workspace=ws[:-16])
 
 
+def test_more_than_2_31_elements():
+    g = update(1, 8192, 5120, torch.bfloat16, 12, "gauss").to(DEV)
+    want = mxq.muon_orthogonalize(g, steps=1)
+    out = mxq.muon_orthogonalize(g.expand(53, 8192, 5120), steps=1)
+    assert out.numel() > 2 ** 31
+    for e in (0, 1, 25, 52):
+        assert torch.equal(out[e], want[0])
+
+
 def test_empty():
     for shape in ((0, 5, 5), (2, 0, 5), (2, 5, 0)):
         assert mxq.muon_orthogonalize(torch.empty(shape, device=DEV)).shape == shape
