@@ -80,6 +80,13 @@ void by_experts(int experts, F &&f)
 #undef MXQ_CONFIG
 }
 
+// runs * experts up to which one kernel does the scan and the placement: a
+// launch less against every workgroup reading all counts.  On the GPU, whole
+// call: 2048 counts (16384 tokens, 8 experts) 10.3 against 13.4 us, 3965 16.3
+// against 17.5, 4096 21.7 against 21.8, 8192 17.6 against 16.2, 16384 28.3
+// against 19.0.
+constexpr int64_t kFinishCounts = 4096;
+
 template <typename T>
 mxq_status run_route(const void *logits, int64_t sl, int tokens, int experts, const uint8_t *mask, int k,
                      int renorm, int align, int32_t *ids, float *weights, int32_t *rows, float *lse,
@@ -109,7 +116,12 @@ mxq_status run_route(const void *logits, int64_t sl, int tokens, int experts, co
             nruns <= 1 ? go(moe_route_kernel<T, L, V, false, THREADS, true>)
                        : go(moe_route_kernel<T, L, V, false, THREADS, false>);
     });
-    if (nruns > 1) {
+    if (nruns > 1 && (int64_t)nruns * experts <= kFinishCounts) {
+        const int parts = std::max(1, kPlaceThreads / experts);
+        moe_finish_kernel<<<dim3((unsigned)(nruns + 1)), dim3(kPlaceThreads),
+                            (size_t)parts * experts * 8 + (size_t)experts * 8, st>>>(
+            tokens, experts, k, align, run, nruns, ids, rows, ws, out);
+    } else if (nruns > 1) {
         moe_scan_kernel<<<dim3((unsigned)((experts + kScanExperts - 1) / kScanExperts)), dim3(kScanThreads), 0, st>>>(
             experts, nruns, ws, out);
         moe_place_kernel<<<dim3((unsigned)(nruns + 1)), dim3(kPlaceThreads), (size_t)experts * 4, st>>>(

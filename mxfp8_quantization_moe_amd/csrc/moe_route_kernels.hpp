@@ -588,6 +588,82 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(int tokens, in
     }
 }
 
+// The second and third kernel in one, for few runs and experts: every
+// workgroup adds up all the runs' counts itself, each expert by several
+// threads (integer sums, in any order).
+__global__ __launch_bounds__(kPlaceThreads) void moe_finish_kernel(int tokens, int experts, int k, int align, int run,
+                                                                   int nruns, const int32_t *__restrict__ ids,
+                                                                   int32_t *__restrict__ rows, RouteWorkspace ws,
+                                                                   RouteResults out)
+{
+    extern __shared__ uint64_t lds[];
+    const int tid = threadIdx.x, r = blockIdx.x;
+    const bool final = r == nruns;
+    const int parts = max(1, kPlaceThreads / experts);
+    double *qsum = reinterpret_cast<double *>(lds);                      // [parts][experts]
+    int32_t *total = reinterpret_cast<int32_t *>(qsum + parts * experts);  // [experts] counts, then starts
+    int32_t *before = total + experts;                                   // [experts] in earlier runs
+    for (int e = tid; e < 2 * experts; e += kPlaceThreads)
+        total[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < parts * experts; i += kPlaceThreads) {
+        const int e = i % experts, part = i / experts;
+        int all = 0, prior = 0;
+        double p = 0.0;
+#pragma unroll 8
+        for (int q = part; q < nruns; q += parts) {
+            const int64_t at = (int64_t)q * experts + e;
+            const int c = ws.counts[at];
+            all += c;
+            prior += q < r ? c : 0;
+            if (final)
+                p += (double)ws.probs[at];
+        }
+        atomicAdd(&total[e], all);
+        atomicAdd(&before[e], prior);
+        if (final)
+            qsum[i] = p;
+    }
+    __syncthreads();
+    if (final) {
+        __shared__ double part[kPlaceThreads / 64];
+        double z = 0.0, n = 0.0, b = 0.0;
+        for (int i = tid; i < nruns; i += kPlaceThreads) {
+            z += (double)ws.z[i];
+            n += (double)ws.live[i];
+        }
+        z = block_sum<kPlaceThreads>(part, z);
+        n = block_sum<kPlaceThreads>(part, n);
+        const double inv = n > 0.0 ? 1.0 / n : 0.0;
+        for (int e = tid; e < experts; e += kPlaceThreads) {
+            double p = 0.0;
+            for (int i = 0; i < parts; ++i)
+                p += qsum[i * experts + e];
+            p *= inv;
+            out.counts[e] = total[e];
+            out.mean_prob[e] = (float)p;
+            b += (double)total[e] * p;
+        }
+        b = block_sum<kPlaceThreads>(part, b);
+        if (tid == 0) {
+            out.losses[0] = (float)(b * (double)experts * inv / (double)k);
+            out.losses[1] = (float)(z * inv);
+            out.live[0] = (int)n;
+        }
+    }
+    if (tid < 64)
+        group_ends(total, total, final ? out.offs : nullptr, experts, align);
+    __syncthreads();
+    if (final)
+        return;
+    const int64_t first = (int64_t)r * run * k, last = min((int64_t)(r + 1) * run, (int64_t)tokens) * k;
+    for (int64_t i = first + tid; i < last; i += kPlaceThreads) {
+        const int e = ids[i];
+        if (e >= 0)
+            rows[i] += total[e] + before[e];
+    }
+}
+
 // dl_te = p_te (g_te - sum_e' p_te' g_te') + 2 g_z lse_t p_te / n with
 // g_te = g_b E c_e / (n^2 k) + [e = ids_tj] q_tj, where q is the gradient of
 // the selected probabilities (through the renormalisation when there is one).

@@ -62,24 +62,26 @@ def _run(t, stream, call):
 def _dtype(t, ndim: int, name: str) -> int:
     torch = _torch()
     if t.dim() == ndim and t.is_cuda:
-        if t.dtype == torch.bfloat16:
+        dtype = t.dtype
+        if dtype is torch.bfloat16:
             return MXQ_BF16
-        if t.dtype == torch.float32:
+        if dtype is torch.float32:
             return MXQ_F32
     raise TypeError(f"{name} must be a {ndim}-D bfloat16 or float32 CUDA tensor, got {t.dtype} "
                     f"{tuple(t.shape)} on {t.device}")
 
 
 def _same(t, like, shape, name: str) -> None:
-    if t.dtype != like.dtype or t.device != like.device or tuple(t.shape) != tuple(shape):
+    if t.dtype is not like.dtype or t.shape != shape or t.device != like.device:
         raise TypeError(f"{name} must be a {like.dtype} tensor of shape {tuple(shape)} on {like.device}, got "
                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _plain(t, dtype, shape, device, name: str) -> None:
-    if t is None or t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}"
-        raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {got}")
+    if t is not None and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}"
+    raise TypeError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {got}")
 
 
 def _unit(t):
@@ -175,12 +177,13 @@ def moe_route_backward(logits, route: MoeRoute, grad_weights=None, grad_losses=N
 
 
 def _plan(route, tokens: int, dev):
-    torch = _torch()
-    k = route.rows.shape[-1] if route.rows is not None and route.rows.dim() == 2 else 0
-    _plain(route.rows, torch.int32, (tokens, k), dev, "route.rows")
-    E = route.offs.numel()
-    _plain(route.offs, torch.int32, (E,), dev, "route.offs")
-    _plain(route.counts, torch.int32, (E,), dev, "route.counts")
+    i32 = _torch().int32
+    rows, offs = route.rows, route.offs
+    k = rows.shape[-1] if rows is not None and rows.dim() == 2 else 0
+    _plain(rows, i32, (tokens, k), dev, "route.rows")
+    E = offs.numel() if offs is not None else 0
+    _plain(offs, i32, (E,), dev, "route.offs")
+    _plain(route.counts, i32, (E,), dev, "route.counts")
     return k, E
 
 
@@ -192,11 +195,12 @@ def moe_dispatch(x, route: MoeRoute, *, stream=None):
     torch = _torch()
     dt = _dtype(x, 2, "x")
     T, W = x.shape
-    k, E = _plan(route, T, x.device)
+    dev = x.device
+    k, E = _plan(route, T, dev)
     cap = moe_row_capacity(T, k, E, route.align)
 
     def call(st):
-        out = torch.empty((cap, W), dtype=x.dtype, device=x.device)
+        out = torch.empty((cap, W), dtype=x.dtype, device=dev)
         code = mxq_moe_dispatch(x.data_ptr(), dt, T, W, x.stride(0), x.stride(1), route.rows.data_ptr(), k,
                                 route.counts.data_ptr(), route.offs.data_ptr(), E, out.data_ptr(), cap, W, 1, st)
         _check(code, "mxq_moe_dispatch")
@@ -209,15 +213,16 @@ def _combine(yg, route, weights, residual, stream, name):
     torch = _torch()
     dt = _dtype(yg, 2, name)
     cap, W = yg.shape
+    dev = yg.device
     T = route.rows.shape[0] if route.rows is not None else 0
-    k, _ = _plan(route, T, yg.device)
+    k, _ = _plan(route, T, dev)
     if weights is not None:
-        _plain(weights, torch.float32, (T, k), yg.device, "route.weights")
+        _plain(weights, torch.float32, (T, k), dev, "route.weights")
     if residual is not None:
         _same(residual, yg, (T, W), "residual")
 
     def call(st):
-        y = torch.empty((T, W), dtype=yg.dtype, device=yg.device)
+        y = torch.empty((T, W), dtype=yg.dtype, device=dev)
         code = mxq_moe_combine(
             yg.data_ptr(), dt, cap, W, yg.stride(0), yg.stride(1), route.rows.data_ptr(),
             0 if weights is None else weights.data_ptr(), k, 0 if residual is None else residual.data_ptr(),
