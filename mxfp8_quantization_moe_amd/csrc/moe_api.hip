@@ -140,7 +140,7 @@ mxq_status run_route_backward(const void *logits, int64_t sl, int tokens, int ex
         constexpr int L = decltype(l)::value, V = decltype(v)::value;
         const int per = 256 / L;
         const int64_t blocks = std::min<int64_t>(((int64_t)tokens + per - 1) / per, 1 << 20);
-        moe_route_backward_kernel<T, L, V><<<dim3((unsigned)blocks), dim3(256), (size_t)256 * V * 4, st>>>(
+        moe_route_backward_kernel<T, L, V><<<dim3((unsigned)blocks), dim3(256), (size_t)256 * route_row_step(V) * 4, st>>>(
             reinterpret_cast<const T *>(logits), sl, tokens, experts, k, renorm, ids, weights, lse, counts, live,
             gw, gl, reinterpret_cast<T *>(dl), sd);
     });

@@ -664,6 +664,9 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_finish_kernel(int tokens, i
     }
 }
 
+// words from one lane's entries to the next lane's in a row of LDS
+constexpr int route_row_step(int v) { return v > 4 && v <= 16 ? v + 4 : v; }
+
 // dl_te = p_te (g_te - sum_e' p_te' g_te') + 2 g_z lse_t p_te / n with
 // g_te = g_b E c_e / (n^2 k) + [e = ids_tj] q_tj, where q is the gradient of
 // the selected probabilities (through the renormalisation when there is one).
@@ -680,11 +683,14 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(
     extern __shared__ uint64_t lds[];
     const int tid = threadIdx.x, sub = tid % L, e0 = sub * V;
     const bool whole = experts % V == 0;
-    // this token's row: L * V entries, V of them per lane, in pieces of 4
-    float *row = reinterpret_cast<float *>(lds) + tid / L * (L * V);
+    // this token's row, V entries per lane; 4 words between lanes' entries
+    // spread the 16-byte reads of 16 lanes over all banks
+    constexpr int STEP = route_row_step(V);
+    float *row = reinterpret_cast<float *>(lds) + tid / L * (L * STEP), *mine = row + sub * STEP;
+    auto entry = [&](int e) -> float & { return row[e / V * STEP + e % V]; };
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        row[e0 + i] = 0.0f;
+        mine[i] = 0.0f;
     const float n = (float)max(live ? live[0] : 1, 1);
     const float gb = gl ? gl[0] * (float)experts / (n * (float)k) / n : 0.0f;
     const float gz = gl ? 2.0f * gl[1] / n : 0.0f;
@@ -723,7 +729,7 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(
             for (int j = sub; j < k; j += L) {
                 const int e = ids[t * k + j];
                 if (e >= 0 && e < experts)
-                    row[e] = (gw[t * k + j] - wg) * inv;
+                    entry(e) = (gw[t * k + j] - wg) * inv;
             }
             // lanes of one wave: LDS runs its instructions in order
             __builtin_amdgcn_wave_barrier();
@@ -731,7 +737,7 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(
         float p[V], g[V], dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            g[i] = bal[i] + (gw ? row[e0 + i] : 0.0f);
+            g[i] = bal[i] + (gw ? mine[i] : 0.0f);
             p[i] = __expf(v[i] - lse);  // 0 for -inf; a dead token's is not used
             dot = fmaf(p[i], g[i], dot);
         }
@@ -741,7 +747,7 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(
             for (int j = sub; j < k; j += L) {
                 const int e = ids[t * k + j];
                 if (e >= 0 && e < experts)
-                    row[e] = 0.0f;
+                    entry(e) = 0.0f;
             }
             __builtin_amdgcn_wave_barrier();
         }
