@@ -242,24 +242,6 @@ __device__ __forceinline__ void group_ends(const int32_t *count, int32_t *start,
     }
 }
 
-// sum over the workgroup's N threads in a fixed order; part: N / 64 entries
-template <int N>
-__device__ __forceinline__ double block_sum(double *part, double v)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-        v += __shfl_xor(v, m, 64);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int w = 0; w < N / 64; ++w)
-        s += part[w];
-    return s;
-}
-
 // One run of tokens per workgroup.  L lanes per token, V experts per lane.
 // FEW: at most 8 slots, so only the first 8 of a lane's sorted keys can be
 // taken.  ONE: the only run.

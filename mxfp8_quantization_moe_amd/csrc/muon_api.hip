@@ -94,7 +94,7 @@ void launch_steps(MuonBuffers &b, MuonStep st, int steps, int64_t count, uint16_
 }
 
 template <typename T>
-void launch_load(const void *g, const MuonView &gv, const MuonBuffers &b, int count, float eps, hipStream_t s)
+void launch_load(const void *g, const MuonView &gv, MuonBuffers &b, int count, float eps, hipStream_t s)
 {
     const T *p = reinterpret_cast<const T *>(g);
     // as rows along the unit stride; one row when they follow one another
@@ -104,7 +104,9 @@ void launch_load(const void *g, const MuonView &gv, const MuonBuffers &b, int co
         inner *= outer;
         outer = 1;
     }
-    muon_norm_kernel<T><<<dim3(kNormParts, (unsigned)count), dim3(256), 0, s>>>(p, gv.se, inner, outer, so, b.part);
+    const int64_t span = kNormThreads * kNormLoads * Piece<T>::N;
+    b.parts = (int)std::min<int64_t>(kNormParts, outer * ((inner + span - 1) / span));
+    muon_norm_kernel<T><<<dim3((unsigned)b.parts, (unsigned)count), dim3(kNormThreads), 0, s>>>(p, gv.se, inner, outer, so, b.part);
     muon_load_kernel<T><<<dim3((unsigned)(b.np / 64), (unsigned)(b.mp / 64), (unsigned)count), dim3(256), 0, s>>>(
         p, gv, b, eps);
 }

@@ -39,6 +39,7 @@
 
 #include "moe_rows_kernels.hpp"
 #include "mxq_device.hpp"
+#include "wave_ops.hpp"
 
 namespace mxq {
 
@@ -51,7 +52,8 @@ constexpr float kScaleA = 2048.0f;   // |o| <= 1.7; room to 32
 constexpr float kScaleB = 2048.0f;   // |b| <= 3; room to 32
 constexpr float kLow = 64.0f;        // low parts are stored times this: half an f16 ulp of 10650 is 4, e4m3 ends at 448
 constexpr int kBand = 8;              // row tiles of a band (order of the tiles)
-constexpr int kNormParts = 256;      // partial sums of a matrix's squared norm
+constexpr int kNormParts = 512;      // at most this many partial sums of a matrix's squared norm
+constexpr int kNormThreads = 512, kNormLoads = 4;
 
 // Buffers of one call; matrix e's parts are `e` strides further.
 struct MuonBuffers {
@@ -62,6 +64,7 @@ struct MuonBuffers {
     float *d, *db;          // [mp] diagonals of A and B
     double *part;           // [kNormParts] partial sums of squares
     int mp, np;             // padded extents
+    int parts;              // partial sums in use
 };
 
 struct MuonView {           // x(i, j) = p[e * se + i * si + j * sj], i < m, j < n
@@ -101,23 +104,25 @@ __device__ __forceinline__ void join8(const half8 &hi, const uint2 &lo, float (&
 // Squares in fp64: no value of a finite bf16 or fp32 matrix over- or
 // underflows, and the rate does not matter beside the reads.  The matrix is
 // read along its unit-stride dim, 16 bytes per lane, as `outer` rows of
-// `inner` elements (one row when it is contiguous).
+// `inner` elements (one row when it is contiguous), by up to kNormParts
+// workgroups: one matrix alone needs two of 8 waves per CU with four loads
+// each on their way.
 template <typename T>
-__global__ __launch_bounds__(256) void muon_norm_kernel(const T *__restrict__ g, int64_t se, int64_t inner,
-                                                        int64_t outer, int64_t so, double *part)
+__global__ __launch_bounds__(kNormThreads) void muon_norm_kernel(const T *__restrict__ g, int64_t se, int64_t inner,
+                                                                 int64_t outer, int64_t so, double *part)
 {
     constexpr int N = Piece<T>::N;
-    __shared__ double sums[256];
+    __shared__ double sums[kNormThreads / 64];
     const int e = blockIdx.y;
     const T *p = g + e * se;
     double s = 0.0;
-    const int64_t span = 256 * N * 4, chunks = (inner + span - 1) / span;
-    for (int64_t item = blockIdx.x; item < outer * chunks; item += kNormParts) {
+    const int64_t span = kNormThreads * N * kNormLoads, chunks = (inner + span - 1) / span;
+    for (int64_t item = blockIdx.x; item < outer * chunks; item += gridDim.x) {
         const int64_t o = item / chunks, i0 = (item - o * chunks) * span + threadIdx.x * N;
         const T *row = p + o * so;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int64_t i = i0 + u * 256 * N;
+        for (int u = 0; u < kNormLoads; ++u) {
+            const int64_t i = i0 + u * kNormThreads * N;
             if (i + N <= inner) {
                 const Piece<T> v = ld_piece<T>(row + i);
 #pragma unroll
@@ -131,15 +136,9 @@ __global__ __launch_bounds__(256) void muon_norm_kernel(const T *__restrict__ g,
             }
         }
     }
-    sums[threadIdx.x] = s;
-    __syncthreads();
-    for (int m = 128; m > 0; m >>= 1) {
-        if ((int)threadIdx.x < m)
-            sums[threadIdx.x] += sums[threadIdx.x + m];
-        __syncthreads();
-    }
+    s = block_sum<kNormThreads>(sums, s);
     if (threadIdx.x == 0)
-        part[(int64_t)e * kNormParts + blockIdx.x] = sums[0];
+        part[(int64_t)e * kNormParts + blockIdx.x] = s;
 }
 
 // X = G / (norm + eps) into the padded buffers, 64 x 64 elements per
@@ -149,18 +148,15 @@ template <typename T>
 __global__ __launch_bounds__(256) void muon_load_kernel(const T *__restrict__ g, MuonView v, MuonBuffers b, float eps)
 {
     __shared__ float tile[64][65];
-    __shared__ double sums[256];
+    __shared__ double sums[4];
     const int tid = threadIdx.x;
     const int e = blockIdx.z, i0 = blockIdx.y * 64, j0 = blockIdx.x * 64;
-    sums[tid] = b.part[(int64_t)e * kNormParts + tid];
-    __syncthreads();
-    for (int m = 128; m > 0; m >>= 1) {
-        if (tid < m)
-            sums[tid] += sums[tid + m];
-        __syncthreads();
-    }
+    double square = 0.0;
+    for (int i = tid; i < b.parts; i += 256)
+        square += b.part[(int64_t)e * kNormParts + i];
+    square = block_sum<256>(sums, square);
     // in fp64: the reciprocal of a tiny norm overflows fp32
-    const double mul = (double)kScaleX / (sqrt(sums[0]) + (double)eps);
+    const double mul = (double)kScaleX / (sqrt(square) + (double)eps);
     const T *p = g + e * v.se;
     const bool inner_j = v.sj == 1;
     const int n_in = inner_j ? v.n - j0 : v.m - i0, n_out = inner_j ? v.m - i0 : v.n - j0;
