@@ -32,22 +32,28 @@ struct MuonPlan {
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 // Larger tiles do more per loaded byte, smaller ones fill the machine from
-// fewer rows and pad less.  Measured, the three products of one step: one
-// 512 x 512 matrix 16 / 19 / 64 us with small / medium / large tiles, one
-// 2048 x 2048 83 / 70 / 148 us, four of 1024 x 2048 70 / 64 / 115 us, four of
-// 2048 x 2048 233 / 204 / 174 us, one 4096 x 4096 437 / 374 / 280 us.  So a
-// size is taken from the number of tiles on that gives every CU one, unless
-// its padding costs more than its rate gains (1.33 times medium over large,
-// 1.17 small over medium).
+// fewer rows and pad less.  Measured, five steps in us with small / medium /
+// large tiles:
+//     1 x  512 x  512   103 /  121 /  211     4 x 1024 x 1024   255 /  239 /  327
+//     2 x 1024 x 1024   175 /  183 /  307     8 x  512 x 1024   164 /  158 /  254
+//     1 x 2048 x 2048   425 /  367 /  484    12 x  768 x 2048   534 /  487 /  507
+//     8 x 1024 x 1024   397 /  385 /  355    16 x  768 x 2048   686 /  632 /  554
+//     2 x 2048 x 2048   665 /  611 /  531     1 x 4096 x 4096  2292 / 2007 / 1359
+// Medium tiles win from half the workgroups on that the CUs hold; large ones
+// when B X has tiles for a good third of the CUs and the symmetric products,
+// which have about half as many, have enough of them for their length.  A size
+// whose padding costs more than its rate gains is not taken (1.33 times medium
+// over large, 1.12 small over medium).
 MuonPlan muon_plan(int64_t count, int64_t rows, int64_t cols)
 {
     const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
-    auto tiles = [&](int64_t t) { return count * ((m + t - 1) / t) * ((n + t - 1) / t); };
+    auto up = [](int64_t v, int64_t t) { return (v + t - 1) / t; };
     auto volume = [&](int64_t tm, int64_t tn) { return (double)round_up(m, tm) * round_up(m, tm) * round_up(n, tn); };
+    const int64_t tm = up(m, 256), tiles = count * tm * up(n, 256), lower = count * (tm * (tm + 1) / 2);
     MuonPlan p;
-    if (tiles(256) >= 192 && volume(256, 256) <= 1.33 * volume(128, 64))
+    if (tiles >= 96 && lower * m >= 65536 && volume(256, 256) <= 1.33 * volume(128, 64))
         p.tile = 2;
-    else if (tiles(128) >= 256 && volume(128, 64) <= 1.17 * volume(64, 64))
+    else if (count * up(m, 128) * up(n, 128) >= 256 && volume(128, 64) <= 1.12 * volume(64, 64))
         p.tile = 1;
     else
         p.tile = 0;

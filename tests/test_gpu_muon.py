@@ -75,6 +75,14 @@ def test_many_matrices_take_larger_tiles(shape):
     check(update(*shape, torch.bfloat16, 5))
 
 
+@pytest.mark.parametrize("shape", [(44, 250, 380), (48, 380, 250), (20, 760, 1000), (24, 1000, 765)])
+@pytest.mark.parametrize("columns", [False, True])
+def test_each_tile_in_both_orders(shape, columns):
+    # 128 x 64 tiles, then 256 x 256 alone and with a last round of halves
+    g = update(*shape, torch.bfloat16, 12)
+    check(g.transpose(1, 2).contiguous().transpose(1, 2) if columns else g)
+
+
 @pytest.mark.parametrize("kind", ["gauss", "lowrank", "rows"])
 @pytest.mark.parametrize("shape", [(1, 128, 512), (2, 400, 400), (1, 640, 96)])
 def test_spectra(kind, shape):
