@@ -48,8 +48,8 @@ constexpr int kRouteTile = 64;        // tokens that share one round of bit mask
 constexpr int kRouteMaxBlocks = 256;  // runs of tokens (workgroups of the first kernel)
 constexpr int kNoExpert = 0xffff;
 constexpr float kLog2E = 1.4426950408889634f;
-constexpr int kScanThreads = 1024;    // workgroups of the second kernel: 32 experts x 32 parts of the runs
-constexpr int kScanExperts = 32;
+constexpr int kScanThreads = 1024;    // workgroups of the second kernel: 16 experts x 64 parts of the runs
+constexpr int kScanExperts = 16;
 constexpr int kPlaceThreads = 256;    // workgroups of the third kernel
 
 // order-preserving bits of fp32 (-0 equals +0: adding zero makes it +0)
@@ -461,33 +461,40 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
     }
 }
 
-// 32 experts per workgroup, 32 threads each, every thread a contiguous part of
+// 16 experts per workgroup, 64 threads each, every thread a contiguous part of
 // the runs: counts of the runs before each run (in place), totals, mean
-// probabilities (64-bit sums in a fixed order).
+// probabilities (64-bit sums in a fixed order).  Bound by its chain of
+// latencies, so all of a thread's loads are issued first; with 32 experts per
+// workgroup the three kernels took 1 us more at 16384 x 256.
 __global__ __launch_bounds__(kScanThreads) void moe_scan_kernel(int experts, int nruns, RouteWorkspace ws,
                                                                 RouteResults out)
 {
     constexpr int PARTS = kScanThreads / kScanExperts, MOST = kRouteMaxBlocks / PARTS;
     __shared__ int32_t psum[PARTS][kScanExperts + 1];
     __shared__ double qsum[PARTS][kScanExperts + 1];
-    __shared__ int32_t alive;
+    __shared__ int32_t alive[kScanThreads / 64];
     const int tid = threadIdx.x, part = tid / kScanExperts, x = tid % kScanExperts;
     const int e = blockIdx.x * kScanExperts + x;
     const int per = (nruns + PARTS - 1) / PARTS, r0 = min(part * per, nruns), r1 = min(r0 + per, nruns);
-    if (tid == 0)
-        alive = 0;
-    __syncthreads();
-    if (tid < nruns)
-        atomicAdd(&alive, ws.live[tid]);
     int c[MOST], sum = 0;
+    float q[MOST];
     double p = 0.0;
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
         const bool on = r0 + i < r1 && e < experts;
         const int64_t at = (int64_t)(r0 + i) * experts + e;
         c[i] = on ? ws.counts[at] : 0;
-        p += on ? (double)ws.probs[at] : 0.0;
+        q[i] = on ? ws.probs[at] : 0.0f;
     }
+    int own = tid < nruns ? ws.live[tid] : 0;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1)
+        own += __shfl_xor(own, m, 64);
+    if (tid % 64 == 0)
+        alive[tid / 64] = own;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i)
+        p += (double)q[i];
 #pragma unroll
     for (int i = 0; i < MOST; ++i)
         sum += c[i];
@@ -509,7 +516,10 @@ __global__ __launch_bounds__(kScanThreads) void moe_scan_kernel(int experts, int
         psum[q][y] = upto - own;
         const int f = blockIdx.x * kScanExperts + y;
         if (q == PARTS - 1 && f < experts) {
-            const double inv = alive > 0 ? 1.0 / (double)alive : 0.0;
+            int n = 0;
+            for (int w = 0; w < (nruns + 63) / 64; ++w)
+                n += alive[w];
+            const double inv = n > 0 ? 1.0 / (double)n : 0.0;
             out.counts[f] = upto;
             out.mean_prob[f] = (float)(all * inv);
             ws.balance[f] = (double)upto * (all * inv);
