@@ -436,8 +436,9 @@ mxq_status mxq_moe_route_backward(const void *logits, int32_t dtype, int64_t tok
  * Token rows into their groups: xg[rows[t, j]] = x[t] for every slot.  Rows of
  * xg that no slot names (a group's padding, and everything past the last
  * group) become 0, so all `capacity` rows are written.
- * x (tokens, width), xg (capacity, width); rows, counts, offs from
- * mxq_moe_route; a row outside [0, capacity) is an empty slot.
+ * x (tokens, width), xg (capacity, width), width <= 2^30 (as below); rows,
+ * counts, offs from mxq_moe_route; a row outside [0, capacity) is an empty
+ * slot.
  */
 mxq_status mxq_moe_dispatch(const void *x, int32_t dtype, int64_t tokens, int64_t width,
                             int64_t sx_t, int64_t sx_c, const int32_t *rows, int32_t top_k,
@@ -478,8 +479,8 @@ mxq_status mxq_moe_combine_backward(const void *grad_y, int32_t dtype, int64_t t
  * (a, b, c) = (3.4445, -4.7750, 2.0315) takes singular values towards
  * [0.7, 1.2] in five steps.
  *
- * Numerics: products of f16 operands with fp32 sums; X is carried in 22 bits
- * and the diagonals of A and B in fp32.  Against 64 bits the result is off by
+ * Numerics: products of f16 operands with fp32 sums; X is carried as f16 and
+ * an e4m3 remainder (about 15 bits), the diagonals of A and B in fp32.  Against 64 bits the result is off by
  * the bf16 rounding (1.7e-3 of its 2-norm) and about 0.5e-3 more.  The powers
  * of two that keep the operands inside f16 leave room for iterates with
  * entries up to 8 and entries of A and B up to 32; coefficients that let X

@@ -27,6 +27,8 @@ int64_t row_capacity(int64_t tokens, int64_t k, int64_t experts, int64_t align)
     return slots + std::min(experts, slots) * (align - 1);
 }
 
+constexpr int64_t kMaxWidth = 1 << 30;  // element numbers of a row and a piece more fit 32 bits
+
 bool plan_ok(int64_t tokens, int32_t k, int32_t experts)
 {
     return tokens >= 0 && tokens <= INT32_MAX && experts >= 1 && experts <= MXQ_MAX_GROUPS && k >= 1 &&
@@ -304,7 +306,7 @@ mxq_status mxq_moe_dispatch(const void *x, int32_t dtype, int64_t tokens, int64_
                             int32_t num_experts, void *xg, int64_t capacity, int64_t sg_r, int64_t sg_c,
                             void *stream)
 {
-    if (!dtype_ok(dtype) || !plan_ok(tokens, top_k, num_experts) || width < 0 || width > INT32_MAX || capacity < 0 ||
+    if (!dtype_ok(dtype) || !plan_ok(tokens, top_k, num_experts) || width < 0 || width > kMaxWidth || capacity < 0 ||
         capacity > INT32_MAX || !counts || !offs || (tokens > 0 && !rows))
         return MXQ_ERR_INVALID_ARG;
     if (width > 1 && (sx_c != 1 || sg_c != 1))
@@ -334,7 +336,7 @@ mxq_status mxq_moe_combine(const void *yg, int32_t dtype, int64_t capacity, int6
                            int64_t sr_t, int64_t sr_c, void *y, int64_t sy_t, int64_t sy_c, int64_t tokens,
                            void *stream)
 {
-    if (!dtype_ok(dtype) || !plan_ok(tokens, top_k, MXQ_MAX_GROUPS) || width < 0 || width > INT32_MAX ||
+    if (!dtype_ok(dtype) || !plan_ok(tokens, top_k, MXQ_MAX_GROUPS) || width < 0 || width > kMaxWidth ||
         capacity < 0 || capacity > INT32_MAX || (tokens > 0 && !rows))
         return MXQ_ERR_INVALID_ARG;
     if (width > 1 && (sg_c != 1 || sy_c != 1 || (residual && sr_c != 1)))
@@ -374,7 +376,7 @@ mxq_status mxq_moe_combine_backward(const void *grad_y, int32_t dtype, int64_t t
                                     int32_t num_experts, int64_t capacity, void *grad_yg, int64_t sd_r, int64_t sd_c,
                                     float *grad_weights, void *stream)
 {
-    if (!dtype_ok(dtype) || !plan_ok(tokens, top_k, num_experts) || width < 0 || width > INT32_MAX || capacity < 0 ||
+    if (!dtype_ok(dtype) || !plan_ok(tokens, top_k, num_experts) || width < 0 || width > kMaxWidth || capacity < 0 ||
         capacity > INT32_MAX || !counts || !offs || (tokens > 0 && (!rows || !weights || !grad_weights)))
         return MXQ_ERR_INVALID_ARG;
     if (width > 1 && (sy_c != 1 || sg_c != 1 || sd_c != 1))

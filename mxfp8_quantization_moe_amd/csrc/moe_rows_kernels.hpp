@@ -96,8 +96,8 @@ __device__ __forceinline__ void zero_rows(int z, int nz, const int32_t *__restri
                                           const int32_t *__restrict__ offs, int experts, T *out, int64_t ld,
                                           int capacity, int width)
 {
-    auto clear = [&](int r) {
-        T *row = out + (int64_t)r * ld;
+    auto clear = [&](int64_t r) {
+        T *row = out + r * ld;
         if (width < Piece<T>::N) {
             for (int c = threadIdx.x; c < width; c += kRowsThreads)
                 row[c] = 0;
@@ -112,13 +112,13 @@ __device__ __forceinline__ void zero_rows(int z, int nz, const int32_t *__restri
             st_piece<T>(row + piece_start<T>(p, width), zero);
     };
     for (int e = z; e < experts; e += nz) {
-        const int start = e ? min(max(offs[e - 1], 0), capacity) : 0;
+        const int64_t start = e ? min(max(offs[e - 1], 0), capacity) : 0;
         const int end = min(max(offs[e], 0), capacity);
-        for (int64_t r = (int64_t)start + max(counts[e], 0); r < end; ++r)
-            clear((int)r);
+        for (int64_t r = start + max(counts[e], 0); r < end; ++r)
+            clear(r);
     }
     const int tail = min(max(offs[experts - 1], 0), capacity);
-    for (int r = tail + z; r < capacity; r += nz)
+    for (int64_t r = tail + z; r < capacity; r += nz)
         clear(r);
 }
 

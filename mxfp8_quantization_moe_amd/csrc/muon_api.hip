@@ -174,7 +174,7 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
         launch_load<float>(g, gv, buf, (int)count, eps, s);
     const MuonStep st = {a, b, c, scale / kScaleX, 0};
     if (steps == 0)
-        muon_copy_kernel<<<dim3((unsigned)((gv.n + 255) / 256), (unsigned)gv.m, (unsigned)count), dim3(256), 0, s>>>(
+        muon_copy_kernel<<<dim3((unsigned)gv.m, (unsigned)((gv.n + 255) / 256), (unsigned)count), dim3(256), 0, s>>>(
             buf, st.out_scale, out, ov);
     else if (p.tile == 2)
         launch_steps<TileLarge, TileHalf>(buf, st, steps, count, out, ov, s);

@@ -839,7 +839,7 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuff
 // With no steps the result is scale * X itself.
 __global__ __launch_bounds__(256) void muon_copy_kernel(MuonBuffers b, float mul, uint16_t *out, MuonView ov)
 {
-    const int e = blockIdx.z, i = blockIdx.y, j = blockIdx.x * 256 + threadIdx.x;
+    const int e = blockIdx.z, i = blockIdx.x, j = blockIdx.y * 256 + threadIdx.x;
     if (i >= ov.m || j >= ov.n)
         return;
     const int64_t at = (int64_t)e * b.mp * b.np + (int64_t)i * b.np + j;

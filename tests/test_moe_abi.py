@@ -99,3 +99,10 @@ def test_rows_refuse(lib):
     assert backward(sd=63) == 1 and backward(E=0) == 1
     assert backward(syc=2) == 2 and backward(sgc=2) == 2 and backward(sdc=2) == 2
     assert backward(T=0, cap=0) == 0
+
+
+def test_rows_refuse_widths_past_32_bits(lib):
+    for W in ((1 << 30) + 1, (1 << 31) - 1, 1 << 31):
+        assert lib.mxq_moe_dispatch(A, 0, 10, W, 0, 1, A, 2, A, A, 8, A, 20, W, 1, None) == 1
+        assert lib.mxq_moe_combine(A, 0, 20, W, W, 1, A, A, 2, 0, 0, 1, A, W, 1, 10, None) == 1
+        assert lib.mxq_moe_combine_backward(A, 0, 10, W, 0, 1, A, W, 1, A, A, 2, A, A, 8, 20, A, W, 1, A, None) == 1
