@@ -14,6 +14,9 @@
 //   P_e = 1/n sum_t p_te     balance = E sum_e c_e/(n k) P_e
 //   z = 1/n sum_t lse_t^2
 //
+// The GPU times beside the kernels are medians of a kernel trace on one MI355X;
+// an empty dependent kernel takes 2.3 us there and a large copy 4.9 TB/s.
+//
 // Three kernels.  The first gives each workgroup a run of tokens (at most
 // kRouteMaxBlocks runs): L lanes hold a token's logits, V consecutive ones per
 // lane, so the whole row stays in registers.  64 tokens at a time set their
@@ -246,6 +249,10 @@ __device__ __forceinline__ void group_ends(const int32_t *count, int32_t *start,
 // One run of tokens per workgroup.  L lanes per token, V experts per lane.
 // FEW: at most 8 slots, so only the first 8 of a lane's sorted keys can be
 // taken.  ONE: the only run.
+// 16384 tokens x 256 experts fp32, 8 slots: 19 us for 19 MB, bound by the
+// vector instructions of the selection (1060 per wave of 4 tokens; 640 with
+// bf16 logits' 32-bit keys); x 8 experts bf16, 2 slots: 4.4 us, latency; one
+// token of 256: 7.5 us, its chain of reductions.
 template <typename T, int L, int V, bool FEW, int THREADS, bool ONE>
 __global__ __launch_bounds__(THREADS) void moe_route_kernel(
     const T *__restrict__ logits, int64_t sl, int tokens, int experts, const uint8_t *__restrict__ mask, int k,
@@ -469,8 +476,8 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
 // 16 experts per workgroup, 64 threads each, every thread a contiguous part of
 // the runs: counts of the runs before each run (in place), totals, mean
 // probabilities (64-bit sums in a fixed order).  Bound by its chain of
-// latencies, so all of a thread's loads are issued first; with 32 experts per
-// workgroup the three kernels took 1 us more at 16384 x 256.
+// latencies, so all of a thread's loads are issued first: 5.1 us for 256 runs
+// of 256 experts; with 32 experts per workgroup 1 us more.
 __global__ __launch_bounds__(kScanThreads) void moe_scan_kernel(int experts, int nruns, RouteWorkspace ws,
                                                                 RouteResults out)
 {
@@ -541,7 +548,8 @@ __global__ __launch_bounds__(kScanThreads) void moe_scan_kernel(int experts, int
 }
 
 // A run per workgroup: its slots' ranks become rows.  The last workgroup
-// writes the group ends and the losses.
+// writes the group ends and the losses.  4.4 us for 131072 slots of 256
+// experts, latency (1.8 MB).
 __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(int tokens, int experts, int k, int align, int run,
                                                                   int nruns, const int32_t *__restrict__ ids,
                                                                   int32_t *__restrict__ rows, RouteWorkspace ws,
@@ -587,7 +595,8 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(int tokens, in
 
 // The second and third kernel in one, for few runs and experts: every
 // workgroup adds up all the runs' counts itself, each expert by several
-// threads (integer sums, in any order).
+// threads (integer sums, in any order).  6.5 us for 256 runs of 8 experts,
+// 8.0 for 65 of 61: latency, against two launches saved into one.
 __global__ __launch_bounds__(kPlaceThreads) void moe_finish_kernel(int tokens, int experts, int k, int align, int run,
                                                                    int nruns, const int32_t *__restrict__ ids,
                                                                    int32_t *__restrict__ rows, RouteWorkspace ws,
@@ -669,7 +678,9 @@ constexpr int route_row_step(int v) { return v > 4 && v <= 16 ? v + 4 : v; }
 // the selected probabilities (through the renormalisation when there is one).
 // A slot's part is worked out by one lane and reaches the lane that holds its
 // expert through a row of zeros in LDS (comparing every expert with every slot
-// took three times as long).
+// took three times as long).  16384 x 256 fp32: 13.7 us for 35 MB (2.6 TB/s);
+// 65536 x 256 bf16 21 us (3.3 TB/s): one pass over the memory, its few tokens
+// per wave bound by latency.
 template <typename T, int L, int V>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(
     const T *__restrict__ logits, int64_t sl, int tokens, int experts, int k, int renorm,
