@@ -39,7 +39,8 @@ int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 //     1 x 2048 x 2048   425 /  367 /  484    12 x  768 x 2048   534 /  487 /  507
 //     8 x 1024 x 1024   397 /  385 /  355    16 x  768 x 2048   686 /  632 /  554
 //     2 x 2048 x 2048   665 /  611 /  531     1 x 4096 x 4096  2292 / 2007 / 1359
-// Medium tiles win from half the workgroups on that the CUs hold; large ones
+//     3 x 1000 x  777   175 /  190 /  319     4 x  987 x  872   220 /  195 /  323
+// Medium tiles win from four workgroups on for five CUs (of 128 x 128); large ones
 // when B X has tiles for a good third of the CUs and the symmetric products,
 // which have about half as many, have enough of them for their length.  A size
 // whose padding costs more than its rate gains is not taken (1.33 times medium
@@ -53,7 +54,7 @@ MuonPlan muon_plan(int64_t count, int64_t rows, int64_t cols)
     MuonPlan p;
     if (tiles >= 96 && lower * m >= 65536 && volume(256, 256) <= 1.33 * volume(128, 64))
         p.tile = 2;
-    else if (count * up(m, 128) * up(n, 128) >= 256 && volume(128, 64) <= 1.12 * volume(64, 64))
+    else if (count * up(m, 128) * up(n, 128) >= 205 && volume(128, 64) <= 1.12 * volume(64, 64))
         p.tile = 1;
     else
         p.tile = 0;
@@ -86,12 +87,44 @@ void launch_product(const MuonBuffers &b, const MuonStep &st, int64_t count, uin
         b, st, out, ov, (int)(tiles - rest));
 }
 
-template <typename TILE, typename HALF>
-void launch_steps(MuonBuffers &b, MuonStep st, int steps, int64_t count, uint16_t *out, const MuonView &ov,
-                  hipStream_t s)
+// X X^T of a long matrix has few tiles with long sums: each sum is then taken
+// in up to 8 parts of at least 12 stages, as many as `at_once` workgroups of
+// the tile run at a time and as fit where the next X will be, and joined by a
+// kernel of its own.  Five steps, without / with: 1 x 64 x 8192 191 / 100 us,
+// 3 x 175 x 7481 232 / 155, 1 x 256 x 4096 155 / 117, 1 x 2048 x 8192 964 /
+// 900; a sum of less than 32 stages loses by the launch (17 x 126 x 1327 106 /
+// 122), and so do medium tiles past one per CU (2 x 1024 x 4096 363 / 370).
+template <typename TILE>
+int sum_splits(const MuonBuffers &b, int64_t count, int64_t at_once)
 {
+    const int64_t tm = b.mp / TILE::TM, tiles = count * TILE::SS * (tm * (tm + 1) / 2), stages = b.np / TILE::BK;
+    if (stages < 32)
+        return 1;
+    const int64_t room = b.np / (2 * b.mp);  // fp32 of mp x mp in f16 of mp x np
+    return (int)std::max<int64_t>(1, std::min({(int64_t)8, at_once / tiles, stages / 12, room}));
+}
+
+template <typename TILE>
+void launch_parts(const MuonBuffers &b, const MuonStep &st, int64_t count, hipStream_t s)
+{
+    const int64_t tm = b.mp / TILE::TM, tiles = count * TILE::SS * (tm * (tm + 1) / 2), t64 = b.mp / 64;
+    const int64_t whole = count * b.mp * b.mp;
+    const MuonView parts = {whole, 0, 0, 0, 0};
+    muon_product_kernel<kModePart, TILE, TILE><<<dim3((unsigned)(tiles * b.splits)), dim3(TILE::THREADS), 0, s>>>(
+        b, st, nullptr, parts, (int)tiles);
+    muon_join_kernel<<<dim3((unsigned)(t64 * (t64 + 1) / 2), (unsigned)count), dim3(256), 0, s>>>(b, st, whole);
+}
+
+template <typename TILE, typename HALF>
+void launch_steps(MuonBuffers &b, MuonStep st, int steps, int64_t count, int64_t at_once, uint16_t *out,
+                  const MuonView &ov, hipStream_t s)
+{
+    b.splits = sum_splits<TILE>(b, count, at_once);
     for (int k = 0; k < steps; ++k) {
-        launch_product<kModeA, TILE, HALF>(b, st, count, out, ov, s);
+        if (b.splits > 1)
+            launch_parts<TILE>(b, st, count, s);
+        else
+            launch_product<kModeA, TILE, HALF>(b, st, count, out, ov, s);
         launch_product<kModeB, TILE, HALF>(b, st, count, out, ov, s);
         if (k + 1 < steps)
             launch_product<kModeX, TILE, HALF>(b, st, count, out, ov, s);
@@ -179,11 +212,11 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
         muon_copy_kernel<<<dim3((unsigned)gv.m, (unsigned)((gv.n + 255) / 256), (unsigned)count), dim3(256), 0, s>>>(
             buf, st.out_scale, out, ov);
     else if (p.tile == 2)
-        launch_steps<TileLarge, TileHalf>(buf, st, steps, count, out, ov, s);
+        launch_steps<TileLarge, TileHalf>(buf, st, steps, count, kCUs, out, ov, s);
     else if (p.tile == 1)
-        launch_steps<TileMedium, TileMedium>(buf, st, steps, count, out, ov, s);
+        launch_steps<TileMedium, TileMedium>(buf, st, steps, count, kCUs, out, ov, s);
     else
-        launch_steps<TileSmall, TileSmall>(buf, st, steps, count, out, ov, s);
+        launch_steps<TileSmall, TileSmall>(buf, st, steps, count, 3 * kCUs, out, ov, s);
     return launch_status();
 }
 

@@ -7,6 +7,7 @@
 //
 // Three products per step.  A and A^2 are symmetric: only the tiles on and
 // below the diagonal are computed, each stored a second time mirrored.
+// The long sums of a long matrix's A are split over workgroups and joined.
 //
 // Numerics.  The products run on f16 MFMA with fp32 accumulators.  f16 keeps
 // 11 bits; X, A and B have magnitudes known from the iteration (|X|_2 <= 1.3
@@ -64,7 +65,9 @@ struct MuonBuffers {
     float *d, *db;          // [mp] diagonals of A and B
     double *part;           // [kNormParts] partial sums of squares
     int mp, np;             // padded extents
+    __device__ __forceinline__ float *sums(int cur) const { return reinterpret_cast<float *>(xh[cur ^ 1]); }
     int parts;              // partial sums in use
+    int splits;             // parts of X X^T's sum, 1: none
 };
 
 struct MuonView {           // x(i, j) = p[e * se + i * si + j * sj], i < m, j < n
@@ -251,7 +254,7 @@ __device__ __forceinline__ half8 read_lds(uint32_t a)
     return *(__attribute__((address_space(3))) const half8 *)(uintptr_t)a;
 }
 
-enum MuonMode { kModeA, kModeB, kModeX, kModeOut };
+enum MuonMode { kModeA, kModeB, kModeX, kModeOut, kModePart };
 
 struct MuonStep {
     float a, b, c, out_scale;
@@ -619,18 +622,28 @@ struct MuonAlternating {
 //   kModeB    P = Q = O (symmetric): off-diagonal B, diagonal db
 //   kModeX    P = B, Q = X: the next X in both parts
 //   kModeOut  the same, to the caller's output
+//   kModePart part `split` of kModeA's sum, as it is, in fp32 to where the
+//             next X will be (muon_join_kernel does the rest)
 template <int MODE, typename TILE>
 __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b, const MuonStep &st, uint16_t *out,
-                                             const MuonView &ov, int e, int i0, int j0, bool mirror)
+                                             const MuonView &ov, int e, int i0, int j0, bool mirror, int split)
 {
     constexpr int FP = TILE::FP, FQ = TILE::FQ;
-    constexpr bool SYM = MODE == kModeA || MODE == kModeB;
+    constexpr bool SYM = MODE == kModeA || MODE == kModeB || MODE == kModePart;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = wave / TILE::WN, wq = wave % TILE::WN;
     const int fr = threadIdx.x & 15, fk = (threadIdx.x & 63) >> 4;
     const int64_t xo = (int64_t)e * b.mp * b.np, ao = (int64_t)e * b.mp * b.mp;
-    const int K = MODE == kModeA ? b.np : b.mp;
-    const _Float16 *P = MODE == kModeA ? b.xh[st.cur] + xo : MODE == kModeB ? b.oh + ao : b.bo + ao;
+    constexpr bool XX = MODE == kModeA || MODE == kModePart;
+    const int K = XX ? b.np : b.mp;
+    int first = 0, last = K / TILE::BK;  // stages
+    if constexpr (MODE == kModePart) {
+        const int all = last;
+        first = split * all / b.splits;
+        last = (split + 1) * all / b.splits;
+    }
+    const _Float16 *P = XX ? b.xh[st.cur] + xo : MODE == kModeB ? b.oh + ao : b.bo + ao;
+    P += first * TILE::BK;
     const _Float16 *Q = SYM ? P + (int64_t)j0 * K : b.xh[st.cur] + xo + j0;
     MuonStages<TILE, !SYM> stages(lds, P + (int64_t)i0 * K, Q, K, b.np, wave, wp * FP * 16, wq * FQ * 16);
 
@@ -647,7 +660,7 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
     uint2 oldl[2][PASSES];
     float di[2][PASSES];
     auto load_old = [&](int ic, int set) {
-        if constexpr (MODE != kModeA) {
+        if constexpr (!XX) {
 #pragma unroll
             for (int p = 0; p < PASSES; ++p) {
                 const int gi = wi0 + ic + p * RPP + pr;
@@ -668,9 +681,9 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
         for (int j = 0; j < FQ; ++j)
             acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
     if constexpr (TILE::TM == 256)
-        MuonAlternating<TILE, !SYM>{stages}.run(K / TILE::BK, acc);
+        MuonAlternating<TILE, !SYM>{stages}.run(last - first, acc);
     else
-        run_pipeline<TILE, !SYM>(stages, K / TILE::BK, acc);
+        run_pipeline<TILE, !SYM>(stages, last - first, acc);
 
     // Results.  A lane holds row l % 16, columns 4 (l / 16) + 0..3 of each
     // fragment; through LDS (each wave in its own region, RC rows at a time)
@@ -678,7 +691,7 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
     // below is read and written in 16-byte pieces of whole 128-byte lines.
     // stored a second time (or only) transposed: the mirror of an off-diagonal
     // tile, and the output of a tall matrix
-    const bool turned = SYM ? mirror : MODE == kModeOut && ov.si == 1 && ov.sj != 1;
+    const bool turned = MODE == kModePart ? false : SYM ? mirror : MODE == kModeOut && ov.si == 1 && ov.sj != 1;
     float *wide = reinterpret_cast<float *>(lds) + wave * RC * WJ;
     _Float16 *turn = reinterpret_cast<_Float16 *>(wide);
     // chunk orders of the two uses of the region: 16-byte chunks of fp32 rows,
@@ -718,7 +731,12 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
                     v[4 * q + k] = x[k];
             }
             uint2 low;
-            if constexpr (MODE == kModeA) {
+            if constexpr (MODE == kModePart) {
+                float *o = b.sums(st.cur) + (int64_t)split * ov.se + ao + (int64_t)gi * b.mp + gj;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    reinterpret_cast<float4v *>(o)[q] = float4v{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            } else if constexpr (MODE == kModeA) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     v[k] *= 1.0f / (kScaleX * kScaleX);
@@ -779,7 +797,7 @@ __device__ __forceinline__ void muon_product(_Float16 *lds, const MuonBuffers &b
             }
         }
         __builtin_amdgcn_wave_barrier();
-        if (MODE == kModeX || !turned)
+        if (MODE == kModeX || MODE == kModePart || !turned)
             continue;
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
@@ -834,17 +852,90 @@ template <int MODE, typename TILE, typename HALF>
 __global__ __launch_bounds__(TILE::THREADS, 2) void muon_product_kernel(MuonBuffers b, MuonStep st, uint16_t *out,
                                                                      MuonView ov, int whole)
 {
-    constexpr bool SYM = MODE == kModeA || MODE == kModeB;
+    constexpr bool SYM = MODE == kModeA || MODE == kModeB || MODE == kModePart;
     __shared__ __attribute__((aligned(16))) _Float16 lds[TILE::NST * TILE::STAGE];
     int e, bi, bj;
-    if ((int)blockIdx.x < whole) {
+    if constexpr (MODE == kModePart) {
+        const int id = xcd_run(blockIdx.x, gridDim.x);
+        muon_tile<TILE, true>(id % whole, b.mp, b.np, e, bi, bj);
+        muon_product<MODE, TILE>(lds, b, st, out, ov, e, bi * TILE::TM, bj * TILE::TN, false, id / whole);
+    } else if ((int)blockIdx.x < whole) {
         muon_tile<TILE, SYM>(xcd_run(blockIdx.x, whole), b.mp, b.np, e, bi, bj);
-        muon_product<MODE, TILE>(lds, b, st, out, ov, e, bi * TILE::TM, bj * TILE::TN, bj < bi * TILE::SS);
+        muon_product<MODE, TILE>(lds, b, st, out, ov, e, bi * TILE::TM, bj * TILE::TN, bj < bi * TILE::SS, 0);
     } else if constexpr (!std::is_same<TILE, HALF>::value) {
         const int id = xcd_run(blockIdx.x - whole, gridDim.x - whole);
         muon_tile<TILE, SYM>(whole + (id >> 1), b.mp, b.np, e, bi, bj);
         muon_product<MODE, HALF>(lds, b, st, out, ov, e, bi * TILE::TM, bj * TILE::TN + (id & 1) * HALF::TN,
-                                 bj < bi * TILE::SS);
+                                 bj < bi * TILE::SS, 0);
+    }
+}
+
+// The parts of X X^T's sum, in order, to A: a 64 x 64 tile on or below the
+// diagonal per workgroup, 16 columns of a row per thread.  `whole`: elements
+// from part to part.  Bound by latency (a launch and the parts' reads).
+__global__ __launch_bounds__(256) void muon_join_kernel(MuonBuffers b, MuonStep st, int64_t whole)
+{
+    __shared__ __attribute__((aligned(16))) _Float16 tile[64][72];
+    __shared__ __attribute__((aligned(16))) uint8_t tail[64][72];
+    int bi = 0, t = blockIdx.x;
+    while (t > bi)
+        t -= ++bi;
+    const int bj = t, r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 16;
+    const int64_t ao = (int64_t)blockIdx.y * b.mp * b.mp;
+    const int gi = bi * 64 + r, gj = bj * 64 + c;
+    const int64_t at = ao + (int64_t)gi * b.mp + gj;
+    const float *p = b.sums(st.cur) + at;
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        v[k] = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < b.splits; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4v x = reinterpret_cast<const float4v *>(p + i * whole)[q];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[4 * q + k] += x[k];
+        }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float x = v[8 * h + k] * (1.0f / (kScaleX * kScaleX));
+            const bool diag = gi == gj + 8 * h + k;
+            if (diag)
+                b.d[(int64_t)blockIdx.y * b.mp + gi] = x;
+            w[k] = diag ? 0.0f : x * kScaleA;
+        }
+        half8 hi;
+        uint2 low;
+        split8(w, hi, low);
+        *reinterpret_cast<half8 *>(b.oh + at + 8 * h) = hi;
+        *reinterpret_cast<uint2 *>(b.ol + at + 8 * h) = low;
+        *reinterpret_cast<half8 *>(&tile[r][c + 8 * h]) = hi;
+        *reinterpret_cast<uint2 *>(&tail[r][c + 8 * h]) = low;
+    }
+    if (bi == bj)
+        return;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        half8 w;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            w[k] = tile[c + 8 * h + k][r];
+        const int64_t to = ao + (int64_t)(bj * 64 + r) * b.mp + bi * 64 + c + 8 * h;
+        *reinterpret_cast<half8 *>(b.oh + to) = w;
+        // the next product reads the low part of whole tiles on the diagonal
+        uint2 low = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            low.x |= (uint32_t)tail[c + 8 * h + k][r] << (8 * k);
+            low.y |= (uint32_t)tail[c + 8 * h + 4 + k][r] << (8 * k);
+        }
+        *reinterpret_cast<uint2 *>(b.ol + to) = low;
     }
 }
 

@@ -83,6 +83,17 @@ def test_each_tile_in_both_orders(shape, columns):
     check(g.transpose(1, 2).contiguous().transpose(1, 2) if columns else g)
 
 
+@pytest.mark.parametrize("shape", [(1, 64, 2048), (3, 175, 7481), (2, 5000, 130), (1, 300, 2300), (4, 200, 2100),
+                                   (1, 1, 8200), (9, 1024, 4100), (1, 1536, 6200), (1, 1000, 8100)])
+def test_long_matrices_split_their_sums(shape):
+    # in 2, 8, 6, 3, 2 and 8 parts; 256 x 256 tiles in 2; 128 x 64 in 1 and 3
+    g = update(*shape, torch.bfloat16, 13, "gauss" if min(shape[1:]) >= 1000 else "tokens")
+    check(g, bound=BOUND if min(shape[1:]) > 8 else 8e-3)
+    a = g.to(DEV)
+    out = mxq.muon_orthogonalize(a)
+    assert all(torch.equal(mxq.muon_orthogonalize(a), out) for _ in range(3))
+
+
 @pytest.mark.parametrize("kind", ["gauss", "lowrank", "rows"])
 @pytest.mark.parametrize("shape", [(1, 128, 512), (2, 400, 400), (1, 640, 96)])
 def test_spectra(kind, shape):
