@@ -86,7 +86,8 @@ def _plain(t, dtype, shape, device, name: str) -> None:
 
 def _unit(t):
     """A gradient as autograd may hand it over (an expanded scalar, a
-    transposed view): copied if its last dim has no unit stride."""
+    transposed view): copied if its last dim has no unit stride.  To be called
+    within _run, so that the copy is made on the call's stream."""
     return t if t.stride(-1) == 1 and min(t.stride()) >= 0 else t.contiguous()
 
 
@@ -209,7 +210,7 @@ def moe_dispatch(x, route: MoeRoute, *, stream=None):
     return _run(x, stream, call)
 
 
-def _combine(yg, route, weights, residual, stream, name):
+def _combine(yg, route, weights, residual, stream, name, any_layout=False):
     torch = _torch()
     dt = _dtype(yg, 2, name)
     cap, W = yg.shape
@@ -222,9 +223,10 @@ def _combine(yg, route, weights, residual, stream, name):
         _same(residual, yg, (T, W), "residual")
 
     def call(st):
+        src = _unit(yg) if any_layout else yg
         y = torch.empty((T, W), dtype=yg.dtype, device=dev)
         code = mxq_moe_combine(
-            yg.data_ptr(), dt, cap, W, yg.stride(0), yg.stride(1), route.rows.data_ptr(),
+            src.data_ptr(), dt, cap, W, src.stride(0), src.stride(1), route.rows.data_ptr(),
             0 if weights is None else weights.data_ptr(), k, 0 if residual is None else residual.data_ptr(),
             0 if residual is None else residual.stride(0), 1 if residual is None else residual.stride(1),
             y.data_ptr(), W, 1, T, st)
@@ -237,7 +239,7 @@ def _combine(yg, route, weights, residual, stream, name):
 def moe_dispatch_backward(grad_xg, route: MoeRoute, *, stream=None):
     """Gradient of ``moe_dispatch`` with respect to ``x``: the sum of each
     token's rows of ``grad_xg`` (capacity, width)."""
-    return _combine(_unit(grad_xg), route, None, None, stream, "grad_xg")
+    return _combine(grad_xg, route, None, None, stream, "grad_xg", any_layout=True)
 
 
 def moe_combine(yg, route: MoeRoute, *, residual=None, stream=None):

@@ -240,3 +240,20 @@ def test_refusals():
         mxq.moe_combine_backward(x, yg, r._replace(weights=None))
     with pytest.raises(TypeError):
         mxq.moe_combine_backward(x[:, :8], yg, r)
+
+
+def test_a_gradient_that_is_copied_first_is_copied_on_the_calls_stream():
+    # a transposed gradient gets its copy behind its producer, on the stream given
+    torch.manual_seed(5)
+    r = mxq.moe_route(torch.randn(500, 8, device=DEV), 2)
+    src = torch.randn(64, 1000, device=DEV)
+    want = mxq.moe_dispatch_backward(src.t().contiguous(), r)
+    grad = torch.zeros(64, 1000, device=DEV)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+        grad.copy_(src)
+    got = mxq.moe_dispatch_backward(grad.t(), r, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
