@@ -405,8 +405,10 @@ int64_t mxq_moe_route_workspace_bytes(int64_t tokens, int32_t num_experts, int32
  * workspace   mxq_moe_route_workspace_bytes bytes (none for up to 64 tokens),
  *             8-byte aligned, contents arbitrary before and after; too small
  *             -> MXQ_ERR_WORKSPACE.
- * A NaN logit is never taken and makes the token's probabilities, and the
- * losses, NaN.
+ * Finite logits of any size are in range, the type's lowest value in every
+ * place of a row included (its experts are then equal); z can be +inf where the
+ * sum of lse^2 passes fp32.  A NaN logit is never taken and makes the token's
+ * probabilities, and the losses, NaN; so does a logit of +inf, which is taken.
  */
 mxq_status mxq_moe_route(const void *logits, int32_t dtype, int64_t tokens, int32_t num_experts,
                          int64_t sl_t, int64_t sl_e, const uint8_t *token_mask, int32_t top_k,

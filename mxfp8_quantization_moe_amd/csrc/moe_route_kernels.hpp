@@ -303,13 +303,14 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
             top = lanes_max<L>(top);
             // fmax drops NaN: a row of -inf and NaN alone has no logit either
             live = live && top > -INFINITY;
-            // exp(v - top) as 2^(v log2 e - top log2 e), one rounding of the
-            // difference; the rounding of top log2 e is common to the row
-            const float ltop = top * kLog2E;
+            // exp(v - top), the difference first: that of two finite logits
+            // overflows to -inf alone, which is right, while top log2 e
+            // overflows for |top| past 2.36e38 (rows barred with the type's
+            // lowest value)
             float p[V], sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(fmaf(v[i], kLog2E, -ltop));
+                p[i] = __builtin_amdgcn_exp2f((v[i] - top) * kLog2E);
                 sum += p[i];
             }
             sum = lanes_sum<L>(sum);
@@ -366,7 +367,7 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
 #pragma unroll
             for (int q = 0; q < KEEP; ++q) {
                 const bool taken = live && kept[q] >= R::kFirst;
-                w[q] = taken ? __builtin_amdgcn_exp2f(fmaf(R::logit(kept[q]), kLog2E, -ltop)) * inv : 0.0f;
+                w[q] = taken ? __builtin_amdgcn_exp2f((R::logit(kept[q]) - top) * kLog2E) * inv : 0.0f;
                 total += w[q];
             }
             const float norm = renorm ? 1.0f / lanes_sum<L>(total) : 1.0f;
