@@ -721,6 +721,16 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(
         load_row<T, V>(logits + t * sl, e0, experts, whole, -INFINITY, v);
         const float lse = lse_in[t];
         const bool dead = lse == INFINITY;
+        // p from exp(l - lse) over its own sum: lse is rounded to fp32, off by
+        // up to half its last place or by log sum (at most log 4096), whichever
+        // is less, and the sum takes that factor out again
+        float p[V], g[V], sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = __expf(v[i] - lse);  // 0 for -inf; a dead token's is not used
+            sum += p[i];
+        }
+        const float scale = 1.0f / lanes_sum<L>(sum);
         if (gw) {
             float total = 0.0f, wg = 0.0f;
             if (renorm) {
@@ -731,7 +741,7 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(
                         wg = fmaf(weights[t * k + j], gw[t * k + j], wg);
                     }
                 }
-                total = lanes_sum<L>(total);
+                total = lanes_sum<L>(total) * scale;
                 wg = lanes_sum<L>(wg);
             }
             const float inv = renorm ? 1.0f / total : 1.0f;
@@ -743,14 +753,14 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(
             // lanes of one wave: LDS runs its instructions in order
             __builtin_amdgcn_wave_barrier();
         }
-        float p[V], g[V], dot = 0.0f;
+        float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            p[i] *= scale;
             g[i] = bal[i] + (gw ? mine[i] : 0.0f);
-            p[i] = __expf(v[i] - lse);  // 0 for -inf; a dead token's is not used
             dot = fmaf(p[i], g[i], dot);
         }
-        dot = lanes_sum<L>(dot) - gz * lse;
+        dot = lanes_sum<L>(dot);
         if (gw) {
             __builtin_amdgcn_wave_barrier();
             for (int j = sub; j < k; j += L) {
@@ -765,7 +775,8 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(
         Vec o;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            o[i] = Piece<T>::from_f32(dead ? 0.0f : p[i] * (g[i] - dot));
+            // (2 g_z p) lse: 0 for p = 0 whatever 2 g_z lse comes to
+            o[i] = Piece<T>::from_f32(dead ? 0.0f : fmaf(gz * p[i], lse, p[i] * (g[i] - dot)));
         if (whole) {
             if (e0 < experts)
                 *reinterpret_cast<Vec *>(out) = o;
