@@ -210,14 +210,15 @@ def moe_dispatch(x, route: MoeRoute, *, stream=None):
     return _run(x, stream, call)
 
 
-def _combine(yg, route, weights, residual, stream, name, any_layout=False):
+def _combine(yg, route, weighted, residual, stream, name, any_layout=False):
     torch = _torch()
     dt = _dtype(yg, 2, name)
     cap, W = yg.shape
     dev = yg.device
     T = route.rows.shape[0] if route.rows is not None else 0
     k, _ = _plan(route, T, dev)
-    if weights is not None:
+    weights = route.weights if weighted else None
+    if weighted:
         _plain(weights, torch.float32, (T, k), dev, "route.weights")
     if residual is not None:
         _same(residual, yg, (T, W), "residual")
@@ -239,14 +240,14 @@ def _combine(yg, route, weights, residual, stream, name, any_layout=False):
 def moe_dispatch_backward(grad_xg, route: MoeRoute, *, stream=None):
     """Gradient of ``moe_dispatch`` with respect to ``x``: the sum of each
     token's rows of ``grad_xg`` (capacity, width)."""
-    return _combine(grad_xg, route, None, None, stream, "grad_xg", any_layout=True)
+    return _combine(grad_xg, route, False, None, stream, "grad_xg", any_layout=True)
 
 
 def moe_combine(yg, route: MoeRoute, *, residual=None, stream=None):
     """Expert outputs ``yg`` (capacity, width) back to the tokens:
     ``residual + sum_j weights[:, j] * yg[rows[:, j]]`` in fp32, rounded once
     to yg's type.  ``residual``: (tokens, width) of yg's type, or None."""
-    return _combine(yg, route, route.weights, residual, stream, "yg")
+    return _combine(yg, route, True, residual, stream, "yg")
 
 
 def moe_combine_backward(grad_y, yg, route: MoeRoute, *, stream=None):
