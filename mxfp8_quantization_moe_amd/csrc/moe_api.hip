@@ -179,20 +179,34 @@ bool streams(int64_t tokens, int64_t width, int k)
     return tokens * width * (k + 1) * (int64_t)sizeof(T) >= kStreamBytes;
 }
 
+// Workgroups of one launch: a grid ends before 2^32 threads.  More tokens than
+// that takes are passed in several launches, `launch(t0, n)` for n of them
+// from t0 on, the first also without tokens.
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 32) / kRowsThreads - 1;
+template <typename F>
+mxq_status in_launches(int64_t tokens, int64_t per, F &&launch)
+{
+    int64_t t0 = 0;
+    do {
+        launch(t0, (int)std::min(per, tokens - t0));
+        t0 += per;
+    } while (t0 < tokens);
+    return launch_status();
+}
+
 template <typename T, int U>
 mxq_status run_dispatch(const void *x, int64_t sx, int tokens, int width, const int32_t *rows, int k,
                         const int32_t *counts, const int32_t *offs, int experts, void *out, int64_t ld,
                         int capacity, hipStream_t st)
 {
     const int64_t span = 64 * Piece<T>::N * U, chunks = (width + span - 1) / span;
-    const int64_t items = tokens * chunks, work = (items + 3) / 4, clear = clear_blocks(capacity);
-    if (items > INT32_MAX - 4096)
-        return MXQ_ERR_INVALID_ARG;
     auto kernel = streams<T>(tokens, width, k) ? moe_dispatch_kernel<T, U, true> : moe_dispatch_kernel<T, U, false>;
-    kernel<<<dim3((unsigned)(work + clear)), dim3(kRowsThreads), 0, st>>>(
-        reinterpret_cast<const T *>(x), sx, tokens, width, rows, k, counts, offs, experts,
-        reinterpret_cast<T *>(out), ld, capacity, (int)chunks, (int)work);
-    return launch_status();
+    return in_launches(tokens, (kMaxBlocks - clear_blocks(capacity)) * 4 / chunks, [&](int64_t t0, int n) {
+        const int64_t work = (n * chunks + 3) / 4, clear = t0 ? 0 : clear_blocks(capacity);
+        kernel<<<dim3((unsigned)(work + clear)), dim3(kRowsThreads), 0, st>>>(
+            reinterpret_cast<const T *>(x) + t0 * sx, sx, n, width, rows + t0 * k, k, counts, offs, experts,
+            reinterpret_cast<T *>(out), ld, capacity, (int)chunks, (int)work);
+    });
 }
 
 template <typename T, int KB>
@@ -201,14 +215,14 @@ mxq_status run_combine(const void *in, int64_t ld, int capacity, int width, cons
                        hipStream_t st)
 {
     const int64_t span = 64 * Piece<T>::N, chunks = (width + span - 1) / span;
-    const int64_t items = tokens * chunks, work = (items + 3) / 4;
-    if (items > INT32_MAX - 4096)
-        return MXQ_ERR_INVALID_ARG;
     auto kernel = streams<T>(tokens, width, k) ? moe_combine_kernel<T, KB, true> : moe_combine_kernel<T, KB, false>;
-    kernel<<<dim3((unsigned)work), dim3(kRowsThreads), 0, st>>>(
-        reinterpret_cast<const T *>(in), ld, capacity, width, rows, weights, k, reinterpret_cast<const T *>(resid),
-        sr, reinterpret_cast<T *>(y), sy, tokens, (int)chunks);
-    return launch_status();
+    return in_launches(tokens, kMaxBlocks * 4 / chunks, [&](int64_t t0, int n) {
+        const int64_t work = (n * chunks + 3) / 4;
+        kernel<<<dim3((unsigned)work), dim3(kRowsThreads), 0, st>>>(
+            reinterpret_cast<const T *>(in), ld, capacity, width, rows + t0 * k, weights ? weights + t0 * k : nullptr,
+            k, resid ? reinterpret_cast<const T *>(resid) + t0 * sr : nullptr, sr, reinterpret_cast<T *>(y) + t0 * sy,
+            sy, n, (int)chunks);
+    });
 }
 
 template <typename T, int NW, int KB>
@@ -218,16 +232,16 @@ mxq_status run_combine_backward(const void *dy, int64_t sy, int tokens, int widt
                                 hipStream_t st)
 {
     constexpr int TPB = kRowsThreads / 64 / NW;
-    const int64_t work = ((int64_t)tokens + TPB - 1) / TPB, clear = clear_blocks(capacity);
-    if (work > INT32_MAX - 4096)
-        return MXQ_ERR_INVALID_ARG;
     // rows read and written
     auto kernel = streams<T>(tokens, width, 2 * k) ? moe_combine_backward_kernel<T, NW, KB, true>
                                                    : moe_combine_backward_kernel<T, NW, KB, false>;
-    kernel<<<dim3((unsigned)(work + clear)), dim3(kRowsThreads), 0, st>>>(
-        reinterpret_cast<const T *>(dy), sy, tokens, width, reinterpret_cast<const T *>(in), ld, rows, weights, k,
-        counts, offs, experts, capacity, reinterpret_cast<T *>(out), ldo, dw, (int)work);
-    return launch_status();
+    return in_launches(tokens, (kMaxBlocks - clear_blocks(capacity)) * TPB, [&](int64_t t0, int n) {
+        const int64_t work = (n + TPB - 1) / TPB, clear = t0 ? 0 : clear_blocks(capacity);
+        kernel<<<dim3((unsigned)(work + clear)), dim3(kRowsThreads), 0, st>>>(
+            reinterpret_cast<const T *>(dy) + t0 * sy, sy, n, width, reinterpret_cast<const T *>(in), ld, rows + t0 * k,
+            weights + t0 * k, k, counts, offs, experts, capacity, reinterpret_cast<T *>(out), ldo, dw + t0 * k,
+            (int)work);
+    });
 }
 
 // a 2-D operand of rows of `width` unit-stride elements, `n` of them
