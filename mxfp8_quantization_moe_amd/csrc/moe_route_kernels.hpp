@@ -286,12 +286,15 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
     for (int i = 0; i < V; ++i)
         acc[i] = 0.0f;
     __syncthreads();
-    const int first = blockIdx.x * run, last = min(first + run, tokens);
-    for (int t0 = first; ONE ? t0 == first : t0 < last; t0 += kRouteTile) {
+    // the end of a whole last run, and the step past its last round, may not
+    // fit 31 bits: rounds are counted by the tokens left
+    const int first = blockIdx.x * run, own = min(run, tokens - first);
+    for (int t0 = first, left = own; ONE ? t0 == first : left > 0;
+         t0 = (int)((uint32_t)t0 + kRouteTile), left -= kRouteTile) {
         // s0: the wave's first token, so that the wave leaves together
-        for (int s0 = wave * (64 / L); s0 < kRouteTile && t0 + s0 < last; s0 += G) {
+        for (int s0 = wave * (64 / L); s0 < min(kRouteTile, left); s0 += G) {
             const int s = s0 + lane / L, t = t0 + s;
-            const bool in = t < last;
+            const bool in = s < left;
             const int tl = in ? t : first;
             float v[V];
             load_row<T, V>(logits + (int64_t)tl * sl, e0, experts, whole, -INFINITY, v);
@@ -397,7 +400,7 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
             __syncthreads();
         }
         // rank of each slot among the run's slots of its expert
-        const int n = min(kRouteTile, last - t0) * k;
+        const int n = min(kRouteTile, left) * k;
         for (int i = tid; i < n; i += THREADS) {
             const int s = i / k;
             const int64_t at = (int64_t)t0 * k + i;
@@ -430,7 +433,7 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(
         zpart[wave] = zsum;
         npart[wave] = fl;
     }
-    const int waves = min(WAVES, (min(last - first, kRouteTile) + 64 / L - 1) / (64 / L));  // that had a token
+    const int waves = min(WAVES, (min(own, kRouteTile) + 64 / L - 1) / (64 / L));  // that had a token
     for (int w = 0; w < max(waves, 2); w += 2) {
         if (wave >> 1 == w >> 1 && lane < L) {
             float *set = psum + (wave & 1) * experts;

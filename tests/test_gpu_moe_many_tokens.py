@@ -55,3 +55,23 @@ def test_wide_rows_few_of_them_taken(T, W):
     want = torch.zeros(T, device=DEV)
     want[at] = float(x.double().square().sum())  # a whole number below 2^24: exact in fp32
     assert torch.equal(dw[:, 0], want)
+
+
+def test_the_most_tokens_that_a_route_takes():
+    """2^31 - 1 tokens: the last run's end and the step past its last round
+    are past 31 bits."""
+    T = (1 << 31) - 1
+    mask = torch.ones(T, dtype=torch.bool, device=DEV)
+    mask[7] = mask[T - 3] = False
+    r = mxq.moe_route(torch.zeros((T, 1), dtype=torch.bfloat16, device=DEV), 1, token_mask=mask)
+    del mask
+    assert int(r.live) == T - 2 and r.counts.tolist() == [T - 2] and r.offs.tolist() == [T - 2]
+    assert r.mean_prob.tolist() == [1.0] and r.losses.tolist() == [1.0, 0.0]
+    want = torch.arange(T, dtype=torch.int32, device=DEV)
+    want[8:] -= 1
+    want[T - 2:] -= 1
+    want[7] = want[T - 3] = -1
+    assert torch.equal(r.rows[:, 0], want)
+    assert torch.equal(r.ids[:, 0], want.clamp_(-1, 0))
+    assert torch.equal(r.weights[:, 0], want.add_(1).float())
+    assert not r.lse[:7].any() and torch.isinf(r.lse[[7, T - 3]]).all() and not r.lse[T - 2:].any()
