@@ -487,8 +487,8 @@ mxq_status mxq_moe_combine_backward(const void *grad_y, int32_t dtype, int64_t t
  * of two that keep the operands inside f16 leave room for iterates with
  * entries up to 8 and entries of A and B up to 32; coefficients that let X
  * grow past that give inf or NaN.  The norm is summed in fp64: any finite G
- * is in range.  A G of zeros gives zeros; a NaN or infinity anywhere in a
- * matrix makes that whole matrix NaN or zero.
+ * is in range.  A G of zeros gives zeros, also with eps = 0; a NaN or
+ * infinity anywhere in a matrix makes that whole matrix NaN or zero.
  *
  * g       (count, rows, cols) bf16 or fp32, strides (sg_e, sg_r, sg_c);
  *         rows and cols <= 65536.

@@ -160,8 +160,9 @@ __global__ __launch_bounds__(256) void muon_load_kernel(const T *__restrict__ g,
     for (int i = tid; i < b.parts; i += 256)
         square += b.part[(int64_t)e * kNormParts + i];
     square = block_sum<256>(sums, square);
-    // in fp64: the reciprocal of a tiny norm overflows fp32
-    const double mul = (double)kScaleX / (sqrt(square) + (double)eps);
+    // in fp64: the reciprocal of a tiny norm overflows fp32.  A matrix of zeros
+    // stays zeros with eps = 0 too.
+    const double norm = sqrt(square) + (double)eps, mul = norm == 0.0 ? 0.0 : (double)kScaleX / norm;
     const T *p = g + e * v.se;
     const bool inner_j = v.sj == 1;
     const int n_in = inner_j ? v.n - j0 : v.m - i0, n_out = inner_j ? v.m - i0 : v.n - j0;
