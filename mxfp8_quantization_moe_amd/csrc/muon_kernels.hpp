@@ -15,7 +15,7 @@
 // kScaleB) keep them far from f16's ends.  Rounding the operands alone would
 // cost 1.4e-3 to 3e-3 of the result (relative 2-norm, simulated), more than
 // the final bf16 rounding (1.65e-3).  Two exact rearrangements bring it to
-// 3e-4 to 7e-4 without another product:
+// 2e-4 to 7e-4 for ordinary gradients without another product:
 //   - X is carried in two parts, f16 and the difference in e4m3 (about 15
 //     bits; 22 bits of f16 + f16 measured no better and cost a byte per element
 //     each way), and a X + diag(B) X is added in fp32 from both parts; only the
@@ -24,6 +24,11 @@
 //     singular values are near one another, never enter an f16 operand: with
 //     A = diag(d) + O,  A^2 = O O + d_i O_ij + O_ij d_j + diag(d^2), and the
 //     last three terms are fp32 in the epilogue (O there from two parts).
+// Where O is large instead (rows that repeat, gradients of few tokens), f16's
+// roundings of O and B come back, without those of the diagonals that would
+// meet them: with the output's rounding 2e-3 to 4e-3, for one token 4e-3 to
+// 1.3e-2.  The same steps on bf16 operands are 2e-2 off for ordinary gradients
+// and of no use for those of one token (1.2).
 //
 // Layout.  X is row-major.  X X^T and O O sum along rows; B X sums along X's
 // columns and reads its operand through the transposing LDS read, so X is
