@@ -171,7 +171,7 @@ int pieces_per_lane(int64_t width)
 }
 
 // from here on a call's loads carry the nontemporal hint (see ld_piece): between
-// the 100 MB that lose by it and the 235 MB that gain
+// the 100 MB that lose by it and the 200 MB that are even or gain
 constexpr int64_t kStreamBytes = 160 << 20;
 template <typename T>
 bool streams(int64_t tokens, int64_t width, int k)

@@ -249,10 +249,12 @@ __device__ __forceinline__ void group_ends(const int32_t *count, int32_t *start,
 // One run of tokens per workgroup.  L lanes per token, V experts per lane.
 // FEW: at most 8 slots, so only the first 8 of a lane's sorted keys can be
 // taken.  ONE: the only run.
-// 16384 tokens x 256 experts fp32, 8 slots: 19 us for 19 MB, bound by the
-// vector instructions of the selection (1060 per wave of 4 tokens; 640 with
-// bf16 logits' 32-bit keys); x 8 experts bf16, 2 slots: 4.4 us, latency; one
-// token of 256: 7.5 us, its chain of reductions.
+// 16384 tokens x 256 experts fp32, 8 slots: 19 us for 19 MB.  Vector
+// instructions (1060 per wave of 4 tokens; 640 with bf16 logits' 32-bit keys)
+// issue in 44% of the cycles; the waves wait in 61% of theirs: one workgroup
+// per CU has one round, whose load, reductions, selection, ranks and closing
+// sum follow one another.  x 8 experts bf16, 2 slots: 4.4 us, latency; one
+// token of 256: 7.6 us, its chain of reductions.
 template <typename T, int L, int V, bool FEW, int THREADS, bool ONE>
 __global__ __launch_bounds__(THREADS) void moe_route_kernel(
     const T *__restrict__ logits, int64_t sl, int tokens, int experts, const uint8_t *__restrict__ mask, int k,
@@ -552,7 +554,7 @@ __global__ __launch_bounds__(kScanThreads) void moe_scan_kernel(int experts, int
 }
 
 // A run per workgroup: its slots' ranks become rows.  The last workgroup
-// writes the group ends and the losses.  4.4 us for 131072 slots of 256
+// writes the group ends and the losses.  4.2 us for 131072 slots of 256
 // experts, latency (1.8 MB).
 __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(int tokens, int experts, int k, int align, int run,
                                                                   int nruns, const int32_t *__restrict__ ids,
@@ -599,8 +601,8 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(int tokens, in
 
 // The second and third kernel in one, for few runs and experts: every
 // workgroup adds up all the runs' counts itself, each expert by several
-// threads (integer sums, in any order).  6.5 us for 256 runs of 8 experts,
-// 8.0 for 65 of 61: latency, against two launches saved into one.
+// threads (integer sums, in any order).  6.2 us for 256 runs of 8 experts,
+// 8.4 for 65 of 61: latency, against two launches saved into one.
 __global__ __launch_bounds__(kPlaceThreads) void moe_finish_kernel(int tokens, int experts, int k, int align, int run,
                                                                    int nruns, const int32_t *__restrict__ ids,
                                                                    int32_t *__restrict__ rows, RouteWorkspace ws,
@@ -686,9 +688,10 @@ constexpr int route_row_step(int v) { return v > 4 && v <= 16 ? v + 4 : v; }
 // the selected probabilities (through the renormalisation when there is one).
 // A slot's part is worked out by one lane and reaches the lane that holds its
 // expert through a row of zeros in LDS (comparing every expert with every slot
-// took three times as long).  16384 x 256 fp32: 13.7 us for 35 MB (2.6 TB/s);
-// 65536 x 256 bf16 21 us (3.3 TB/s): one pass over the memory, its few tokens
-// per wave bound by latency.
+// took three times as long).  16384 x 256 fp32: 13.6 us for 35 MB (2.6 TB/s);
+// 65536 x 256 bf16 21.6 us (3.2 TB/s): one pass over the memory, each group of
+// lanes with one token at a time, bound by the latency of its chain (vector
+// instructions issue in 28% of the first one's cycles, its waves wait in 63%).
 template <typename T, int L, int V>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(
     const T *__restrict__ logits, int64_t sl, int tokens, int experts, int k, int renorm,

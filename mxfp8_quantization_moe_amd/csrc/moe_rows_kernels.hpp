@@ -65,10 +65,13 @@ __device__ __forceinline__ int piece_start(int p, int width)
 }
 
 // STREAM: with the nontemporal hint, for calls that move more than the caches
-// hold.  16384 tokens of 4096 bf16 over 2 slots (402 MB): dispatch 75 -> 61 us,
-// combine 76 -> 65, its gradient 130 -> 104; 4096 tokens (100 MB) lose: 16.2
-// -> 18.8, 19.7 -> 19.8, 30.8 -> 30.0.  The hint on the stores as well, or on
-// them alone, is slower (70 and 72 us for the first).
+// hold.  Three sets of inputs in turn, one call after the other: 16384 tokens
+// of 4096 bf16 over 2 slots (402 MB) dispatch 75 -> 61 us, combine 71 -> 62, its
+// gradient 132 -> 105; 8192 tokens 33.3 -> 33.3, 34.0 -> 34.6, 69 -> 57; 4096
+// tokens (100 MB) lose: 16.9 -> 19.5, 16.4 -> 18.4, 30.8 -> 30.0.  Dispatch and
+// its gradient in turn 153 -> 144, combine and its gradient 190 -> 186.  The
+// hint on the stores as well, or on them alone, is slower (70 and 72 us for
+// the first).
 template <typename T, bool STREAM = false>
 __device__ __forceinline__ Piece<T> ld_piece(const T *p)
 {
@@ -124,7 +127,8 @@ __device__ __forceinline__ void zero_rows(int z, int nz, const int32_t *__restri
 
 // One wave per (token, chunk of 64 * U pieces); the workgroups past
 // `work` blocks clear the rows without a slot.  16384 tokens of 4096 bf16 over
-// 2 slots: 73 us for 403 MB (5.5 TB/s), bound by memory.
+// 2 slots: 61 us for 403 MB (6.6 TB/s) after calls of its own kind, 74 (5.4)
+// after its gradient on other rows: bound by memory.
 template <typename T, int U, bool STREAM>
 __global__ __launch_bounds__(kRowsThreads) void moe_dispatch_kernel(
     const T *__restrict__ x, int64_t sx, int tokens, int width, const int32_t *__restrict__ rows, int k,
@@ -176,7 +180,9 @@ __global__ __launch_bounds__(kRowsThreads) void moe_dispatch_kernel(
 // lane make fewer, longer waves, which is slower: 16384 tokens of 2048 bf16
 // over 2 slots 32.6 us, 36.7 with four; of 4096 62.8 us, 66.3.  Between other
 // passes, its rows in no cache, the last takes 72 us (5.6 TB/s); 8 tokens of
-// 5120 over 8 slots 3.6 us.
+// 5120 over 8 slots 3.7 us.  Slots that do not fill a block of KB cost little:
+// rows of 4096 bf16 over 1, 3, 5 and 9 slots run at 5.9, 6.3, 5.9 and 5.4 TB/s,
+// over 2, 4, 8 and 16 at 6.4, 6.1, 5.8 and 5.7.
 template <typename T, int KB, bool STREAM>
 __global__ __launch_bounds__(kRowsThreads) void moe_combine_kernel(
     const T *__restrict__ in, int64_t ld, int capacity, int width, const int32_t *__restrict__ rows,
@@ -256,7 +262,8 @@ __device__ __forceinline__ float wave_sum(float v)
 // NW waves per token; each lane holds its piece of dy while KB slots' rows
 // pass, and the dot products meet in a fixed order (lane tree, then waves).
 // 16384 tokens of 4096 bf16 over 2 slots, a tenth masked: 122 us for 652 MB
-// (5.3 TB/s), bound by memory.
+// (5.3 TB/s), bound by memory.  Rows of 4096 bf16 over 1, 3, 5 and 9 slots: 6.0,
+// 6.1, 6.1 and 5.1 TB/s, over 2, 4, 8 and 16 6.4, 6.1, 6.1 and 5.8.
 template <typename T, int NW, int KB, bool STREAM>
 __global__ __launch_bounds__(kRowsThreads) void moe_combine_backward_kernel(
     const T *__restrict__ dy, int64_t sy, int tokens, int width, const T *__restrict__ in, int64_t ld,

@@ -90,9 +90,9 @@ void launch_product(const MuonBuffers &b, const MuonStep &st, int64_t count, uin
 // X X^T of a long matrix has few tiles with long sums: each sum is then taken
 // in up to 8 parts of at least 12 stages, as many as `at_once` workgroups of
 // the tile run at a time and as fit where the next X will be, and joined by a
-// kernel of its own.  Five steps, without / with: 1 x 64 x 8192 191 / 100 us,
-// 3 x 175 x 7481 232 / 155, 1 x 256 x 4096 155 / 117, 1 x 2048 x 8192 964 /
-// 900; a sum of less than 32 stages loses by the launch (17 x 126 x 1327 106 /
+// kernel of its own.  Five steps, without / with: 1 x 64 x 8192 191 / 101 us,
+// 3 x 175 x 7481 233 / 160, 1 x 256 x 4096 155 / 117, 1 x 2048 x 8192 932 /
+// 871; a sum of less than 32 stages loses by the launch (17 x 126 x 1327 106 /
 // 122), and so do medium tiles past one per CU (2 x 1024 x 4096 363 / 370).
 template <typename TILE>
 int sum_splits(const MuonBuffers &b, int64_t count, int64_t at_once)
