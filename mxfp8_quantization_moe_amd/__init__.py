@@ -28,7 +28,10 @@ from ._capi import (MXQ_ERR_INVALID_ARG, MXQ_ERR_LAUNCH, MXQ_ERR_UNSUPPORTED, MX
                     mxq_relayout_mx_scales_grouped, MXQ_BF16, MXQ_F32, MXQ_MAX_GROUP_ALIGN,
                     MXQ_MAX_TOP_K, mxq_moe_combine, mxq_moe_combine_backward, mxq_moe_dispatch,
                     mxq_moe_route, mxq_moe_route_backward, mxq_moe_route_workspace_bytes,
-                    mxq_moe_row_capacity, mxq_muon_orthogonalize, mxq_muon_workspace_bytes)
+                    mxq_moe_row_capacity, mxq_muon_orthogonalize, mxq_muon_workspace_bytes,
+                    MXQ_ACT_GELU, MXQ_ACT_NONE, MXQ_ACT_RELU, MXQ_ACT_SILU, mxq_moe_linear,
+                    mxq_moe_linear_backward, mxq_moe_linear_backward_workspace_bytes, mxq_moe_linear_mx,
+                    mxq_moe_linear_mx_workspace_bytes, mxq_moe_linear_workspace_bytes)
 
 __all__ = [
     "quantize_jagged_rowwise", "quantize_jagged_colwise", "quantize_mx_3d_colwise",
@@ -48,6 +51,9 @@ __all__ = [
     "mxq_moe_row_capacity", "mxq_moe_dispatch", "mxq_moe_combine", "mxq_moe_combine_backward",
     "MUON_COEFFICIENTS", "muon_orthogonalize", "muon_workspace", "mxq_muon_orthogonalize",
     "mxq_muon_workspace_bytes",
+    "ACTIVATIONS", "moe_linear", "moe_linear_backward", "moe_linear_mx", "mxq_moe_linear",
+    "mxq_moe_linear_backward", "mxq_moe_linear_backward_workspace_bytes", "mxq_moe_linear_mx",
+    "mxq_moe_linear_mx_workspace_bytes", "mxq_moe_linear_workspace_bytes",
 ]
 
 
@@ -330,3 +336,4 @@ def debug_cast4_e4m3(y, unclamped: bool, *, stream=None):
 from .moe import (MoeRoute, moe_combine, moe_combine_backward, moe_dispatch,  # noqa: E402
                   moe_dispatch_backward, moe_route, moe_route_backward, moe_row_capacity)
 from .muon import MUON_COEFFICIENTS, muon_orthogonalize, muon_workspace  # noqa: E402
+from .linear import ACTIVATIONS, moe_linear, moe_linear_backward, moe_linear_mx  # noqa: E402

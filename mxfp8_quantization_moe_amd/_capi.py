@@ -27,6 +27,10 @@ MXQ_MAX_GROUP_ALIGN = 4096
 MXQ_BF16 = 0
 MXQ_F32 = 1
 MXQ_NOALLOC_SCRATCH_BYTES = 4 << 20
+MXQ_ACT_NONE = 0
+MXQ_ACT_RELU = 1
+MXQ_ACT_GELU = 2
+MXQ_ACT_SILU = 3
 
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
@@ -75,12 +79,23 @@ SIGNATURES = {
     "mxq_muon_workspace_bytes": [_i64, _i64, _i64],
     "mxq_muon_orthogonalize": [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _i64,
                                _i32, _f32, _f32, _f32, _f32, _f32, _vp, _i64, _vp],
+    "mxq_moe_linear_workspace_bytes": [_i64, _i64, _i32, _i64, _i32],
+    "mxq_moe_linear": [_vp, _i64, _i64, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _i32, _i32,
+                       _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp],
+    "mxq_moe_linear_backward_workspace_bytes": [_i64, _i64, _i32, _i64, _i32, _i32, _i32, _i32],
+    "mxq_moe_linear_backward": [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp,
+                                _i64, _i64, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp],
+    "mxq_moe_linear_mx_workspace_bytes": [_i64, _i64, _i32, _i64, _i32],
+    "mxq_moe_linear_mx": [_vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _i64,
+                          _i64, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
+                          _i64, _vp],
     "mxq_debug_cast_e4m3": [_vp, _i64, _vp, _vp],
     "mxq_debug_cast4_e4m3": [_vp, _i64, _vp, _i32, _vp],
 }
 RESTYPES = {"mxq_status_string": ctypes.c_char_p, "mxq_jagged_colwise_workspace_bytes": _i64,
             "mxq_moe_row_capacity": _i64, "mxq_moe_route_workspace_bytes": _i64,
-            "mxq_muon_workspace_bytes": _i64}
+            "mxq_muon_workspace_bytes": _i64, "mxq_moe_linear_workspace_bytes": _i64,
+            "mxq_moe_linear_backward_workspace_bytes": _i64, "mxq_moe_linear_mx_workspace_bytes": _i64}
 
 _lib = None
 
@@ -142,5 +157,11 @@ mxq_moe_combine = _fwd("mxq_moe_combine")
 mxq_moe_combine_backward = _fwd("mxq_moe_combine_backward")
 mxq_muon_workspace_bytes = _fwd("mxq_muon_workspace_bytes")
 mxq_muon_orthogonalize = _fwd("mxq_muon_orthogonalize")
+mxq_moe_linear_workspace_bytes = _fwd("mxq_moe_linear_workspace_bytes")
+mxq_moe_linear = _fwd("mxq_moe_linear")
+mxq_moe_linear_backward_workspace_bytes = _fwd("mxq_moe_linear_backward_workspace_bytes")
+mxq_moe_linear_backward = _fwd("mxq_moe_linear_backward")
+mxq_moe_linear_mx_workspace_bytes = _fwd("mxq_moe_linear_mx_workspace_bytes")
+mxq_moe_linear_mx = _fwd("mxq_moe_linear_mx")
 mxq_debug_cast_e4m3 = _fwd("mxq_debug_cast_e4m3")
 mxq_debug_cast4_e4m3 = _fwd("mxq_debug_cast4_e4m3")

@@ -1,0 +1,407 @@
+// C entry points of the experts' products: argument checks, operands whose
+// rows the kernels cannot read in place, the choice of a tile and the launches.
+// No allocation, no synchronisation, no read-back.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "mxq.h"
+#include "api_common.hpp"
+#include "linear_kernels.hpp"
+
+namespace {
+
+using namespace mxq;
+
+constexpr int64_t kMaxDim = 65536;
+
+using TileSmall = LinearTile<64, 64, 2, 2, 3>;
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+bool sizes_ok(int64_t rows, int64_t width, int32_t experts, int64_t wide)
+{
+    return rows >= 0 && rows <= INT32_MAX - 4096 && width >= 0 && width <= kMaxDim && experts >= 1 &&
+           experts <= MXQ_MAX_GROUPS && wide >= 0 && wide <= kMaxDim;
+}
+
+bool act_ok(int32_t activation, int32_t gated, int64_t wide)
+{
+    return activation >= MXQ_ACT_NONE && activation <= MXQ_ACT_SILU && (gated == 0 || gated == 1) &&
+           (!gated || wide % 2 == 0);
+}
+
+// A bf16 operand (count, rows, cols) with unit stride along cols that the
+// kernels read in place: 16-byte pieces throughout, rows that do not overlap,
+// and offsets within a tile that fit 31 bits.
+struct Rows {
+    const void *p;
+    int64_t se, sr, rows, cols;
+    bool direct() const
+    {
+        return cols % 8 == 0 && aligned16(p) && se % 8 == 0 && sr % 8 == 0 && sr < (1 << 21) && (sr >= cols || rows <= 1);
+    }
+    int64_t packed_bytes(int64_t count) const { return round_up(count * rows * round_up(cols, 8) * 2, 256); }
+};
+
+// What a call's workspace has been used for so far.
+struct Room {
+    char *at, *end;
+    void *take(int64_t bytes)
+    {
+        char *p = at;
+        at += bytes;
+        return p;
+    }
+};
+
+// the operand in place or a copy in padded rows
+Rows readable(const Rows &r, int64_t count, Room &room, hipStream_t st)
+{
+    if (r.direct())
+        return r;
+    Rows to = {nullptr, 0, round_up(r.cols, 8), r.rows, r.cols};
+    to.se = r.rows * to.sr;
+    to.p = room.take(r.packed_bytes(count));
+    const int64_t pieces = r.rows * to.sr / 8;
+    if (pieces > 0)
+        linear_pack_kernel<<<dim3((unsigned)std::min<int64_t>((pieces + 255) / 256, 8192), (unsigned)count), dim3(256), 0, st>>>(
+            reinterpret_cast<const uint16_t *>(r.p), r.se, r.sr, (int)r.rows, (int)r.cols,
+            const_cast<uint16_t *>(reinterpret_cast<const uint16_t *>(to.p)), (int)to.sr);
+    return to;
+}
+
+// e8m0 scales (count, rows, blocks), read in words of four blocks
+struct Scales {
+    const uint8_t *p;
+    int64_t se, sr, sb, rows, blocks;
+    bool direct() const
+    {
+        return blocks % 4 == 0 && sb == 1 && aligned_to(p, 4) && se % 4 == 0 && sr % 4 == 0;
+    }
+    int64_t packed_bytes(int64_t count) const { return round_up(count * rows * round_up(blocks, 4), 256); }
+};
+
+Scales readable(const Scales &s, int64_t count, Room &room, hipStream_t st)
+{
+    if (s.direct())
+        return s;
+    Scales to = {nullptr, 0, round_up(s.blocks, 4), 1, s.rows, s.blocks};
+    to.se = s.rows * to.sr;
+    to.p = reinterpret_cast<uint8_t *>(room.take(s.packed_bytes(count)));
+    const int64_t words = s.rows * to.sr / 4;
+    if (words > 0)
+        linear_pack_scales_kernel<<<dim3((unsigned)std::min<int64_t>((words + 255) / 256, 8192), (unsigned)count), dim3(256), 0, st>>>(
+            s.p, s.se, s.sr, s.sb, (int)s.rows, (int)s.blocks, const_cast<uint8_t *>(to.p), (int)to.sr);
+    return to;
+}
+
+// Row tiles that any group ends can need; one group has none behind it.
+int64_t row_tiles(int64_t rows, int32_t experts, bool grouped, int64_t tm)
+{
+    const int64_t even = (rows + tm - 1) / tm;
+    return grouped ? std::min<int64_t>(even + experts, rows) : even;
+}
+
+// a grid that `spread` covers, or 0 if it is past what one launch takes
+int64_t grid_of(int64_t tiles, int64_t threads)
+{
+    const int64_t g = round_up(tiles, 256);
+    return g * threads < ((int64_t)1 << 32) && g <= INT32_MAX ? g : 0;
+}
+
+template <int MODE, typename TILE, bool GATED, bool MX>
+mxq_status launch(const LinearArgs &a, hipStream_t st)
+{
+    const int64_t tj = GATED ? TILE::TN / 2 : TILE::TN, tn = (a.n + tj - 1) / tj;
+    const int64_t tm = MODE == kGradW ? (int64_t)a.experts * ((a.wide + TILE::TM - 1) / TILE::TM)
+                                      : row_tiles(a.rows, a.experts, a.offs != nullptr, TILE::TM);
+    if (tm * tn == 0)
+        return MXQ_OK;
+    const int64_t grid = grid_of(tm * tn, TILE::THREADS);
+    if (grid == 0)
+        return MXQ_ERR_UNSUPPORTED;
+    linear_kernel<MODE, TILE, GATED, MX><<<dim3((unsigned)grid), dim3(TILE::THREADS), 0, st>>>(a);
+    return launch_status();
+}
+
+template <bool MX>
+mxq_status launch_forward(const LinearArgs &a, int gated, hipStream_t st)
+{
+    return gated ? launch<kForward, TileSmall, true, MX>(a, st) : launch<kForward, TileSmall, false, MX>(a, st);
+}
+
+// a 2-D operand or result of bf16: rows of unit stride
+bool rows_ok(const void *p, int64_t n, int64_t stride, bool writes, int64_t cols)
+{
+    return (n == 0 || cols == 0 || p) && aligned_to(p, 2) && stride >= 0 && (!writes || n <= 1 || stride >= cols);
+}
+
+bool bias_ok(const void *bias, int32_t dtype, int64_t sb_e)
+{
+    return !bias || ((dtype == MXQ_BF16 || dtype == MXQ_F32) && aligned_to(bias, dtype == MXQ_BF16 ? 2 : 4) && sb_e >= 0);
+}
+
+// of a gated product a tile's rows of W lie `wide` / 2 apart
+bool reach_ok(int64_t wide, int64_t row_bytes) { return wide * row_bytes < ((int64_t)1 << 31); }
+
+}  // namespace
+
+extern "C" {
+
+int64_t mxq_moe_linear_workspace_bytes(int64_t rows, int64_t width, int32_t num_experts, int64_t wide, int32_t aligned)
+{
+    if (!sizes_ok(rows, width, num_experts, wide))
+        return -1;
+    if (aligned && width % 8 == 0)
+        return 0;
+    return Rows{nullptr, 0, 0, rows, width}.packed_bytes(1) + Rows{nullptr, 0, 0, wide, width}.packed_bytes(num_experts);
+}
+
+mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_t sx_r, int64_t sx_c, const uint16_t *w,
+                          int32_t num_experts, int64_t wide, int64_t sw_e, int64_t sw_n, int64_t sw_k,
+                          const int32_t *offs, const void *bias, int32_t bias_dtype, int64_t sb_e, int32_t activation,
+                          int32_t gated, const uint16_t *residual, int64_t sr_r, int64_t sr_c, uint16_t *y, int64_t sy_r,
+                          int64_t sy_c, uint16_t *pre, int64_t sp_r, int64_t sp_c, void *workspace,
+                          int64_t workspace_bytes, void *stream)
+{
+    if (!sizes_ok(rows, width, num_experts, wide) || !act_ok(activation, gated, wide) || (!offs && num_experts != 1) ||
+        !bias_ok(bias, bias_dtype, sb_e) || !aligned16(workspace))
+        return MXQ_ERR_INVALID_ARG;
+    const int64_t n = gated ? wide / 2 : wide;
+    if ((width > 1 && (sx_c != 1 || sw_k != 1)) || (n > 1 && (sy_c != 1 || (residual && sr_c != 1) || (pre && sp_c != 1))))
+        return MXQ_ERR_UNSUPPORTED;
+    if (!rows_ok(x, rows, sx_r, false, width) || !rows_ok(w, num_experts * wide, sw_n, false, width) || sw_e < 0 ||
+        !rows_ok(y, rows, sy_r, true, n) || (residual && !rows_ok(residual, rows, sr_r, false, n)) ||
+        (pre && !rows_ok(pre, rows, sp_r, true, wide)))
+        return MXQ_ERR_INVALID_ARG;
+    if (rows == 0 || n == 0)
+        return MXQ_OK;
+    const Rows xr = {x, 0, sx_r, rows, width}, wr = {w, sw_e, sw_n, wide, width};
+    const int64_t need = (xr.direct() ? 0 : xr.packed_bytes(1)) + (wr.direct() ? 0 : wr.packed_bytes(num_experts));
+    if (workspace_bytes < need || (need > 0 && !workspace))
+        return MXQ_ERR_WORKSPACE;
+    if (!reach_ok(wide, wr.direct() ? sw_n * 2 : round_up(width, 8) * 2))
+        return MXQ_ERR_UNSUPPORTED;
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    Room room = {reinterpret_cast<char *>(workspace), nullptr};
+    const Rows xo = readable(xr, 1, room, st), wo = readable(wr, num_experts, room, st);
+    LinearArgs a = {};
+    a.p = reinterpret_cast<const char *>(xo.p);
+    a.ldp = xo.sr * 2;
+    a.q = reinterpret_cast<const char *>(wo.p);
+    a.ldq = wo.sr * 2;
+    a.qe = wo.se * 2;
+    a.offs = offs;
+    a.experts = num_experts;
+    a.rows = (int)rows;
+    a.width = (int)width;
+    a.wide = (int)wide;
+    a.n = (int)n;
+    a.bias = bias;
+    a.sb = sb_e;
+    a.bias_f32 = bias_dtype == MXQ_F32;
+    a.act = activation;
+    a.resid = residual;
+    a.sr = sr_r;
+    a.out = y;
+    a.so = sy_r;
+    a.pre = pre;
+    a.spre = sp_r;
+    return launch_forward<false>(a, gated, st);
+}
+
+int64_t mxq_moe_linear_mx_workspace_bytes(int64_t rows, int64_t width, int32_t num_experts, int64_t wide, int32_t aligned)
+{
+    if (!sizes_ok(rows, width, num_experts, wide) || width % 32)
+        return -1;
+    if (aligned && width % 128 == 0)
+        return 0;
+    return Scales{nullptr, 0, 0, 1, rows, width / 32}.packed_bytes(1) +
+           Scales{nullptr, 0, 0, 1, wide, width / 32}.packed_bytes(num_experts);
+}
+
+mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int64_t sx_r, int64_t sx_c,
+                             const uint8_t *x_scales, int64_t sxs_r, int64_t sxs_b, const uint8_t *w,
+                             int32_t num_experts, int64_t wide, int64_t sw_e, int64_t sw_n, int64_t sw_k,
+                             const uint8_t *w_scales, int64_t sws_e, int64_t sws_n, int64_t sws_b, const int32_t *offs,
+                             const void *bias, int32_t bias_dtype, int64_t sb_e, int32_t activation, int32_t gated,
+                             const uint16_t *residual, int64_t sr_r, int64_t sr_c, uint16_t *y, int64_t sy_r,
+                             int64_t sy_c, uint16_t *pre, int64_t sp_r, int64_t sp_c, void *workspace,
+                             int64_t workspace_bytes, void *stream)
+{
+    if (!sizes_ok(rows, width, num_experts, wide) || width % 32 || !act_ok(activation, gated, wide) ||
+        (!offs && num_experts != 1) || !bias_ok(bias, bias_dtype, sb_e) || !aligned16(workspace))
+        return MXQ_ERR_INVALID_ARG;
+    const int64_t n = gated ? wide / 2 : wide;
+    if ((width > 1 && (sx_c != 1 || sw_k != 1)) || (n > 1 && (sy_c != 1 || (residual && sr_c != 1) || (pre && sp_c != 1))))
+        return MXQ_ERR_UNSUPPORTED;
+    if (rows > 0 && wide > 0 && width > 0 && (!x || !w || !x_scales || !w_scales))
+        return MXQ_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w) || sx_r % 16 || sw_e % 16 || sw_n % 16 || sx_r < 0 || sw_e < 0 || sw_n < 0 ||
+        sx_r >= (1 << 22) || sw_n >= (1 << 22) || sxs_r < 0 || sxs_b < 0 || sws_e < 0 || sws_n < 0 || sws_b < 0 ||
+        !rows_ok(y, rows, sy_r, true, n) || (residual && !rows_ok(residual, rows, sr_r, false, n)) ||
+        (pre && !rows_ok(pre, rows, sp_r, true, wide)))
+        return MXQ_ERR_INVALID_ARG;
+    if (rows == 0 || n == 0)
+        return MXQ_OK;
+    const Scales xs = {x_scales, 0, sxs_r, sxs_b, rows, width / 32};
+    const Scales ws = {w_scales, sws_e, sws_n, sws_b, wide, width / 32};
+    const int64_t need = (xs.direct() ? 0 : xs.packed_bytes(1)) + (ws.direct() ? 0 : ws.packed_bytes(num_experts));
+    if (workspace_bytes < need || (need > 0 && !workspace))
+        return MXQ_ERR_WORKSPACE;
+    if (!reach_ok(wide, sw_n))
+        return MXQ_ERR_UNSUPPORTED;
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    Room room = {reinterpret_cast<char *>(workspace), nullptr};
+    const Scales xo = readable(xs, 1, room, st), wo = readable(ws, num_experts, room, st);
+    LinearArgs a = {};
+    a.p = reinterpret_cast<const char *>(x);
+    a.ldp = sx_r;
+    a.q = reinterpret_cast<const char *>(w);
+    a.ldq = sw_n;
+    a.qe = sw_e;
+    a.sp = xo.p;
+    a.ldsp = xo.sr;
+    a.sq = wo.p;
+    a.ldsq = wo.sr;
+    a.sqe = wo.se;
+    a.offs = offs;
+    a.experts = num_experts;
+    a.rows = (int)rows;
+    a.width = (int)width;
+    a.wide = (int)wide;
+    a.n = (int)n;
+    a.bias = bias;
+    a.sb = sb_e;
+    a.bias_f32 = bias_dtype == MXQ_F32;
+    a.act = activation;
+    a.resid = residual;
+    a.sr = sr_r;
+    a.out = y;
+    a.so = sy_r;
+    a.pre = pre;
+    a.spre = sp_r;
+    return launch_forward<true>(a, gated, st);
+}
+
+namespace {
+
+// slices of kSliceRows rows that any group ends can need
+int64_t slice_count(int64_t rows, int32_t experts, bool grouped)
+{
+    return row_tiles(rows, experts, grouped, kSliceRows);
+}
+
+int64_t parts_bytes(int64_t rows, int32_t experts, int64_t wide)
+{
+    return round_up(slice_count(rows, experts, true) * wide * 4, 256);
+}
+
+}  // namespace
+
+int64_t mxq_moe_linear_backward_workspace_bytes(int64_t rows, int64_t width, int32_t num_experts, int64_t wide,
+                                                int32_t activation, int32_t gated, int32_t bias, int32_t aligned)
+{
+    if (!sizes_ok(rows, width, num_experts, wide) || !act_ok(activation, gated, wide))
+        return -1;
+    const Rows z = {nullptr, 0, 0, rows, wide}, x = {nullptr, 0, 0, rows, width}, w = {nullptr, 0, 0, wide, width};
+    int64_t need = bias ? parts_bytes(rows, num_experts, wide) : 0;
+    if (activation != MXQ_ACT_NONE || gated || !aligned || wide % 8)
+        need += z.packed_bytes(1);
+    if (!aligned || width % 8)
+        need += x.packed_bytes(1) + w.packed_bytes(num_experts);
+    return need;
+}
+
+mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t sg_c, const uint16_t *x, int64_t rows,
+                                   int64_t width, int64_t sx_r, int64_t sx_c, const uint16_t *w, int32_t num_experts,
+                                   int64_t wide, int64_t sw_e, int64_t sw_n, int64_t sw_k, const int32_t *offs,
+                                   const uint16_t *pre, int64_t sp_r, int64_t sp_c, int32_t activation, int32_t gated,
+                                   uint16_t *grad_x, int64_t sdx_r, int64_t sdx_c, uint16_t *grad_w, int64_t sdw_e,
+                                   int64_t sdw_n, int64_t sdw_k, float *grad_bias, void *workspace,
+                                   int64_t workspace_bytes, void *stream)
+{
+    if (!sizes_ok(rows, width, num_experts, wide) || !act_ok(activation, gated, wide) || (!offs && num_experts != 1) ||
+        !aligned16(workspace) || !aligned_to(grad_bias, 4))
+        return MXQ_ERR_INVALID_ARG;
+    const int64_t n = gated ? wide / 2 : wide;
+    const bool saved = activation != MXQ_ACT_NONE || gated;
+    if ((n > 1 && (sg_c != 1 || (saved && sp_c != 1))) ||
+        (width > 1 && ((grad_w && (sx_c != 1 || sdw_k != 1)) || (grad_x && (sw_k != 1 || sdx_c != 1)))))
+        return MXQ_ERR_UNSUPPORTED;
+    if (!rows_ok(grad_y, rows, sg_r, false, n) || (saved && !rows_ok(pre, rows, sp_r, false, wide)) ||
+        (grad_w && (!rows_ok(x, rows, sx_r, false, width) || !rows_ok(grad_w, wide, sdw_n, true, width) || sdw_e < 0 ||
+                    (num_experts > 1 && sdw_e < wide * sdw_n))) ||
+        (grad_x && (!rows_ok(w, num_experts * wide, sw_n, false, width) || sw_e < 0 ||
+                    !rows_ok(grad_x, rows, sdx_r, true, width))))
+        return MXQ_ERR_INVALID_ARG;
+    const Rows yr = {grad_y, 0, sg_r, rows, n}, zr = {nullptr, 0, 0, rows, wide}, xr = {x, 0, sx_r, rows, width},
+               wr = {w, sw_e, sw_n, wide, width};
+    int64_t need = grad_bias ? parts_bytes(rows, num_experts, wide) : 0;
+    if (saved || !yr.direct())
+        need += zr.packed_bytes(1);
+    if (grad_w && !xr.direct())
+        need += xr.packed_bytes(1);
+    if (grad_x && !wr.direct())
+        need += wr.packed_bytes(num_experts);
+    if (workspace_bytes < need || (need > 0 && !workspace))
+        return MXQ_ERR_WORKSPACE;
+    if (wide == 0 && !(grad_x && rows > 0))
+        return MXQ_OK;
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    Room room = {reinterpret_cast<char *>(workspace), nullptr};
+    LinearArgs a = {};
+    a.offs = offs;
+    a.experts = num_experts;
+    a.rows = (int)rows;
+    a.width = (int)width;
+    a.wide = (int)wide;
+    a.act = activation;
+    float *parts = grad_bias ? reinterpret_cast<float *>(room.take(parts_bytes(rows, num_experts, wide))) : nullptr;
+    Rows z = yr;
+    if (saved) {
+        z = {room.take(zr.packed_bytes(1)), 0, round_up(wide, 8), rows, wide};
+    } else {
+        z = readable(yr, 1, room, st);
+    }
+    if (rows > 0 && wide > 0 && (saved || parts)) {
+        const int64_t slices = slice_count(rows, num_experts, offs != nullptr);
+        const dim3 grid((unsigned)std::min<int64_t>(slices, 1 << 20), (unsigned)((n + 511) / 512));
+        uint16_t *dz = const_cast<uint16_t *>(reinterpret_cast<const uint16_t *>(z.p));
+        auto go = [&](auto kernel) {
+            kernel<<<grid, dim3(256), 0, st>>>(a, grad_y, sg_r, pre, sp_r, saved ? dz : nullptr, z.sr, parts);
+        };
+        gated ? go(linear_dact_kernel<true, true>) : saved ? go(linear_dact_kernel<false, true>) : go(linear_dact_kernel<false, false>);
+    }
+    if (grad_bias && wide > 0)
+        linear_bias_kernel<<<dim3((unsigned)((wide + 255) / 256), (unsigned)num_experts), dim3(256), 0, st>>>(a, parts, grad_bias);
+    a.p = reinterpret_cast<const char *>(z.p);
+    a.ldp = z.sr * 2;
+    a.n = (int)width;
+    mxq_status status = launch_status();
+    if (grad_x && status == MXQ_OK && rows > 0 && width > 0) {
+        const Rows wo = readable(wr, num_experts, room, st);
+        LinearArgs b = a;
+        b.q = reinterpret_cast<const char *>(wo.p);
+        b.ldq = wo.sr * 2;
+        b.qe = wo.se * 2;
+        b.out = grad_x;
+        b.so = sdx_r;
+        status = launch<kGradX, TileSmall, false, false>(b, st);
+    }
+    if (grad_w && status == MXQ_OK && wide > 0 && width > 0) {
+        const Rows xo = readable(xr, 1, room, st);
+        LinearArgs b = a;
+        b.q = reinterpret_cast<const char *>(xo.p);
+        b.ldq = xo.sr * 2;
+        b.out = grad_w;
+        b.so = sdw_n;
+        b.oe = sdw_e;
+        status = launch<kGradW, TileSmall, false, false>(b, st);
+    }
+    return status;
+}
+
+}  // extern "C"

@@ -1,0 +1,208 @@
+"""The experts' products: grouped rows (``moe_dispatch``) times their expert's
+weights with bias, activation, gate and residual in the product's kernel, in
+bf16 with gradients and on MXFP8 operands.
+
+Tensor-level binding over the C ABI in ``include/mxq.h`` like the rest of the
+package: shapes and types are checked, outputs allocated with torch, device
+pointers and the HIP stream forwarded.  With a ``stream`` the outputs are
+allocated on that stream.
+"""
+from __future__ import annotations
+
+from . import MXQError, _check, _torch
+from ._capi import (MXQ_ACT_GELU, MXQ_ACT_NONE, MXQ_ACT_RELU, MXQ_ACT_SILU, MXQ_BF16, MXQ_ERR_INVALID_ARG, MXQ_F32,
+                    mxq_moe_linear, mxq_moe_linear_backward, mxq_moe_linear_backward_workspace_bytes,
+                    mxq_moe_linear_mx, mxq_moe_linear_mx_workspace_bytes, mxq_moe_linear_workspace_bytes)
+from .moe import _plain, _run, _unit
+
+ACTIVATIONS = {"none": MXQ_ACT_NONE, "relu": MXQ_ACT_RELU, "gelu": MXQ_ACT_GELU, "silu": MXQ_ACT_SILU}
+
+
+def _activation(name: str) -> int:
+    try:
+        return ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}") from None
+
+
+def _tensor(t, dtype, ndim: int, device, name: str) -> None:
+    if t.dtype is not dtype or t.dim() != ndim or t.device != device or not t.is_cuda:
+        raise TypeError(f"{name} must be a {ndim}-D {dtype} tensor on {device if device.type == 'cuda' else 'a GPU'}, "
+                        f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _rows(t, shape, device, name: str) -> None:
+    _tensor(t, _torch().bfloat16, 2, device, name)
+    if t.shape != shape:
+        raise TypeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _aligned(*tensors) -> int:
+    """Every operand's rows start on 16 bytes and do not overlap."""
+    for t in tensors:
+        if t.data_ptr() % 16 or any(s % 8 for s in t.stride()[:-1]) or t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
+            return 0
+    return 1
+
+
+def _experts(w, x_width: int, offs, device, dtype, name: str):
+    """w as (E, wide, width) and E, wide; the groups checked."""
+    torch = _torch()
+    if w.dim() == 2:
+        w = w[None]
+    _tensor(w, dtype, 3, device, name)
+    if w.shape[2] != x_width:
+        raise TypeError(f"{name} must have {x_width} columns like x, got {tuple(w.shape)}")
+    if offs is not None:
+        _plain(offs, torch.int32, (w.shape[0],), device, "offs")
+    elif w.shape[0] != 1:
+        raise TypeError(f"{name} of {w.shape[0]} experts needs offs, their group ends")
+    return w
+
+
+class _Epilogue:
+    """Bias, activation, gate and residual of a call, checked, and its
+    outputs."""
+
+    def __init__(self, rows, E, wide, device, bias, activation, gated, residual):
+        torch = _torch()
+        self.act, self.gated = _activation(activation), int(bool(gated))
+        if self.gated and wide % 2:
+            raise TypeError(f"a gated product needs an even number of weight rows, got {wide}")
+        self.n = wide // 2 if self.gated else wide
+        if bias is not None:
+            if bias.dim() == 1:
+                bias = bias[None]
+            if (bias.dtype not in (torch.bfloat16, torch.float32) or bias.shape != (E, wide) or bias.device != device
+                    or wide > 1 and bias.stride(1) != 1):
+                raise TypeError(f"bias must be a bfloat16 or float32 tensor of shape {(E, wide)} and unit stride on "
+                                f"{device}, got {bias.dtype} {tuple(bias.shape)} on {bias.device}")
+        if residual is not None:
+            _rows(residual, (rows, self.n), device, "residual")
+        self.bias, self.residual = bias, residual
+
+    def args(self, y, pre):
+        b, r = self.bias, self.residual
+        return (0 if b is None else b.data_ptr(), MXQ_BF16 if b is not None and b.dtype == _torch().bfloat16 else MXQ_F32,
+                0 if b is None else b.stride(0), self.act, self.gated, 0 if r is None else r.data_ptr(),
+                0 if r is None else r.stride(0), 1 if r is None else r.stride(1), y.data_ptr(), max(self.n, 1), 1,
+                0 if pre is None else pre.data_ptr(), 0 if pre is None else pre.stride(0), 1)
+
+
+def _workspace(need: int, what: str, device):
+    if need < 0:
+        raise MXQError(MXQ_ERR_INVALID_ARG, what)
+    return _torch().empty(need, dtype=_torch().uint8, device=device) if need else None
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def moe_linear(x, w, offs=None, *, bias=None, activation: str = "none", gated: bool = False, residual=None,
+               save_pre: bool = False, stream=None):
+    """Rows ``x`` (rows, width) times their expert's weights ``w`` (experts,
+    wide, width), both bf16: ``act(x W^T + bias) + residual``, or with
+    ``gated`` ``act(first half) * second half + residual`` over wide / 2
+    columns.  ``offs``: int32 group ends on the device (``route.offs``); without
+    them w is one expert's (2-D, or one of 3-D) and takes every row.
+    ``activation``: "none", "relu", "gelu" or "silu"; ``bias`` (experts, wide),
+    bf16 or fp32; ``residual`` (rows, n) bf16.  Returns y (rows, n) bf16, rows
+    past the last group zeros; with ``save_pre`` also what the activation took
+    (rows, wide), for ``moe_linear_backward``."""
+    torch = _torch()
+    _tensor(x, torch.bfloat16, 2, x.device, "x")
+    rows, width = x.shape
+    w = _experts(w, width, offs, x.device, torch.bfloat16, "w")
+    E, wide, _ = w.shape
+    ep = _Epilogue(rows, E, wide, x.device, bias, activation, gated, residual)
+
+    def call(st):
+        y = torch.empty((rows, ep.n), dtype=x.dtype, device=x.device)
+        pre = torch.empty((rows, wide), dtype=x.dtype, device=x.device) if save_pre else None
+        need = mxq_moe_linear_workspace_bytes(rows, width, E, wide, _aligned(x, w))
+        ws = _workspace(need, "mxq_moe_linear", x.device)
+        code = mxq_moe_linear(x.data_ptr(), rows, width, *x.stride(), w.data_ptr(), E, wide, *w.stride(), _ptr(offs),
+                              *ep.args(y, pre), _ptr(ws), max(need, 0), st)
+        _check(code, "mxq_moe_linear")
+        return (y, pre) if save_pre else y
+
+    return _run(x, stream, call)
+
+
+def moe_linear_backward(grad_y, x, w, offs=None, *, pre=None, activation: str = "none", gated: bool = False,
+                        bias: bool = False, need_x: bool = True, need_w: bool = True, stream=None):
+    """Gradients of ``moe_linear``: ``(grad_x, grad_w, grad_bias)``, bf16, bf16
+    and fp32 (experts, wide), None for what is not asked for.  ``pre`` is what
+    the forward call saved, needed with an activation or a gate.  The
+    residual's gradient is ``grad_y`` itself."""
+    torch = _torch()
+    _tensor(x, torch.bfloat16, 2, x.device, "x")
+    rows, width = x.shape
+    w = _experts(w, width, offs, x.device, torch.bfloat16, "w")
+    E, wide, _ = w.shape
+    ep = _Epilogue(rows, E, wide, x.device, None, activation, gated, None)
+    _rows(grad_y, (rows, ep.n), x.device, "grad_y")
+    saved = ep.act != MXQ_ACT_NONE or ep.gated
+    if saved:
+        if pre is None:
+            raise TypeError("an activation or a gate needs pre, what moe_linear(..., save_pre=True) returned")
+        _rows(pre, (rows, wide), x.device, "pre")
+
+    def call(st):
+        g = _unit(grad_y)
+        new = lambda *s, dtype=x.dtype: torch.empty(s, dtype=dtype, device=x.device)  # noqa: E731
+        dx = new(rows, width) if need_x else None
+        dw = new(E, wide, width) if need_w else None
+        db = new(E, wide, dtype=torch.float32) if bias else None
+        need = mxq_moe_linear_backward_workspace_bytes(rows, width, E, wide, ep.act, ep.gated, int(bool(bias)),
+                                                       _aligned(g, x, w))
+        ws = _workspace(need, "mxq_moe_linear_backward", x.device)
+        code = mxq_moe_linear_backward(
+            g.data_ptr(), *g.stride(), x.data_ptr(), rows, width, *x.stride(), w.data_ptr(), E, wide, *w.stride(),
+            _ptr(offs), pre.data_ptr() if saved else 0, pre.stride(0) if saved else 0, pre.stride(1) if saved else 1,
+            ep.act, ep.gated, _ptr(dx), width, 1, _ptr(dw), wide * width, width, 1, _ptr(db), _ptr(ws), max(need, 0), st)
+        _check(code, "mxq_moe_linear_backward")
+        return dx, dw, db
+
+    return _run(x, stream, call)
+
+
+def moe_linear_mx(x, x_scales, w, w_scales, offs=None, *, bias=None, activation: str = "none", gated: bool = False,
+                  residual=None, save_pre: bool = False, stream=None):
+    """``moe_linear`` on MXFP8 operands with blocks along ``width``: ``x``
+    (rows, width) e4m3 with ``x_scales`` (rows, width / 32) uint8, as
+    ``quantize_mx_rowwise`` returns them, ``w`` (experts, wide, width) with
+    ``w_scales`` (experts, wide, width / 32).  Weights quantized along N
+    (``quantize_mx_3d_colwise``) are the operands of the product with their
+    transposes, which is the gradient with respect to x:
+    ``moe_linear_mx(*quantize_mx_rowwise(grad_z), q.transpose(1, 2),
+    scales.transpose(1, 2), offs)``."""
+    torch = _torch()
+    f8 = torch.float8_e4m3fn
+    _tensor(x, f8, 2, x.device, "x")
+    rows, width = x.shape
+    w = _experts(w, width, offs, x.device, f8, "w")
+    E, wide, _ = w.shape
+    if w_scales.dim() == 2:
+        w_scales = w_scales[None]
+    for t, shape, name in ((x_scales, (rows, width // 32), "x_scales"), (w_scales, (E, wide, width // 32), "w_scales")):
+        _tensor(t, torch.uint8, len(shape), x.device, name)
+        if t.shape != shape or width % 32:
+            raise TypeError(f"{name} must have shape {shape} for blocks of 32 of {width}, got {tuple(t.shape)}")
+    ep = _Epilogue(rows, E, wide, x.device, bias, activation, gated, residual)
+
+    def call(st):
+        y = torch.empty((rows, ep.n), dtype=torch.bfloat16, device=x.device)
+        pre = torch.empty((rows, wide), dtype=torch.bfloat16, device=x.device) if save_pre else None
+        words = all(t.data_ptr() % 4 == 0 and t.stride(-1) == 1 and not any(s % 4 for s in t.stride()[:-1])
+                    for t in (x_scales, w_scales))
+        need = mxq_moe_linear_mx_workspace_bytes(rows, width, E, wide, int(words))
+        ws = _workspace(need, "mxq_moe_linear_mx", x.device)
+        code = mxq_moe_linear_mx(x.data_ptr(), rows, width, *x.stride(), x_scales.data_ptr(), *x_scales.stride(),
+                                 w.data_ptr(), E, wide, *w.stride(), w_scales.data_ptr(), *w_scales.stride(), _ptr(offs),
+                                 *ep.args(y, pre), _ptr(ws), max(need, 0), st)
+        _check(code, "mxq_moe_linear_mx")
+        return (y, pre) if save_pre else y
+
+    return _run(x, stream, call)

@@ -1,0 +1,255 @@
+"""The experts' products and their gradients against plain 64-bit forms, over
+tile edges, odd sizes, group layouts, epilogues, strides and alignments."""
+import pytest
+import torch
+
+import linear_reference as ref
+import mxfp8_quantization_moe_amd as mxq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+HALF = 2.0 ** -8   # one rounding to bf16
+SUM = 2.0 ** -23   # one addition on the matrix cores, as if it truncated
+
+
+def offsets(sizes):
+    return torch.tensor(sizes).cumsum(0).to(torch.int32).to(DEV)
+
+
+def normal(*shape, seed=0, scale=1.0, pad=0, shift=0):
+    """bf16 with a row stride of cols + pad, `shift` elements into a buffer of NaN."""
+    g = torch.Generator().manual_seed(seed)
+    x = (scale * torch.randn(*shape, generator=g)).to(torch.bfloat16)
+    if not pad and not shift:
+        return x.to(DEV)
+    *lead, rows, cols = shape
+    count = lead[0] if lead else 1
+    ld = cols + pad
+    buf = torch.full((count * rows * ld + shift + 8,), float("nan"), dtype=torch.bfloat16, device=DEV)
+    strides = ((rows * ld,) if lead else ()) + (ld, 1)
+    v = buf[shift:].as_strided(shape, strides)
+    v.copy_(x)
+    return v
+
+
+def near(got, want, bound, what):
+    bad = ~((got.double() - want).abs() <= bound)
+    assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:4].tolist(), got[bad][:4].tolist(), want[bad][:4].tolist())
+
+
+def make(rows, width, n, sizes, gated, bias, resid, pad=0, shift=0, seed=0):
+    E = len(sizes) if sizes is not None else 1
+    wide = 2 * n if gated else n
+    x = normal(rows, width, seed=seed, pad=pad, shift=shift)
+    w = normal(E, wide, width, seed=seed + 1, scale=max(width, 1) ** -0.5, pad=pad, shift=shift)
+    offs = offsets(sizes) if sizes is not None else None
+    b = None
+    if bias is not None:
+        b = (0.3 * torch.randn(E, wide, generator=torch.Generator().manual_seed(seed + 2))).to(bias).to(DEV)
+    r = normal(rows, n, seed=seed + 3, pad=pad, shift=shift) if resid else None
+    return x, w, offs, b, r
+
+
+def check(rows, width, n, sizes=None, act="none", gated=False, bias=None, resid=False, grad=True, **kw):
+    x, w, offs, b, r = make(rows, width, n, sizes, gated, bias, resid, **kw)
+    saves = act != "none" or gated
+    y, pre = mxq.moe_linear(x, w, offs, bias=b, activation=act, gated=gated, residual=r, save_pre=True)
+    xd, wd, ends = x.double(), w.double(), None if offs is None else offs.tolist()
+    wy, wz, size = ref.forward(xd, wd, ends, b, act, gated, r)
+    assert y.dtype == torch.bfloat16 and y.shape == wy.shape and pre.shape == wz.shape
+    terms = (width + 8) * SUM
+    # GELU's cdf is 2e-7 off, times z (and the gate's value)
+    near(y, wy, HALF * wy.abs() + (1 + HALF) * terms * size + 4e-7 * size + 1e-30, "y")
+    near(pre, wz, HALF * wz.abs() + terms * ref.forward(xd, wd, ends, b)[2] / 1.13 * 1.01 + 1e-30, "pre")
+    if not grad:
+        return
+    dy = normal(rows, n, seed=11, pad=kw.get("pad", 0), shift=kw.get("shift", 0))
+    gx, gw, gb = mxq.moe_linear_backward(dy, x, w, offs, pre=pre if saves else None, activation=act, gated=gated, bias=True)
+    used = torch.zeros(rows, 1, dtype=torch.bool, device=DEV)
+    for lo, hi in ref.groups(ends, rows):
+        used[lo:hi] = True
+    dz = torch.where(used, ref.grad_z(dy.double(), pre.double(), act, gated), 0.0)
+    want = ref.backward(dz, xd, wd, ends)
+    sizes_ = ref.backward(dz.abs(), xd.abs(), wd.abs(), ends)
+    # dz in bf16: each of its values half a step off (and the activation's own
+    # few fp32 roundings), none without activation
+    rounding = HALF * 1.01 if saves else 0.0
+    longest = max([hi - lo for lo, hi in ref.groups(ends, rows)] + [0])
+    for got, wnt, sz, terms_, what in ((gx, want[0], sizes_[0], w.shape[1], "grad_x"), (gw, want[1], sizes_[1], longest, "grad_w")):
+        assert got.dtype == torch.bfloat16 and got.shape == wnt.shape
+        near(got, wnt, HALF * wnt.abs() + (rounding + (terms_ + 8) * SUM) * 1.01 * sz + 1e-30, what)
+        # independent roundings: a third of their squares' bound on average, for
+        # dz and for the result
+        if wnt.numel() > 256:
+            off = torch.linalg.vector_norm(got.double() - wnt) / torch.linalg.vector_norm(wnt).clamp(min=1e-30)
+            assert off < (1.2 if saves else 0.75) * HALF, (what, float(off))
+    # fp32 activations (8 roundings, GELU 4e-7 of the slope) and slices of 64
+    # rows in fp32, slices in fp64
+    assert gb.dtype == torch.float32
+    near(gb, want[2], (16 + 8 + 4) * 2.0 ** -23 * sizes_[2] + 6e-7 * ref.backward(dy.double().abs().repeat(1, 2 if gated else 1) * (1 + pre.double().abs().amax() if gated else 1.0), xd.abs(), wd.abs(), ends)[2] + 1e-30, "grad_bias")
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_epilogues(act, gated):
+    check(150, 192, 96, [70, 0, 64, 10], act, gated, torch.float32, True)
+    check(150, 192, 96, [70, 0, 64, 10], act, gated, torch.bfloat16)
+    check(150, 192, 96, None, act, gated)
+
+
+@pytest.mark.parametrize("width", [1, 7, 8, 9, 31, 32, 56, 63, 64, 65, 128, 200, 777, 1024])
+def test_widths(width):
+    check(70, width, 64, [33, 37], "silu", True, torch.float32)
+    check(70, width, 72, [33, 37])
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 6, 7, 8, 13, 16, 33, 63, 64, 65, 127, 128, 130, 257, 515])
+def test_result_widths(n):
+    check(70, 96, n, [33, 37], "gelu", True, torch.float32, True)
+    check(70, 96, n, [33, 37], "relu", False, None, True)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 63, 64, 65, 128, 129, 300, 1025])
+def test_rows(rows):
+    check(rows, 136, 80, None, "silu", True, torch.float32)
+    check(rows, 136, 80, [rows // 3, 0, rows - rows // 3], "none")
+
+
+@pytest.mark.parametrize("sizes,rows", [([0, 0, 0], 40), ([0], 7), ([5], 40), ([0, 40, 0], 40), ([1] * 40, 40),
+                                        ([3, 0] * 70, 256), ([64, 64, 64], 200), ([0] * 130 + [17] + [0] * 130, 20)])
+def test_groups_and_rows_behind_the_last(sizes, rows):
+    check(rows, 64, 48, sizes, "relu", False, torch.float32, True)
+    check(rows, 64, 48, sizes, "silu", True)
+
+
+@pytest.mark.parametrize("pad,shift", [(0, 1), (1, 0), (8, 0), (8, 8), (3, 5), (64, 16)])
+def test_strides_and_alignment(pad, shift):
+    check(80, 104, 72, [31, 49], "gelu", False, torch.float32, True, pad=pad, shift=shift)
+    check(80, 104, 72, [31, 49], "none", False, None, False, pad=pad, shift=shift)
+    check(80, 104, 72, [31, 49], "silu", True, None, True, pad=pad, shift=shift)
+
+
+def test_repeated_rows():
+    """One row for all tokens, one matrix for all experts, an expanded gradient."""
+    x, w, offs, _, _ = make(90, 64, 64, [40, 50], False, None, False)
+    xe, we = x[:1].expand(90, 64), w[:1].expand(2, 64, 64)
+    y = mxq.moe_linear(xe, we, offs)
+    wy, _, size = ref.forward(xe.double(), we.double(), offs.tolist())
+    near(y, wy, HALF * wy.abs() + 80 * SUM * size, "y")
+    dy = torch.ones((), dtype=torch.bfloat16, device=DEV).expand(90, 64)
+    got = mxq.moe_linear_backward(dy, xe, we, offs, bias=True)
+    want = mxq.moe_linear_backward(dy.contiguous(), xe.contiguous(), we.contiguous(), offs, bias=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_offsets_outside_the_rows_are_cut():
+    x, w, _, _, _ = make(50, 64, 64, [20, 30], False, None, False)
+    y = mxq.moe_linear(x, w, torch.tensor([-5, 1000], dtype=torch.int32, device=DEV))
+    want = mxq.moe_linear(x, w, torch.tensor([0, 50], dtype=torch.int32, device=DEV))
+    assert torch.equal(y, want)
+
+
+def test_nothing_to_do():
+    new = lambda *s: torch.ones(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    zero = torch.zeros(3, dtype=torch.int32, device=DEV)
+    assert mxq.moe_linear(new(0, 8), new(3, 4, 8), zero).shape == (0, 4)
+    assert mxq.moe_linear(new(5, 8), new(1, 0, 8)).shape == (5, 0)
+    gx, gw, gb = mxq.moe_linear_backward(new(0, 4), new(0, 8), new(3, 4, 8), zero, bias=True)
+    assert gx.shape == (0, 8) and not gw.any() and not gb.any()
+    # no columns to sum over: the bias alone
+    b = torch.arange(4.0, device=DEV)
+    assert torch.equal(mxq.moe_linear(new(5, 0), new(1, 4, 0), bias=b).float(), b.expand(5, 4))
+    gx, gw, gb = mxq.moe_linear_backward(new(5, 0), new(5, 8), new(1, 0, 8), bias=True)
+    assert not gx.any() and gw.shape == (1, 0, 8) and gb.shape == (1, 0)
+
+
+def test_infinities_stay_in_their_rows():
+    """Neither a row of another group nor what lies past an operand reaches a result."""
+    x, w, offs, _, _ = make(100, 72, 64, [30, 40, 20], False, None, False)
+    want = mxq.moe_linear(x, w, offs)
+    x[29], x[35] = float("nan"), float("inf")
+    x[90:] = float("nan")
+    y = mxq.moe_linear(x, w, offs)
+    keep = [r for r in range(100) if r not in (29, 35)]
+    assert torch.equal(y[keep], want[keep]) and y[29].isnan().all()
+    gw = mxq.moe_linear_backward(want, x, w, offs)[1]
+    assert gw[0].isnan().all() and not gw[2].isnan().any()
+
+
+def test_equal_calls_give_equal_bits():
+    x, w, offs, b, _ = make(1000, 512, 264, [333, 0, 500, 100], True, torch.float32, False)
+    first = None
+    for _ in range(3):
+        y, pre = mxq.moe_linear(x, w, offs, bias=b, activation="silu", gated=True, save_pre=True)
+        out = (y, pre) + mxq.moe_linear_backward(y, x, w, offs, pre=pre, activation="silu", gated=True, bias=True)
+        first = first or out
+        assert all(torch.equal(a, c) for a, c in zip(first, out))
+
+
+def test_on_another_stream():
+    x, w, offs, b, _ = make(500, 260, 100, [200, 290], False, torch.float32, False)
+    want = mxq.moe_linear(x, w, offs, bias=b, activation="gelu")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    y = mxq.moe_linear(x, w, offs, bias=b, activation="gelu", stream=s)
+    s.synchronize()
+    assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------- MXFP8
+
+def mx(x):
+    """Both parts of a bf16 matrix (or stack of them) in blocks along the last dim."""
+    flat = x.reshape(-1, x.shape[-1])
+    q, s = mxq.quantize_mx_rowwise(flat)
+    return q.reshape(x.shape), s.reshape(*x.shape[:-1], -1)
+
+
+# The scaled matrix instruction aligns the products of a group of up to 16 to
+# the largest of them, m, and cuts what lies below 2^-13 m: 1 - 1 + 2^-13 is
+# 2^-13 and 1 - 1 + 2^-14 is 0 within a group (a product of two e4m3 values has
+# 8 bits, so the largest loses nothing).  At most 15 products of a group lose at
+# most 2^-13 m each, and m is at most the sum of their magnitudes: 15 * 2^-13 <
+# 2^-9 of it, which summed over the groups is 2^-9 of the whole sum's.
+MX_SUM = 2.0 ** -9
+
+
+def check_mx(rows, width, n, sizes=None, act="none", gated=False, bias=None, resid=False):
+    x, w, offs, b, r = make(rows, width, n, sizes, gated, bias, resid)
+    # blocks of very different size: the scales matter
+    x = x * torch.exp2(torch.randint(-9, 10, (rows, width // 32), generator=torch.Generator().manual_seed(5)).to(DEV).repeat_interleave(32, 1)).to(x.dtype)
+    (xq, xs), (wq, ws) = mx(x), mx(w)
+    y, pre = mxq.moe_linear_mx(xq, xs, wq, ws, offs, bias=b, activation=act, gated=gated, residual=r, save_pre=True)
+    xd, wd, ends = ref.mx_values(xq, xs), ref.mx_values(wq, ws), None if offs is None else offs.tolist()
+    wy, wz, size = ref.forward(xd, wd, ends, b, act, gated, r)
+    terms = MX_SUM + (width + 8) * SUM
+    near(y, wy, HALF * wy.abs() + (1 + HALF) * terms * size + 4e-7 * size + 1e-30, "y")
+    near(pre, wz, HALF * wz.abs() + terms * ref.forward(xd, wd, ends, b)[2] / 1.13 * 1.01 + 1e-30, "pre")
+    if pre.numel() > 256:  # those cuts point either way: in the 2-norm the rounding to bf16 alone is left
+        assert torch.linalg.vector_norm(pre.double() - wz) < 0.75 * HALF * torch.linalg.vector_norm(wz)
+
+
+@pytest.mark.parametrize("width", [32, 64, 96, 128, 160, 256, 480, 512, 1056, 2080])
+def test_mx_widths(width):
+    check_mx(70, width, 72, [33, 37])
+    check_mx(70, width, 40, [33, 37], "silu", True, torch.float32, True)
+
+
+@pytest.mark.parametrize("rows,n,sizes", [(1, 1, None), (17, 7, None), (64, 64, None), (129, 200, [0, 100, 29]),
+                                          (300, 130, [64, 64, 0, 101]), (40, 48, [1] * 40)])
+def test_mx_sizes(rows, n, sizes):
+    for gated in (False, True):
+        check_mx(rows, 320, n, sizes, "gelu", gated, torch.bfloat16)
+
+
+def test_mx_weights_along_n():
+    """Weights quantized along N are the operands of the product with their transposes."""
+    rows, K, N, sizes = 90, 96, 160, [40, 50]
+    dz, w = normal(rows, N, seed=1), normal(2, N, K, seed=2)
+    q, s = mxq.quantize_mx_3d_colwise(w)
+    dq, ds = mxq.quantize_mx_rowwise(dz)
+    offs = offsets(sizes)
+    y = mxq.moe_linear_mx(dq, ds, q.transpose(1, 2), s.transpose(1, 2), offs)
+    wd = ref.mx_values(q.transpose(1, 2), s.transpose(1, 2).contiguous())
+    wy, _, size = ref.forward(ref.mx_values(dq, ds), wd, offs.tolist())
+    near(y, wy, HALF * wy.abs() + (MX_SUM + 170 * SUM) * size, "y")
