@@ -613,6 +613,56 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
                              void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
+ * A whole mixture-of-experts layer for a few tokens (a decoding step):
+ *
+ *   ids_t, s_t = experts and weights as mxq_moe_route gives them for logits_t
+ *   h_tj = act(U_e x_t + a_e)                 gated = 0, e = ids_tj
+ *   h_tj = act(z[:hidden]) * z[hidden:]       gated = 1, z = U_e x_t + a_e
+ *   y_t  = residual_t + sum_j s_tj (D_e h_tj + b_e)
+ *
+ * Empty slots (a masked token, no expert left) add nothing.  Sums are fp32, h
+ * passes between the products with 16 bits or more, y is rounded once to bf16.
+ * The order of a sum depends on the extents and on the experts that the tokens
+ * take, not on the call: equal calls give equal bits.
+ *
+ * tokens <= MXQ_LAYER_MAX_TOKENS, num_experts <= MXQ_LAYER_MAX_EXPERTS, width,
+ * hidden <= 65536.  More tokens: mxq_moe_route, mxq_moe_dispatch,
+ * mxq_moe_linear (twice) and mxq_moe_combine.
+ *
+ * x           (tokens, width) bf16, strides (sx_t, sx_c).
+ * logits      (tokens, num_experts) of logits_dtype, strides (sl_t, sl_e);
+ *             token_mask, top_k, renormalize as mxq_moe_route takes them.
+ * format      of both weights.  MXQ_WEIGHTS_BF16: up (num_experts, wide, width),
+ *             wide = hidden or (gated) 2 hidden, down (num_experts, width,
+ *             hidden), bf16, scales NULL.  MXQ_WEIGHTS_MX: e4m3 of the same
+ *             shapes, with e8m0 scales of blocks of 32 along their last dim
+ *             (width % 32 == 0, hidden % 32 == 0, matrices on 16 bytes, strides
+ *             multiples of 16).  Their values enter the products exactly.
+ * bias_up     NULL, or (num_experts, wide), bias_down NULL, or (num_experts,
+ *             width), both of bias_dtype, unit stride, sbu_e and sbd_e from
+ *             expert to expert.
+ * residual    NULL, or (tokens, width) bf16; y (tokens, width) bf16.
+ * The last dim of every operand has unit stride (else MXQ_ERR_UNSUPPORTED).
+ * workspace   mxq_moe_layer_workspace_bytes bytes, 16-byte aligned, contents
+ *             arbitrary before and after; too small -> MXQ_ERR_WORKSPACE.
+ */
+#define MXQ_LAYER_MAX_TOKENS 64
+#define MXQ_LAYER_MAX_EXPERTS 1024
+typedef enum mxq_weights { MXQ_WEIGHTS_BF16 = 0, MXQ_WEIGHTS_MX = 1 } mxq_weights;
+
+int64_t mxq_moe_layer_workspace_bytes(int64_t tokens, int64_t width, int64_t hidden, int32_t num_experts, int32_t top_k);
+mxq_status mxq_moe_layer(const uint16_t *x, int64_t tokens, int64_t width, int64_t sx_t, int64_t sx_c,
+                         const void *logits, int32_t logits_dtype, int32_t num_experts, int64_t sl_t, int64_t sl_e,
+                         const uint8_t *token_mask, int32_t top_k, int32_t renormalize, int64_t hidden, int32_t format,
+                         const void *up, const uint8_t *up_scales, int64_t su_e, int64_t su_r, int64_t su_c,
+                         int64_t sus_e, int64_t sus_r, int64_t sus_b, const void *bias_up, const void *down,
+                         const uint8_t *down_scales, int64_t sd_e, int64_t sd_r, int64_t sd_c, int64_t sds_e,
+                         int64_t sds_r, int64_t sds_b, const void *bias_down, int32_t bias_dtype, int64_t sbu_e,
+                         int64_t sbd_e, int32_t activation, int32_t gated, const uint16_t *residual, int64_t sr_t,
+                         int64_t sr_c, uint16_t *y, int64_t sy_t, int64_t sy_c, void *workspace,
+                         int64_t workspace_bytes, void *stream);
+
+/*
  * TEST-ONLY diagnostics, not part of the quantization API: the library's own
  * device conversions applied to n fp32 values, so that tests can check them
  * against the CPU definition over whole fp32 ranges.  y: n floats, out: n

@@ -31,7 +31,8 @@ from ._capi import (MXQ_ERR_INVALID_ARG, MXQ_ERR_LAUNCH, MXQ_ERR_UNSUPPORTED, MX
                     mxq_moe_row_capacity, mxq_muon_orthogonalize, mxq_muon_workspace_bytes,
                     MXQ_ACT_GELU, MXQ_ACT_NONE, MXQ_ACT_RELU, MXQ_ACT_SILU, mxq_moe_linear,
                     mxq_moe_linear_backward, mxq_moe_linear_backward_workspace_bytes, mxq_moe_linear_mx,
-                    mxq_moe_linear_mx_workspace_bytes, mxq_moe_linear_workspace_bytes)
+                    mxq_moe_linear_mx_workspace_bytes, mxq_moe_linear_workspace_bytes, mxq_moe_layer, mxq_moe_layer_workspace_bytes,
+                    MXQ_LAYER_MAX_EXPERTS, MXQ_LAYER_MAX_TOKENS, MXQ_WEIGHTS_BF16, MXQ_WEIGHTS_MX)
 
 __all__ = [
     "quantize_jagged_rowwise", "quantize_jagged_colwise", "quantize_mx_3d_colwise",
@@ -54,6 +55,7 @@ __all__ = [
     "ACTIVATIONS", "moe_linear", "moe_linear_backward", "moe_linear_mx", "mxq_moe_linear",
     "mxq_moe_linear_backward", "mxq_moe_linear_backward_workspace_bytes", "mxq_moe_linear_mx",
     "mxq_moe_linear_mx_workspace_bytes", "mxq_moe_linear_workspace_bytes",
+    "moe_layer", "moe_layer_workspace", "mxq_moe_layer", "mxq_moe_layer_workspace_bytes",
 ]
 
 
@@ -336,4 +338,5 @@ def debug_cast4_e4m3(y, unclamped: bool, *, stream=None):
 from .moe import (MoeRoute, moe_combine, moe_combine_backward, moe_dispatch,  # noqa: E402
                   moe_dispatch_backward, moe_route, moe_route_backward, moe_row_capacity)
 from .muon import MUON_COEFFICIENTS, muon_orthogonalize, muon_workspace  # noqa: E402
-from .linear import ACTIVATIONS, moe_linear, moe_linear_backward, moe_linear_mx  # noqa: E402
+from .linear import (ACTIVATIONS, moe_layer, moe_layer_workspace, moe_linear, moe_linear_backward,  # noqa: E402
+                     moe_linear_mx)

@@ -31,6 +31,10 @@ MXQ_ACT_NONE = 0
 MXQ_ACT_RELU = 1
 MXQ_ACT_GELU = 2
 MXQ_ACT_SILU = 3
+MXQ_WEIGHTS_BF16 = 0
+MXQ_WEIGHTS_MX = 1
+MXQ_LAYER_MAX_TOKENS = 64
+MXQ_LAYER_MAX_EXPERTS = 1024
 
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
@@ -89,13 +93,18 @@ SIGNATURES = {
     "mxq_moe_linear_mx": [_vp, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _i64,
                           _i64, _vp, _vp, _i32, _i64, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
                           _i64, _vp],
+    "mxq_moe_layer_workspace_bytes": [_i64, _i64, _i64, _i32, _i32],
+    "mxq_moe_layer": [_vp, _i64, _i64, _i64, _i64, _vp, _i32, _i32, _i64, _i64, _vp, _i32, _i32, _i64, _i32,
+                      _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i64, _vp,
+                      _i32, _i64, _i64, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp],
     "mxq_debug_cast_e4m3": [_vp, _i64, _vp, _vp],
     "mxq_debug_cast4_e4m3": [_vp, _i64, _vp, _i32, _vp],
 }
 RESTYPES = {"mxq_status_string": ctypes.c_char_p, "mxq_jagged_colwise_workspace_bytes": _i64,
             "mxq_moe_row_capacity": _i64, "mxq_moe_route_workspace_bytes": _i64,
             "mxq_muon_workspace_bytes": _i64, "mxq_moe_linear_workspace_bytes": _i64,
-            "mxq_moe_linear_backward_workspace_bytes": _i64, "mxq_moe_linear_mx_workspace_bytes": _i64}
+            "mxq_moe_linear_backward_workspace_bytes": _i64, "mxq_moe_linear_mx_workspace_bytes": _i64,
+            "mxq_moe_layer_workspace_bytes": _i64}
 
 _lib = None
 
@@ -163,5 +172,7 @@ mxq_moe_linear_backward_workspace_bytes = _fwd("mxq_moe_linear_backward_workspac
 mxq_moe_linear_backward = _fwd("mxq_moe_linear_backward")
 mxq_moe_linear_mx_workspace_bytes = _fwd("mxq_moe_linear_mx_workspace_bytes")
 mxq_moe_linear_mx = _fwd("mxq_moe_linear_mx")
+mxq_moe_layer_workspace_bytes = _fwd("mxq_moe_layer_workspace_bytes")
+mxq_moe_layer = _fwd("mxq_moe_layer")
 mxq_debug_cast_e4m3 = _fwd("mxq_debug_cast_e4m3")
 mxq_debug_cast4_e4m3 = _fwd("mxq_debug_cast4_e4m3")

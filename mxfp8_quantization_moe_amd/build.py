@@ -13,13 +13,14 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmxq.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("api.hip", "moe_api.hip", "muon_api.hip", "linear_api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("api.hip", "moe_api.hip", "muon_api.hip", "linear_api.hip",
+                                            "moe_layer_api.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in ("mxq_device.hpp", "wave_ops.hpp", "jagged_kernels.hpp",
                                             "jagged_mx_kernels.hpp", "block_kernels.hpp", "group_tables.hpp",
                                             "colwise_tile_kernels.hpp",
                                             "relayout_kernels.hpp", "api_common.hpp",
                                             "moe_route_kernels.hpp", "moe_rows_kernels.hpp", "muon_kernels.hpp",
-                                            "tile_ops.hpp", "linear_kernels.hpp")] + [os.path.join(ROOT, "include", "mxq.h")]
+                                            "tile_ops.hpp", "linear_ops.hpp", "linear_kernels.hpp", "moe_layer_kernels.hpp")] + [os.path.join(ROOT, "include", "mxq.h")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

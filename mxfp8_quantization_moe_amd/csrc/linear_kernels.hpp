@@ -26,6 +26,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "linear_ops.hpp"
 #include "moe_rows_kernels.hpp"
 #include "mxq_device.hpp"
 #include "tile_ops.hpp"
@@ -34,8 +35,6 @@
 namespace mxq {
 
 enum LinearMode { kForward, kGradX, kGradW };
-enum LinearAct { kActNone, kActRelu, kActGelu, kActSilu };
-
 // Operands and results of a call; leading strides in bytes for what is read
 // into LDS, else in elements.
 struct LinearArgs {
@@ -66,18 +65,6 @@ __device__ __forceinline__ void group_rows(const int32_t *__restrict__ offs, int
     const int e = offs && g < experts ? min(max(offs[g], 0), rows) : rows;
     start = s;
     len = g <= experts && (offs || g < experts) ? max(e - s, 0) : 0;
-}
-
-__device__ __forceinline__ int wave_scan(int v)
-{
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int y = __shfl_up(v, d, 64);
-        if (lane >= d)
-            v += y;
-    }
-    return v;
 }
 
 // Tiles of TM rows of all groups, the rows behind the last one included.
@@ -273,8 +260,6 @@ struct Panel {
 };
 
 typedef int int8v __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
 // acc += P Q over a stage, fragments I0.. of P.  Q is the first operand: a
 // lane's four results lie along j.  The scaled product takes both halves of a
 // stage at once (128 values of k): lane 16 b + i holds bytes 16 b and 64 + 16 b
@@ -419,92 +404,6 @@ __device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT,
 }
 
 // ---------------------------------------------------------------- epilogue
-
-// The normal distribution's cdf at x and exp(-x^2 / 2), by formula 7.1.26 of
-// Abramowitz and Stegun (1964) for erfc: 1.5e-7 absolute, far under the
-// rounding to bf16, in 14 instructions where erff takes 40: results pass here
-// while the matrix units wait.
-__device__ __forceinline__ void normal_cdf(float x, float &cdf, float &e)
-{
-    const float z = fabsf(x), t = __builtin_amdgcn_rcpf(fmaf(z, 0.3275911f * 0.70710678f, 1.0f));
-    float p = fmaf(t, 1.061405429f, -1.453152027f);
-    p = fmaf(t, p, 1.421413741f);
-    p = fmaf(t, p, -0.284496736f);
-    p = fmaf(t, p, 0.254829592f);
-    e = __builtin_amdgcn_exp2f(x * x * -0.72134752f);
-    const float tail = 0.5f * t * p * e;
-    cdf = x >= 0.0f ? 1.0f - tail : tail;
-}
-
-__device__ __forceinline__ float sigmoid(float x)
-{
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
-}
-
-__device__ __forceinline__ float act_value(int act, float x)
-{
-    if (act == kActRelu)
-        return x < 0.0f ? 0.0f : x;  // a NaN stays one
-    if (act == kActGelu) {
-        float cdf, e;
-        normal_cdf(x, cdf, e);
-        return x * cdf;
-    }
-    if (act == kActSilu)
-        return x * sigmoid(x);
-    return x;
-}
-
-// act'(x)
-__device__ __forceinline__ float act_slope(int act, float x)
-{
-    if (act == kActRelu)
-        return x > 0.0f ? 1.0f : 0.0f;
-    if (act == kActGelu) {
-        float cdf, e;
-        normal_cdf(x, cdf, e);
-        return fmaf(x * 0.39894228f, e, cdf);
-    }
-    if (act == kActSilu) {
-        const float s = sigmoid(x);
-        return s * fmaf(x, 1.0f - s, 1.0f);
-    }
-    return 1.0f;
-}
-
-__device__ __forceinline__ float bias_at(const void *bias, int f32, int64_t at)
-{
-    return f32 ? reinterpret_cast<const float *>(bias)[at]
-               : Piece<uint16_t>::to_f32(reinterpret_cast<const uint16_t *>(bias)[at]);
-}
-
-// eight elements of bf16 from column c of a row of n, c < n
-__device__ __forceinline__ Piece<uint16_t> load8(const uint16_t *row, int c, int n)
-{
-    if (c + 8 <= n)
-        return ld_piece<uint16_t>(row + c);
-    Piece<uint16_t> r;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        r.v[k] = c + k < n ? row[c + k] : (uint16_t)0;
-    return r;
-}
-
-__device__ __forceinline__ void store8(uint16_t *row, int c, int n, const float (&v)[8])
-{
-    Piece<uint16_t> r;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        r.set(k, v[k]);
-    if (c + 8 <= n) {
-        st_piece<uint16_t>(row + c, r);
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (c + k < n)
-            row[c + k] = r.v[k];
-}
 
 // Results to memory.  A lane holds row l % 16, columns 4 (l / 16) + 0..3 of
 // each fragment; through LDS (each wave in its own region, RC rows at a time)

@@ -1,6 +1,7 @@
 """The experts' products: grouped rows (``moe_dispatch``) times their expert's
 weights with bias, activation, gate and residual in the product's kernel, in
-bf16 with gradients and on MXFP8 operands.
+bf16 with gradients and on MXFP8 operands; a whole mixture-of-experts layer for
+a few tokens.
 
 Tensor-level binding over the C ABI in ``include/mxq.h`` like the rest of the
 package: shapes and types are checked, outputs allocated with torch, device
@@ -11,7 +12,7 @@ from __future__ import annotations
 
 from . import MXQError, _check, _torch
 from ._capi import (MXQ_ACT_GELU, MXQ_ACT_NONE, MXQ_ACT_RELU, MXQ_ACT_SILU, MXQ_BF16, MXQ_ERR_INVALID_ARG, MXQ_F32,
-                    mxq_moe_linear, mxq_moe_linear_backward, mxq_moe_linear_backward_workspace_bytes,
+                    mxq_moe_layer, mxq_moe_layer_workspace_bytes, mxq_moe_linear, mxq_moe_linear_backward, mxq_moe_linear_backward_workspace_bytes,
                     mxq_moe_linear_mx, mxq_moe_linear_mx_workspace_bytes, mxq_moe_linear_workspace_bytes)
 from .moe import _plain, _run, _unit
 
@@ -204,5 +205,105 @@ def moe_linear_mx(x, x_scales, w, w_scales, offs=None, *, bias=None, activation:
                                  *ep.args(y, pre), _ptr(ws), max(need, 0), st)
         _check(code, "mxq_moe_linear_mx")
         return (y, pre) if save_pre else y
+
+    return _run(x, stream, call)
+
+
+# ---------------------------------------------------------------- a layer for a few tokens
+
+def _weights(w, shape, device, name: str):
+    """(tensor, scales or None) of expert weights: bf16, or MXFP8 as a pair."""
+    torch = _torch()
+    if not isinstance(w, (tuple, list)):
+        _tensor(w, torch.bfloat16, 3, device, name)
+        q, scales = w, None
+    else:
+        q, scales = w
+        _tensor(q, torch.float8_e4m3fn, 3, device, name)
+        _tensor(scales, torch.uint8, 3, device, f"{name}'s scales")
+        blocks = shape[:2] + (shape[2] // 32,)
+        if scales.shape != blocks or shape[2] % 32:
+            raise TypeError(f"{name}'s scales must have shape {blocks} for blocks of 32 of {shape[2]}, got {tuple(scales.shape)}")
+    if q.shape != shape:
+        raise TypeError(f"{name} must have shape {shape}, got {tuple(q.shape)}")
+    return q, scales
+
+
+def _layer_bias(bias, shape, device, name: str):
+    torch = _torch()
+    if bias is None:
+        return 0, 0, MXQ_F32
+    if (bias.dtype not in (torch.bfloat16, torch.float32) or bias.shape != shape or bias.device != device
+            or shape[1] > 1 and bias.stride(1) != 1):
+        raise TypeError(f"{name} must be a bfloat16 or float32 tensor of shape {shape} and unit stride on {device}, got "
+                        f"{bias.dtype} {tuple(bias.shape)} on {bias.device}")
+    return bias.data_ptr(), bias.stride(0), MXQ_BF16 if bias.dtype == torch.bfloat16 else MXQ_F32
+
+
+def moe_layer_workspace(tokens: int, width: int, hidden: int, num_experts: int, top_k: int, device=None):
+    """A workspace for ``moe_layer(..., workspace=ws)`` of this extent; it can
+    be reused by calls that do not overlap in time."""
+    need = mxq_moe_layer_workspace_bytes(tokens, width, hidden, num_experts, top_k)
+    if need < 0:
+        raise MXQError(MXQ_ERR_INVALID_ARG, "mxq_moe_layer_workspace_bytes")
+    return _torch().empty(max(need, 16), dtype=_torch().uint8, device=device or "cuda")
+
+
+def moe_layer(x, logits, up, down, top_k: int, *, activation: str = "silu", gated: bool = True, bias_up=None,
+              bias_down=None, token_mask=None, renormalize: bool = True, residual=None, workspace=None, stream=None):
+    """A whole mixture-of-experts layer for up to 64 tokens ``x`` (tokens,
+    width) bf16: the ``top_k`` experts of their router ``logits`` (tokens,
+    experts), bf16 or fp32, as ``moe_route`` chooses and weighs them; ``up``
+    (experts, hidden or with ``gated`` 2 hidden, width), the activation,
+    ``down`` (experts, width, hidden), the weighted sum and the ``residual``.
+    Weights are bf16 tensors, or pairs ``(q, scales)`` of MXFP8 blocks along
+    their last dim.  Every active expert's weights are read once.  More tokens:
+    ``moe_route``, ``moe_dispatch``, ``moe_linear``, ``moe_combine``."""
+    torch = _torch()
+    _tensor(x, torch.bfloat16, 2, x.device, "x")
+    T, D = x.shape
+    dev = x.device
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32) or logits.device != dev or logits.shape[0] != T:
+        raise TypeError(f"logits must be a bfloat16 or float32 tensor of {T} rows on {dev}, got {logits.dtype} "
+                        f"{tuple(logits.shape)} on {logits.device}")
+    E = logits.shape[1]
+    act = _activation(activation)
+    q = down[0] if isinstance(down, (tuple, list)) else down
+    H = q.shape[-1]
+    wide = 2 * H if gated else H
+    (uq, us), (dq, ds) = _weights(up, (E, wide, D), dev, "up"), _weights(down, (E, D, H), dev, "down")
+    if (us is None) != (ds is None):
+        raise TypeError("up and down must have the same format")
+    bu, bus, bdt = _layer_bias(bias_up, (E, wide), dev, "bias_up")
+    bd, bds, bdt2 = _layer_bias(bias_down, (E, D), dev, "bias_down")
+    if bias_up is not None and bias_down is not None and bdt != bdt2:
+        raise TypeError("bias_up and bias_down must have the same type")
+    if residual is not None:
+        _rows(residual, (T, D), dev, "residual")
+    if token_mask is not None:
+        if token_mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"token_mask must be a bool or uint8 tensor, got {token_mask.dtype}")
+        _plain(token_mask, token_mask.dtype, (T,), dev, "token_mask")
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise TypeError("workspace must be a contiguous CUDA tensor on x's device")
+    k = int(top_k)
+    need = mxq_moe_layer_workspace_bytes(T, D, H, E, k)
+    if need < 0:
+        raise MXQError(MXQ_ERR_INVALID_ARG, "mxq_moe_layer")
+
+    def call(st):
+        y = torch.empty((T, D), dtype=x.dtype, device=dev)
+        ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=dev)
+        none = (0, 0, 0)
+        code = mxq_moe_layer(
+            x.data_ptr(), T, D, *x.stride(), logits.data_ptr(), MXQ_BF16 if logits.dtype == torch.bfloat16 else MXQ_F32, E,
+            *logits.stride(), _ptr(token_mask), k, int(bool(renormalize)), H, int(us is not None),
+            uq.data_ptr(), _ptr(us), *uq.stride(), *(none if us is None else us.stride()), bu,
+            dq.data_ptr(), _ptr(ds), *dq.stride(), *(none if ds is None else ds.stride()), bd,
+            bdt if bias_up is not None else bdt2, bus, bds, act, int(bool(gated)), _ptr(residual),
+            0 if residual is None else residual.stride(0), 1 if residual is None else residual.stride(1), y.data_ptr(), D, 1,
+            ws.data_ptr(), ws.numel() * ws.element_size(), st)
+        _check(code, "mxq_moe_layer")
+        return y
 
     return _run(x, stream, call)
