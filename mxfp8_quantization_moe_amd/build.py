@@ -20,7 +20,7 @@ HEADERS = [os.path.join(CSRC, f) for f in ("mxq_device.hpp", "wave_ops.hpp", "ja
                                             "colwise_tile_kernels.hpp",
                                             "relayout_kernels.hpp", "api_common.hpp",
                                             "moe_route_kernels.hpp", "moe_rows_kernels.hpp", "muon_kernels.hpp",
-                                            "tile_ops.hpp", "linear_ops.hpp", "linear_kernels.hpp", "moe_layer_kernels.hpp")] + [os.path.join(ROOT, "include", "mxq.h")]
+                                            "tile_ops.hpp", "linear_ops.hpp", "stream_ops.hpp", "linear_kernels.hpp", "moe_layer_kernels.hpp")] + [os.path.join(ROOT, "include", "mxq.h")]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -16,7 +16,9 @@ using namespace mxq;
 
 constexpr int64_t kMaxDim = 65536;
 
+// 48 KB of LDS, three workgroups of four waves per CU; 72 KB, two of eight waves
 using TileSmall = LinearTile<64, 64, 2, 2, 3>;
+using TileMedium = LinearTile<64, 128, 2, 4, 3>;
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
@@ -104,6 +106,67 @@ int64_t row_tiles(int64_t rows, int32_t experts, bool grouped, int64_t tm)
     return grouped ? std::min<int64_t>(even + experts, rows) : even;
 }
 
+// Row tiles that groups of about equal length have.
+int64_t usual_row_tiles(int64_t rows, int32_t experts, int64_t tm)
+{
+    if (experts == 1)
+        return (rows + tm - 1) / tm;
+    return 2 * rows >= experts * tm ? rows / tm + experts / 2 : std::min<int64_t>(experts, rows);
+}
+
+constexpr int64_t kCUs = 256;
+
+enum Kernel { kFew, kSmall, kMedium, kLarge };
+
+struct Choice {
+    Kernel kernel;
+    int splits;
+};
+
+// What a product runs on, by its extents alone (cols: result columns, of a gate
+// and its value both).  us per call, weights out of the caches for few rows:
+//   few    up to 16 rows in all: 1 row x 4096 x 4096 12.6 (27 on small tiles), 16
+//          rows x 5120 x 8192 30 (34); 32 rows 43 (35)
+//   large  from 72 large tiles on, that groups fill to a quarter: 4096 rows x
+//          4096 x 4096 100 (medium 164, small 197), over 8 experts 159 (212, 253);
+//          1024 rows over 8 experts 71 (81, 94), in one group (64 tiles) 61 (45, 56);
+//          1024 rows over 64 experts of 2048 x 768 42 (41, 33); grad x of 4096
+//          rows over 8 experts of 2048 x 1024 (80 tiles) 36 (48, 45)
+//   medium more small tiles than the CUs hold at a time, which groups fill: 4096
+//          rows over 64 experts of 1024 x 2048 56 (small 67), 1024 rows x 4096 x
+//          4096 45 (56); 128 rows over 64 gated experts of 2048 x 768 79 (70).
+//          grad x also of small groups: 256 rows over 64 experts of 1024 x 2048 41
+//          (54).  With MXFP8 operands even or slower (1024 x 4096 x 4096 42
+//          against 45, 4096 rows over 64 experts of 2048 x 768 37 against 32)
+//   parts  sums of 16 stages and more with small tiles for half the room or less
+Choice choose(LinearMode mode, bool mx, int64_t rows, int32_t experts, int64_t width, int64_t wide)
+{
+    const int64_t cols = mode == kForward ? wide : width;
+    auto tiles = [&](int64_t tm, int64_t tn) {
+        const int64_t r = mode == kGradW ? experts * ((wide + tm - 1) / tm) : usual_row_tiles(rows, experts, tm);
+        return r * ((cols + tn - 1) / tn);
+    };
+    if (mode == kForward && rows <= 16)
+        return {kFew, 1};
+    if (tiles(256, 256) >= 72 && (mode == kGradW || rows >= 64 * (int64_t)experts))
+        return {kLarge, 1};
+    const int64_t small = tiles(64, 64), room = 3 * kCUs;
+    const int64_t stages = mode == kGradW ? rows / experts / 64 : (mode == kForward ? width : wide) / (mx ? 128 : 64);
+    if (2 * small <= room && stages >= 16 && small > 0)
+        return {kSmall, (int)std::min<int64_t>({(int64_t)16, room / small, stages / 8})};
+    const bool medium = !mx && small > room && (mode != kForward || rows >= 64 * (int64_t)experts);
+    return {medium ? kMedium : kSmall, 1};
+}
+
+// Parts of a product's sums in the workspace: (splits, result rows, columns).
+int64_t parts_bytes(LinearMode mode, int splits, int64_t rows, int32_t experts, int64_t width, int64_t wide)
+{
+    if (splits <= 1)
+        return 0;
+    const int64_t r = mode == kGradW ? experts * wide : rows, c = mode == kForward ? wide : width;
+    return round_up(splits * r * round_up(c, 4) * 4, 256);
+}
+
 // a grid that `spread` covers, or 0 if it is past what one launch takes
 int64_t grid_of(int64_t tiles, int64_t threads)
 {
@@ -111,25 +174,64 @@ int64_t grid_of(int64_t tiles, int64_t threads)
     return g * threads < ((int64_t)1 << 32) && g <= INT32_MAX ? g : 0;
 }
 
-template <int MODE, typename TILE, bool GATED, bool MX>
-mxq_status launch(const LinearArgs &a, hipStream_t st)
+template <int MODE, typename TILE, bool GATED, bool MX, bool SPLIT>
+mxq_status launch_tile(const LinearArgs &a, hipStream_t st)
 {
     const int64_t tj = GATED ? TILE::TN / 2 : TILE::TN, tn = (a.n + tj - 1) / tj;
     const int64_t tm = MODE == kGradW ? (int64_t)a.experts * ((a.wide + TILE::TM - 1) / TILE::TM)
                                       : row_tiles(a.rows, a.experts, a.offs != nullptr, TILE::TM);
-    if (tm * tn == 0)
-        return MXQ_OK;
-    const int64_t grid = grid_of(tm * tn, TILE::THREADS);
+    const int64_t grid = grid_of(tm * tn * (SPLIT ? a.splits : 1), TILE::THREADS);
     if (grid == 0)
         return MXQ_ERR_UNSUPPORTED;
-    linear_kernel<MODE, TILE, GATED, MX><<<dim3((unsigned)grid), dim3(TILE::THREADS), 0, st>>>(a);
+    linear_kernel<MODE, TILE, GATED, MX, SPLIT><<<dim3((unsigned)grid), dim3(TILE::THREADS), 0, st>>>(a);
+    return launch_status();
+}
+
+template <bool GATED, bool MX>
+mxq_status launch_few(const LinearArgs &a, hipStream_t st)
+{
+    const dim3 grid((unsigned)((a.n + 15) / 16), (unsigned)(a.experts + (a.offs ? 1 : 0)));
+    linear_few_kernel<GATED, MX><<<grid, dim3(kFewWaves * 64), 0, st>>>(a);
+    return launch_status();
+}
+
+// `room`: where parts may go
+template <int MODE, bool GATED, bool MX>
+mxq_status launch(LinearArgs a, const Choice &c, Room &room, hipStream_t st)
+{
+    if (a.n == 0 || (MODE == kGradW ? a.wide : a.rows) == 0)
+        return MXQ_OK;
+    if (c.kernel == kLarge) {
+        const int64_t tn = (a.n + 127) / 128, tm = MODE == kGradW ? a.experts * ((a.wide + 255) / 256) : row_tiles(a.rows, a.experts, a.offs != nullptr, 256);
+        if (tm * tn > (1 << 30))
+            return MXQ_ERR_UNSUPPORTED;
+        linear_large_kernel<MODE, GATED, MX><<<dim3((unsigned)kCUs), dim3(LinearLarge::THREADS), 0, st>>>(a);
+        return launch_status();
+    }
+    if constexpr (MODE == kForward)
+        if (c.kernel == kFew)
+            return launch_few<GATED, MX>(a, st);
+    if constexpr (!MX)
+        if (c.kernel == kMedium)
+            return launch_tile<MODE, TileMedium, GATED, MX, false>(a, st);
+    if (c.splits == 1)
+        return launch_tile<MODE, TileSmall, GATED, MX, false>(a, st);
+    const int64_t rows = MODE == kGradW ? (int64_t)a.experts * a.wide : a.rows;
+    a.splits = c.splits;
+    a.ldparts = round_up(MODE == kForward ? a.wide : a.width, 4);
+    a.part_size = rows * a.ldparts;
+    a.parts = reinterpret_cast<float *>(room.take(parts_bytes((LinearMode)MODE, c.splits, a.rows, a.experts, a.width, a.wide)));
+    const mxq_status s = launch_tile<MODE, TileSmall, GATED, MX, true>(a, st);
+    if (s != MXQ_OK)
+        return s;
+    linear_join_kernel<MODE, GATED><<<dim3((unsigned)std::min<int64_t>(rows, 1 << 20), (unsigned)((a.n + 1023) / 1024)), dim3(256), 0, st>>>(a);
     return launch_status();
 }
 
 template <bool MX>
-mxq_status launch_forward(const LinearArgs &a, int gated, hipStream_t st)
+mxq_status launch_forward(const LinearArgs &a, int gated, const Choice &c, Room &room, hipStream_t st)
 {
-    return gated ? launch<kForward, TileSmall, true, MX>(a, st) : launch<kForward, TileSmall, false, MX>(a, st);
+    return gated ? launch<kForward, true, MX>(a, c, room, st) : launch<kForward, false, MX>(a, c, room, st);
 }
 
 // a 2-D operand or result of bf16: rows of unit stride
@@ -154,9 +256,11 @@ int64_t mxq_moe_linear_workspace_bytes(int64_t rows, int64_t width, int32_t num_
 {
     if (!sizes_ok(rows, width, num_experts, wide))
         return -1;
-    if (aligned && width % 8 == 0)
-        return 0;
-    return Rows{nullptr, 0, 0, rows, width}.packed_bytes(1) + Rows{nullptr, 0, 0, wide, width}.packed_bytes(num_experts);
+    const Choice c = choose(kForward, false, rows, num_experts, width, wide);
+    const int64_t parts = parts_bytes(kForward, c.splits, rows, num_experts, width, wide);
+    if (c.kernel == kFew || (aligned && width % 8 == 0))
+        return parts;
+    return parts + Rows{nullptr, 0, 0, rows, width}.packed_bytes(1) + Rows{nullptr, 0, 0, wide, width}.packed_bytes(num_experts);
 }
 
 mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_t sx_r, int64_t sx_c, const uint16_t *w,
@@ -179,14 +283,17 @@ mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_
     if (rows == 0 || n == 0)
         return MXQ_OK;
     const Rows xr = {x, 0, sx_r, rows, width}, wr = {w, sw_e, sw_n, wide, width};
-    const int64_t need = (xr.direct() ? 0 : xr.packed_bytes(1)) + (wr.direct() ? 0 : wr.packed_bytes(num_experts));
+    const Choice choice = choose(kForward, false, rows, num_experts, width, wide);
+    const bool few = choice.kernel == kFew;
+    const int64_t need = (few || xr.direct() ? 0 : xr.packed_bytes(1)) + (few || wr.direct() ? 0 : wr.packed_bytes(num_experts)) +
+                         parts_bytes(kForward, choice.splits, rows, num_experts, width, wide);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return MXQ_ERR_WORKSPACE;
-    if (!reach_ok(wide, wr.direct() ? sw_n * 2 : round_up(width, 8) * 2))
+    if (!few && !reach_ok(wide, wr.direct() ? sw_n * 2 : round_up(width, 8) * 2))
         return MXQ_ERR_UNSUPPORTED;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     Room room = {reinterpret_cast<char *>(workspace), nullptr};
-    const Rows xo = readable(xr, 1, room, st), wo = readable(wr, num_experts, room, st);
+    const Rows xo = few ? xr : readable(xr, 1, room, st), wo = few ? wr : readable(wr, num_experts, room, st);
     LinearArgs a = {};
     a.p = reinterpret_cast<const char *>(xo.p);
     a.ldp = xo.sr * 2;
@@ -209,16 +316,18 @@ mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_
     a.so = sy_r;
     a.pre = pre;
     a.spre = sp_r;
-    return launch_forward<false>(a, gated, st);
+    return launch_forward<false>(a, gated, choice, room, st);
 }
 
 int64_t mxq_moe_linear_mx_workspace_bytes(int64_t rows, int64_t width, int32_t num_experts, int64_t wide, int32_t aligned)
 {
     if (!sizes_ok(rows, width, num_experts, wide) || width % 32)
         return -1;
-    if (aligned && width % 128 == 0)
-        return 0;
-    return Scales{nullptr, 0, 0, 1, rows, width / 32}.packed_bytes(1) +
+    const Choice c = choose(kForward, true, rows, num_experts, width, wide);
+    const int64_t parts = parts_bytes(kForward, c.splits, rows, num_experts, width, wide);
+    if (c.kernel == kFew || (aligned && width % 128 == 0))
+        return parts;
+    return parts + Scales{nullptr, 0, 0, 1, rows, width / 32}.packed_bytes(1) +
            Scales{nullptr, 0, 0, 1, wide, width / 32}.packed_bytes(num_experts);
 }
 
@@ -248,14 +357,17 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
         return MXQ_OK;
     const Scales xs = {x_scales, 0, sxs_r, sxs_b, rows, width / 32};
     const Scales ws = {w_scales, sws_e, sws_n, sws_b, wide, width / 32};
-    const int64_t need = (xs.direct() ? 0 : xs.packed_bytes(1)) + (ws.direct() ? 0 : ws.packed_bytes(num_experts));
+    const Choice choice = choose(kForward, true, rows, num_experts, width, wide);
+    const bool few = choice.kernel == kFew;
+    const int64_t need = (few || xs.direct() ? 0 : xs.packed_bytes(1)) + (few || ws.direct() ? 0 : ws.packed_bytes(num_experts)) +
+                         parts_bytes(kForward, choice.splits, rows, num_experts, width, wide);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return MXQ_ERR_WORKSPACE;
-    if (!reach_ok(wide, sw_n))
+    if (!few && !reach_ok(wide, sw_n))
         return MXQ_ERR_UNSUPPORTED;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     Room room = {reinterpret_cast<char *>(workspace), nullptr};
-    const Scales xo = readable(xs, 1, room, st), wo = readable(ws, num_experts, room, st);
+    const Scales xo = few ? xs : readable(xs, 1, room, st), wo = few ? ws : readable(ws, num_experts, room, st);
     LinearArgs a = {};
     a.p = reinterpret_cast<const char *>(x);
     a.ldp = sx_r;
@@ -267,6 +379,8 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
     a.sq = wo.p;
     a.ldsq = wo.sr;
     a.sqe = wo.se;
+    a.sbp = xo.sb;
+    a.sbq = wo.sb;
     a.offs = offs;
     a.experts = num_experts;
     a.rows = (int)rows;
@@ -283,7 +397,7 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
     a.so = sy_r;
     a.pre = pre;
     a.spre = sp_r;
-    return launch_forward<true>(a, gated, st);
+    return launch_forward<true>(a, gated, choice, room, st);
 }
 
 namespace {
@@ -294,7 +408,7 @@ int64_t slice_count(int64_t rows, int32_t experts, bool grouped)
     return row_tiles(rows, experts, grouped, kSliceRows);
 }
 
-int64_t parts_bytes(int64_t rows, int32_t experts, int64_t wide)
+int64_t slices_bytes(int64_t rows, int32_t experts, int64_t wide)
 {
     return round_up(slice_count(rows, experts, true) * wide * 4, 256);
 }
@@ -307,11 +421,13 @@ int64_t mxq_moe_linear_backward_workspace_bytes(int64_t rows, int64_t width, int
     if (!sizes_ok(rows, width, num_experts, wide) || !act_ok(activation, gated, wide))
         return -1;
     const Rows z = {nullptr, 0, 0, rows, wide}, x = {nullptr, 0, 0, rows, width}, w = {nullptr, 0, 0, wide, width};
-    int64_t need = bias ? parts_bytes(rows, num_experts, wide) : 0;
+    int64_t need = bias ? slices_bytes(rows, num_experts, wide) : 0;
     if (activation != MXQ_ACT_NONE || gated || !aligned || wide % 8)
         need += z.packed_bytes(1);
     if (!aligned || width % 8)
         need += x.packed_bytes(1) + w.packed_bytes(num_experts);
+    for (LinearMode mode : {kGradX, kGradW})
+        need += parts_bytes(mode, choose(mode, false, rows, num_experts, width, wide).splits, rows, num_experts, width, wide);
     return need;
 }
 
@@ -339,13 +455,18 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         return MXQ_ERR_INVALID_ARG;
     const Rows yr = {grad_y, 0, sg_r, rows, n}, zr = {nullptr, 0, 0, rows, wide}, xr = {x, 0, sx_r, rows, width},
                wr = {w, sw_e, sw_n, wide, width};
-    int64_t need = grad_bias ? parts_bytes(rows, num_experts, wide) : 0;
+    int64_t need = grad_bias ? slices_bytes(rows, num_experts, wide) : 0;
     if (saved || !yr.direct())
         need += zr.packed_bytes(1);
     if (grad_w && !xr.direct())
         need += xr.packed_bytes(1);
     if (grad_x && !wr.direct())
         need += wr.packed_bytes(num_experts);
+    const Choice cx = choose(kGradX, false, rows, num_experts, width, wide), cw = choose(kGradW, false, rows, num_experts, width, wide);
+    if (grad_x)
+        need += parts_bytes(kGradX, cx.splits, rows, num_experts, width, wide);
+    if (grad_w)
+        need += parts_bytes(kGradW, cw.splits, rows, num_experts, width, wide);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return MXQ_ERR_WORKSPACE;
     if (wide == 0 && !(grad_x && rows > 0))
@@ -359,7 +480,7 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
     a.width = (int)width;
     a.wide = (int)wide;
     a.act = activation;
-    float *parts = grad_bias ? reinterpret_cast<float *>(room.take(parts_bytes(rows, num_experts, wide))) : nullptr;
+    float *parts = grad_bias ? reinterpret_cast<float *>(room.take(slices_bytes(rows, num_experts, wide))) : nullptr;
     Rows z = yr;
     if (saved) {
         z = {room.take(zr.packed_bytes(1)), 0, round_up(wide, 8), rows, wide};
@@ -389,7 +510,7 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         b.qe = wo.se * 2;
         b.out = grad_x;
         b.so = sdx_r;
-        status = launch<kGradX, TileSmall, false, false>(b, st);
+        status = launch<kGradX, false, false>(b, cx, room, st);
     }
     if (grad_w && status == MXQ_OK && wide > 0 && width > 0) {
         const Rows xo = readable(xr, 1, room, st);
@@ -399,7 +520,7 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         b.out = grad_w;
         b.so = sdw_n;
         b.oe = sdw_e;
-        status = launch<kGradW, TileSmall, false, false>(b, st);
+        status = launch<kGradW, false, false>(b, cw, room, st);
     }
     return status;
 }

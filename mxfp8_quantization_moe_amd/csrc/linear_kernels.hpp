@@ -26,9 +26,12 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "linear_ops.hpp"
 #include "moe_rows_kernels.hpp"
 #include "mxq_device.hpp"
+#include "stream_ops.hpp"
 #include "tile_ops.hpp"
 #include "wave_ops.hpp"
 
@@ -42,6 +45,7 @@ struct LinearArgs {
     int64_t ldp, ldq, qe;         // qe: from expert to expert
     const uint8_t *sp, *sq;       // e8m0 scales (MXFP8), rows of whole words
     int64_t ldsp, ldsq, sqe;
+    int64_t sbp, sbq;             // from block to block (few rows; else 1)
     const int32_t *offs;          // NULL: one group of all rows
     int experts, rows;
     int width, wide;              // inner extents: of x, and of z
@@ -53,6 +57,9 @@ struct LinearArgs {
     int64_t sr;
     uint16_t *out, *pre;          // pre: z, forward only
     int64_t so, spre, oe;         // oe: grad W, from expert to expert
+    float *parts;                 // sums in parts: (splits, result rows, ldparts)
+    int64_t ldparts, part_size;   // part_size: from part to part
+    int splits;
 };
 
 // ---------------------------------------------------------------- groups
@@ -118,7 +125,7 @@ __device__ __forceinline__ void find_row_tile(const LinearArgs &a, int t, int &e
 __device__ __forceinline__ int spread(int block, int total)
 {
     const int run = max(1, min(32, (total + 7) >> 3)), s = block >> 3;
-    return ((s / run) * 8 + (block & 7)) * run + s % run;
+    return uniform(((s / run) * 8 + (block & 7)) * run + s % run);
 }
 
 constexpr int kLinearBand = 8;  // row tiles of a band: a run of 32 is 8 x 4 tiles
@@ -140,28 +147,27 @@ struct LinearTile {
     static constexpr int THREADS = WM * WN * 64;
     static constexpr int FP = TM / WM / 16, FQ = TN / WN / 16;  // 16 x 16 fragments of a wave
     static constexpr int STAGE = (TM + TN) * 128;               // bytes
-    // the results pass through LDS RC rows of a wave's part at a time
-    static constexpr int RC = FP * 16 < 64 ? FP * 16 : 64, WJ = FQ * 16;
-    static_assert(RC * WJ * 4 * WM * WN <= NST * STAGE, "the results fit in the stages");
-    static_assert(THREADS >= TM + TN, "one load of scales per thread and stage");
 };
+
+// one workgroup of eight alternating waves per CU, 128 KB of LDS
+using LinearLarge = LinearTile<256, 256, 2, 4, 2>;
+using LinearHalf = LinearTile<256, 128, 2, 4, 2>;
 
 // k of a stage
 constexpr int kRowBytes = 128;
 
-// One operand of a tile: EXT rows of 128 bytes, or turned 64 rows of EXT
-// elements of bf16, THREADS threads.
+// One operand of a tile: EXT rows of 128 bytes of k; or turned, EXT / 64 blocks
+// of 64 rows of k, 64 elements (128 bytes) of bf16 each.  THREADS threads.
 //
-// Loads into LDS are linear; to spread the lanes of one LDS read over the
-// banks, the order of the chunks of a row is exchanged in the addresses that
-// are loaded: 16-byte chunk c of row r is at c ^ rswap(r), 32-byte chunk c of
-// a turned row k at c ^ tswap(k).
+// Loads into LDS are linear, so a load is whole rows or a whole block's; to
+// spread the lanes of one LDS read over the banks, the order of the chunks of a
+// row is exchanged in the addresses that are loaded: 16-byte chunk c of row r is
+// at c ^ rswap(r), 32-byte chunk c of a turned row k at c ^ tswap(k).
 template <int EXT, int THREADS, bool TURNED>
 struct Panel {
-    static constexpr int CH = TURNED ? EXT / 8 : 8;       // 16-byte chunks of a row
-    static constexpr int RPL = THREADS / CH;              // rows per load
-    static constexpr int LOADS = EXT * 8 / THREADS;
-    static_assert(RPL % 16 == 0, "the chunk orders repeat with each load");
+    static constexpr int RPL = THREADS / 8;               // rows per load
+    static constexpr int LOADS = EXT / RPL;
+    static_assert(RPL % 16 == 0 && 64 % RPL == 0, "the chunk orders repeat with each load");
     const char *base;
     int64_t step;                 // bytes from stage to stage
     int64_t ld;
@@ -171,10 +177,7 @@ struct Panel {
     int chunk;                    // this thread's chunk of k
 
     static __device__ __forceinline__ int rswap(int r) { return (r >> 1) & 7; }
-    static __device__ __forceinline__ int tswap(int k)
-    {
-        return EXT >= 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
-    }
+    static __device__ __forceinline__ int tswap(int k) { return ((k >> 1) & 1) | ((k >> 3) & 1) << 1; }
 
     // row(r): the operand's row that tile row r holds, relative to base, or -1
     template <typename Row>
@@ -184,8 +187,9 @@ struct Panel {
         ld = stride;
         step = kRowBytes;
         range = bytes;
-        const int r = threadIdx.x / CH;
-        chunk = (threadIdx.x % CH) ^ rswap(r);
+        rows = 0;
+        const int r = threadIdx.x / 8;
+        chunk = (threadIdx.x % 8) ^ rswap(r);
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
             const int at = row(r + u * RPL);
@@ -202,10 +206,23 @@ struct Panel {
         range = bytes;
         rows = n;
         chunk = 0;
-        const int k = threadIdx.x / CH;
 #pragma unroll
-        for (int u = 0; u < LOADS; ++u)
-            off[u] = (uint32_t)((k + u * RPL) * (uint32_t)stride + ((threadIdx.x % CH) ^ (tswap(k) << 1)) * 16);
+        for (int u = 0; u < LOADS; ++u) {
+            const int r = threadIdx.x / 8 + u * RPL, k = r % 64;
+            const uint32_t c = (r / 64) * 128 + ((threadIdx.x % 8) ^ (tswap(k) << 1)) * 16;
+            // a row shorter than the tile: not the next row's start, where
+            // that may be past the last row
+            off[u] = c < bytes ? (uint32_t)(k * (uint32_t)stride + c) : 0x80000000u;
+        }
+    }
+
+    __device__ __forceinline__ void skip(int stages)
+    {
+        base += stages * step;
+        if (TURNED)
+            rows -= stages * 64;
+        else
+            range -= (uint32_t)(stages * kRowBytes);
     }
 
     // load u of stage kt to lds + 16 * thread; `live`: chunks of k of the stage
@@ -213,7 +230,11 @@ struct Panel {
     {
         const uint32_t bytes = TURNED ? (uint32_t)((min(rows - kt * 64, 64) - 1) * ld) + range
                                       : range - (uint32_t)(kt * kRowBytes);
-        __amdgpu_buffer_rsrc_t rs = buffer_rsrc(base + kt * step, bytes);
+        // uniform all of it, but not provably so: without this the load becomes
+        // a loop over the lanes' descriptors
+        const uint64_t at = (uint64_t)(uintptr_t)base + (uint64_t)(kt * step);
+        const uint64_t from = (uint32_t)uniform((int)at) | (uint64_t)(uint32_t)uniform((int)(at >> 32)) << 32;
+        __amdgpu_buffer_rsrc_t rs = buffer_rsrc(reinterpret_cast<const void *>(from), (uint32_t)uniform((int)bytes));
         uint32_t o = off[u];
         if (!TURNED && live < 8)
             o = chunk < live ? o : 0x80000000u;
@@ -222,19 +243,21 @@ struct Panel {
             rs, (__attribute__((address_space(3))) void *)(uintptr_t)uniform((int)dst), 16, (int)o, 0, 0, 0);
     }
 
-    // LDS addresses of this lane's fragment reads: N fragments from tile row
-    // (or column) `first` on
+    // LDS addresses of this lane's fragment reads, from tile row (or column)
+    // `first`, a multiple of 16 N, on; the rest of an address is a constant of
+    // the instruction
     template <int N>
     struct Reads {
-        uint32_t a[TURNED ? N : 2];
+        static constexpr int A = TURNED ? (N < 4 ? N : 4) : 2;
+        uint32_t a[A];
         __device__ __forceinline__ Reads(uint32_t lds, int first)
         {
             const int fr = threadIdx.x & 15, fk = (threadIdx.x & 63) >> 4;
             if constexpr (TURNED) {
                 const int kr = 8 * fk + (fr >> 2);  // and the four rows after
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    a[i] = lds + (uint32_t)(kr * EXT + ((first / 16 + i) ^ tswap(kr)) * 16 + (fr & 3) * 4) * 2;
+                for (int i = 0; i < A; ++i)
+                    a[i] = lds + (uint32_t)((first / 64) * 8192 + kr * 128 + ((first / 16 + i) % 4 ^ tswap(kr)) * 32 + (fr & 3) * 8);
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -248,8 +271,8 @@ struct Panel {
 #pragma unroll
             for (int i = 0; i < M; ++i) {
                 if constexpr (TURNED) {
-                    const uint32_t b = a[I0 + i] + at + h * 32 * EXT * 2;
-                    const half4 x = read_transposed(b), y = read_transposed(b + 4 * EXT * 2);
+                    const uint32_t b = a[(I0 + i) % A] + at + (I0 + i) / 4 * 8192 + h * 4096;
+                    const half4 x = read_transposed(b), y = read_transposed(b + 512);
                     f[i] = half8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
                 } else {
                     f[i] = read_lds(a[h] + at + (I0 + i) * 16 * 128);
@@ -259,27 +282,28 @@ struct Panel {
     };
 };
 
-typedef int int8v __attribute__((ext_vector_type(8)));
 // acc += P Q over a stage, fragments I0.. of P.  Q is the first operand: a
 // lane's four results lie along j.  The scaled product takes both halves of a
 // stage at once (128 values of k): lane 16 b + i holds bytes 16 b and 64 + 16 b
 // of row i and supplies the scale of its 32-value block b.
 template <bool MX, int I0, int N, int FP, int FQ>
 __device__ __forceinline__ void multiply_stage(const half8 (&p0)[N], const half8 (&p1)[N], const half8 (&q0)[FQ],
-                                               const half8 (&q1)[FQ], const int (&sp)[N], const int (&sq)[FQ],
+                                               const half8 (&q1)[FQ], const int (&sp)[FP], const int (&sq)[FQ],
                                                float4v (&acc)[FP][FQ])
 {
     if constexpr (MX) {
-        struct Pair {
-            half8 a, b;
+        // both halves of a fragment
+        auto whole = [](const half8 &x, const half8 &y) {
+            typedef int int4v __attribute__((ext_vector_type(4)));
+            const int4v u = __builtin_bit_cast(int4v, x), v = __builtin_bit_cast(int4v, y);
+            return int8v{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
         };
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int j = 0; j < FQ; ++j)
                 acc[I0 + i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    __builtin_bit_cast(int8v, Pair{q0[j], q1[j]}), __builtin_bit_cast(int8v, Pair{p0[i], p1[i]}),
-                    acc[I0 + i][j], 0, 0, 0, sq[j], 0, sp[i]);
+                    whole(q0[j], q1[j]), whole(p0[i], p1[i]), acc[I0 + i][j], 0, 0, 0, sq[j], 0, sp[I0 + i]);
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -299,11 +323,12 @@ template <typename TILE, bool PT, bool QT, bool MX>
 struct LinearStages {
     typedef Panel<TILE::TM, TILE::THREADS, PT> PanelP;
     typedef Panel<TILE::TN, TILE::THREADS, QT> PanelQ;
-    static constexpr int LP = PanelP::LOADS, LQ = PanelQ::LOADS, LOADS = LP + LQ + (MX ? 1 : 0);
-    static constexpr int BYTES = TILE::STAGE + (MX ? TILE::THREADS * 4 : 0);
+    static constexpr int LP = PanelP::LOADS, LQ = PanelQ::LOADS, LS = MX ? (TILE::TM + TILE::TN + TILE::THREADS - 1) / TILE::THREADS : 0;
+    static constexpr int LOADS = LP + LQ + LS;
+    static constexpr int BYTES = TILE::STAGE + LS * TILE::THREADS * 4;
     PanelP p;
     PanelQ q;
-    const uint8_t *scales;        // this thread's row
+    const uint8_t *scales[LS > 0 ? LS : 1];  // this thread's rows
     int stages, live;             // live: chunks of k in the last stage
     uint32_t lds0;
 
@@ -316,8 +341,9 @@ struct LinearStages {
         } else if (u < LP + LQ) {
             q.load(u - LP, kt, n, at + TILE::TM * 128);
         } else {
-            const uint32_t dst = at + TILE::STAGE + (threadIdx.x & ~63) * 4;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(scales + kt * 4),
+            const int l = u - LP - LQ;
+            const uint32_t dst = at + TILE::STAGE + (l * TILE::THREADS + (threadIdx.x & ~63)) * 4;
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(scales[l] + kt * 4),
                                              (__attribute__((address_space(3))) void *)(uintptr_t)uniform((int)dst), 4, 0, 0);
         }
     }
@@ -328,20 +354,30 @@ struct LinearStages {
             load_one(s, u, kt);
     }
 
+    // stages [first, last) alone
+    __device__ __forceinline__ void part(int first, int last)
+    {
+        p.skip(first);
+        q.skip(first);
+        if constexpr (MX)
+#pragma unroll
+            for (int l = 0; l < LS; ++l)
+                scales[l] += first * 4;
+        live = last < stages ? 8 : live;
+        stages = last - first;
+    }
+
     // scales of N fragments from tile row `first` on (of Q: TM further), each
-    // lane its block's; blocks past k (whose values are zeros) count as 2^-127
+    // lane its block's in the lowest byte; blocks past k are zeros in memory
     template <int N>
-    __device__ __forceinline__ void read_scales(int s, int kt, int first, int (&v)[N]) const
+    __device__ __forceinline__ void read_scales(int s, int first, int (&v)[N]) const
     {
         if constexpr (MX) {
             const int fr = threadIdx.x & 15, fk = (threadIdx.x & 63) >> 4;
             const uint32_t a = lds0 + s * BYTES + TILE::STAGE + (uint32_t)(first + fr) * 4;
-            const bool there = kt + 1 < stages || 2 * fk < live;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t w = *(__attribute__((address_space(3))) const uint32_t *)(uintptr_t)(a + i * 64);
-                v[i] = there ? (int)((w >> (8 * fk)) & 0xffu) : 0;
-            }
+            for (int i = 0; i < N; ++i)
+                v[i] = *(__attribute__((address_space(3))) const int *)(uintptr_t)(a + i * 64) >> (8 * fk);
         }
     }
 };
@@ -361,14 +397,14 @@ __device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT,
         half8 p0[FP], p1[FP], q0[FQ], q1[FQ];
         int sp[FP], sq[FQ];
     } f[2];
-    auto read = [&](int s, int kt, Frags &x) {
+    auto read = [&](int s, Frags &x) {
         const uint32_t at = s * S::BYTES;
         rq.template read<0>(at, 0, x.q0);
         rp.template read<0>(at, 0, x.p0);
         rq.template read<0>(at, 1, x.q1);
         rp.template read<0>(at, 1, x.p1);
-        st.read_scales(s, kt, row0, x.sp);
-        st.read_scales(s, kt, TILE::TM + col0, x.sq);
+        st.read_scales(s, row0, x.sp);
+        st.read_scales(s, TILE::TM + col0, x.sq);
     };
     const int end = st.stages;
     for (int s = 0; s < NST; ++s)
@@ -378,7 +414,7 @@ __device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT,
         wait_stage<(NST - 1) * S::LOADS>();
     else
         wait_stage<0>();
-    read(0, 0, f[0]);
+    read(0, f[0]);
     int now = 0, kt = 0;
     auto step = [&](Frags &x, Frags &y) {
         const int next = now + 1 == NST ? 0 : now + 1;
@@ -389,7 +425,7 @@ __device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT,
                 wait_stage<0>();
             if (kt + NST < end)
                 st.load(now, kt + NST);
-            read(next, kt + 1, y);
+            read(next, y);
         }
         multiply_stage<MX, 0>(x.p0, x.p1, x.q0, x.q1, x.sp, x.sq, acc);
         now = next;
@@ -405,94 +441,277 @@ __device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT,
 
 // ---------------------------------------------------------------- epilogue
 
-// Results to memory.  A lane holds row l % 16, columns 4 (l / 16) + 0..3 of
-// each fragment; through LDS (each wave in its own region, RC rows at a time)
-// it gets 8 consecutive columns of one row instead, so that bias, residual and
-// results are read and written in 16-byte pieces of whole lines.  Everything is
-// fp32 up to the one rounding to the output.
-//   out: the tile's first row; left: rows there; e: expert of the bias;
-//   c0: first result column of the tile
+// Two groups of four waves, one wave of each on every SIMD, one phase apart:
+// while one group's MFMAs run the other reads its fragments.  Group 0 has the
+// upper half of the tile's rows, group 1 the lower; each half's rows are taken
+// in two quarters.  A stage takes four phases with a barrier after each:
+//   ra  read Q, all scales and the first quarter     ma  multiply
+//   rb  read the second quarter                      mb  multiply
+// and group 1 is in the phase before group 0's.
+//
+// Two stages in LDS, but a stage's parts are loaded as soon as the part that
+// they overwrite has been read by both groups (a read phase ends with its
+// reads returned), so every part has five phases to arrive.  In either group's
+// phases of stage t:
+//   ra(t)  quarters 1 and 3 of t + 1             (first read in rb(t + 1))
+//   rb(t)  Q, scales, quarters 0 and 2 of t + 2  (first read in ra(t + 2))
+// The loads of a wave return in order: at the end of group 0's mb(t) the parts
+// for ra(t + 1) have landed when only those issued since are pending, 2 of t + 1
+// and the FIRST of t + 2, at the end of its ma(t) those for rb(t) when again as
+// many are.
+template <typename TILE, bool PT, bool QT, bool MX>
+struct LinearAlternating {
+    typedef LinearStages<TILE, PT, QT, MX> S;
+    static_assert(TILE::NST == 2 && TILE::WM == 2 && TILE::WN == 4 && TILE::TM == 256 && S::LP == 4,
+                  "loads 0-3 are the quarters, the rest Q and the scales");
+    static constexpr int FP = TILE::FP, FQ = TILE::FQ, H = FP / 2;
+    static constexpr int FIRST = S::LOADS - 2;
+    const S &st;
+    const typename S::PanelP::template Reads<FP> rp;
+    const typename S::PanelQ::template Reads<FQ> rq;
+    int row0, col0;
+    half8 p0[H], p1[H], q0[FQ], q1[FQ];
+    int sp[FP], sq[FQ];
+
+    __device__ __forceinline__ LinearAlternating(const S &s, int r, int c)
+        : st(s), rp(s.lds0, r), rq(s.lds0 + TILE::TM * 128, c), row0(r), col0(c)
+    {
+    }
+
+    static __device__ __forceinline__ void load_a(const S &st, int kt)
+    {
+#pragma unroll
+        for (int u = 4; u < S::LOADS; ++u)
+            st.load_one(kt & 1, u, kt);
+        st.load_one(kt & 1, 0, kt);
+        st.load_one(kt & 1, 2, kt);
+    }
+    __device__ __forceinline__ void load_b(int kt) const
+    {
+        st.load_one(kt & 1, 1, kt);
+        st.load_one(kt & 1, 3, kt);
+    }
+    __device__ __forceinline__ void read_a(int kt)
+    {
+        const uint32_t at = (kt & 1) * S::BYTES;
+        rq.template read<0>(at, 0, q0);
+        rp.template read<0>(at, 0, p0);
+        rq.template read<0>(at, 1, q1);
+        rp.template read<0>(at, 1, p1);
+        st.read_scales(kt & 1, row0, sp);
+        st.read_scales(kt & 1, TILE::TM + col0, sq);
+    }
+    __device__ __forceinline__ void read_b(int kt)
+    {
+        const uint32_t at = (kt & 1) * S::BYTES;
+        rp.template read<H>(at, 0, p0);
+        rp.template read<H>(at, 1, p1);
+    }
+    template <int I0>
+    __device__ __forceinline__ void products(float4v (&acc)[FP][FQ])
+    {
+        __builtin_amdgcn_s_setprio(1);
+        multiply_stage<MX, I0>(p0, p1, q0, q1, sp, sq, acc);
+        __builtin_amdgcn_s_setprio(0);
+    }
+
+    // one stage; MORE: how many stages follow (0, 1, or 2 for two and more)
+    template <bool LATER, int MORE>
+    __device__ __forceinline__ void stage(int kt, float4v (&acc)[FP][FQ])
+    {
+        constexpr int kB = MORE >= 1 ? 2 + FIRST : 0;                         // pending when rb may begin
+        constexpr int kNext = MORE >= 2 ? 2 + FIRST : MORE == 1 ? 2 : -1;     // when the next ra may
+        read_a(kt);
+        if (MORE >= 1)
+            load_b(kt + 1);
+        phase_end<LATER ? kB : -1>();
+        products<0>(acc);
+        phase_end<LATER ? -1 : kB>();
+        read_b(kt);
+        if (MORE >= 2)
+            load_a(st, kt + 2);
+        phase_end<LATER ? kNext : -1>();
+        products<H>(acc);
+        phase_end<LATER ? -1 : kNext>();
+    }
+
+    template <bool LATER>
+    __device__ __forceinline__ void run_group(float4v (&acc)[FP][FQ])
+    {
+        if (LATER)
+            phase_end<-1>();
+        const int end = st.stages;
+        int kt = 0;
+        for (; kt + 2 < end; ++kt)
+            stage<LATER, 2>(kt, acc);
+        if (kt + 1 < end) {
+            stage<LATER, 1>(kt, acc);
+            ++kt;
+        }
+        stage<LATER, 0>(kt, acc);
+        if (!LATER)
+            phase_end<-1>();
+    }
+
+    // what is on its way before run(); the stages are free
+    static __device__ __forceinline__ void first_loads(const S &st)
+    {
+        st.load(0, 0);
+        if (st.stages > 1)
+            load_a(st, 1);
+    }
+
+    // Waits for whatever was issued after first_loads, too.  At the end every
+    // wave has read every stage: the last read phase of either group is before
+    // the last barrier.
+    __device__ __forceinline__ void run(float4v (&acc)[FP][FQ])
+    {
+        phase_end<0>();
+        if (row0 != 0)
+            run_group<true>(acc);
+        else
+            run_group<false>(acc);
+    }
+};
+
+// Rows of 16 lanes: a's second and fourth change places with b's first and
+// third.
+__device__ __forceinline__ void swap_rows(float &a, float &b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+}
+
+// Results to memory.  A lane holds row l % 16, columns 4 (l / 16) + 0..3 of each
+// fragment.  Two fragments change lane rows, and each lane has 8 consecutive
+// columns of one of them: bias, residual and results are read and written in
+// 16-byte pieces, 64 bytes of a row at a time, without LDS and without meeting
+// the other waves.  Everything is fp32 up to the one rounding to the output.
+//   row0: first row of the tile in the results; left: rows there; e: expert of
+//   the bias; c0: first result column of the tile
 template <typename TILE, bool GATED, bool EPILOGUE>
-__device__ __forceinline__ void linear_store(char *lds, const LinearArgs &a, float4v (&acc)[TILE::FP][TILE::FQ], int e,
+__device__ __forceinline__ void linear_store(const LinearArgs &a, float4v (&acc)[TILE::FP][TILE::FQ], int e,
                                              int64_t row0, int left, int c0, int n, uint16_t *out, int64_t so)
 {
-    constexpr int FP = TILE::FP, FQ = TILE::FQ, RC = TILE::RC, WJ = TILE::WJ;
-    constexpr int OJ = GATED ? WJ / 2 : WJ;          // result columns of a wave
-    constexpr int LPR = OJ / 8, RPP = 64 / LPR, PASSES = RC / RPP;
+    constexpr int FP = TILE::FP, FQ = TILE::FQ;
+    // the pairs of fragments: next to one another along j, of a gate two
+    // further (the value between); with one gate fragment along i
+    constexpr bool ALONG_I = GATED && FQ == 2;
+    constexpr int PAIRS = ALONG_I ? 1 : GATED ? FQ / 4 : FQ / 2;
     const int wave = uniform(threadIdx.x >> 6), wp = wave / TILE::WN, wq = wave % TILE::WN;
-    const int lane = threadIdx.x & 63, fr = lane & 15, fk = lane >> 4, pr = lane / LPR, pc = lane % LPR;
-    const int c = c0 + wq * OJ + pc * 8;
-    // columns in LDS of this lane's (gate's) eight, in fragments of 16
-    const int lc = GATED ? (pc >> 1) * 32 + (pc & 1) * 8 : pc * 8;
-    float *wide = reinterpret_cast<float *>(lds) + wave * RC * WJ;
-    auto wswap = [](int r) { return WJ == 64 ? r & 15 : (r >> 1) & 7; };
-    float bias[2][8];
+    const int lane = threadIdx.x & 63, fr = lane & 15, fk = lane >> 4;
+    const int r0 = wp * FP * 16 + fr + (ALONG_I ? (fk & 1) * 16 : 0);
+    const int w0 = c0 + wq * (GATED ? FQ * 8 : FQ * 16) + (fk >> 1) * 8 + (ALONG_I ? 0 : (fk & 1) * 16);
+    float bias[PAIRS][GATED ? 2 : 1][8];
     if constexpr (EPILOGUE) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const bool there = a.bias && c + k < n;
-            bias[0][k] = there ? bias_at(a.bias, a.bias_f32, e * a.sb + c + k) : 0.0f;
-            if (GATED)
-                bias[1][k] = there ? bias_at(a.bias, a.bias_f32, e * a.sb + n + c + k) : 0.0f;
-        }
-    }
-    wait_stage<0>();  // every wave is done with the stages
+        for (int p = 0; p < PAIRS; ++p)
 #pragma unroll
-    for (int ic = 0; ic < FP * 16; ic += RC) {
+            for (int h = 0; h < (GATED ? 2 : 1); ++h)
 #pragma unroll
-        for (int i = 0; i < RC / 16; ++i)
-#pragma unroll
-            for (int j = 0; j < FQ; ++j)
-                *reinterpret_cast<float4v *>(wide + (i * 16 + fr) * WJ + ((4 * j + fk) ^ wswap(i * 16 + fr)) * 4) =
-                    acc[ic / 16 + i][j];
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int p = 0; p < PASSES; ++p) {
-            const int r = p * RPP + pr, i = wp * FP * 16 + ic + r;
-            if (i >= left || c >= n)
-                continue;
-            auto read = [&](int col, float (&v)[8]) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float4v x = *reinterpret_cast<const float4v *>(wide + r * WJ + ((col / 4 + h) ^ wswap(r)) * 4);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[4 * h + k] = x[k];
+                for (int k = 0; k < 8; ++k) {
+                    const int c = w0 + p * 32 + k;
+                    bias[p][h][k] = a.bias && c < n ? bias_at(a.bias, a.bias_f32, e * a.sb + h * n + c) : 0.0f;
                 }
-            };
-            float v[8];
-            read(lc, v);
+    }
+    // eight values of one fragment from its pair
+    auto join = [](float4v x, float4v y, float (&v)[8]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float lo = x[k], hi = y[k];
+            swap_rows(lo, hi);
+            v[k] = lo;
+            v[4 + k] = hi;
+        }
+    };
+    Piece<uint16_t> resid[2][PAIRS];
+    auto load_resid = [&](int i, int set) {
+        if constexpr (EPILOGUE) {
+            if (a.resid) {
+                const int r = r0 + i * 16;
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p)
+                    if (r < left && w0 + p * 32 < n)
+                        resid[set][p] = load8(a.resid + (row0 + r) * a.sr, w0 + p * 32, n);
+            }
+        }
+    };
+    constexpr int STEP = ALONG_I ? 2 : 1;
+    load_resid(0, 0);
+#pragma unroll
+    for (int i = 0; i < FP; i += STEP) {
+        if (i + STEP < FP)
+            load_resid(i + STEP, (i / STEP + 1) & 1);
+        const int r = r0 + i * 16;
+        const int64_t row = row0 + r;
+#pragma unroll
+        for (int p = 0; p < PAIRS; ++p) {
+            const int c = w0 + p * 32;
+            float v[8], g[8];
+            if constexpr (ALONG_I) {
+                join(acc[i][0], acc[i + 1][0], v);
+                join(acc[i][1], acc[i + 1][1], g);
+            } else if constexpr (GATED) {
+                join(acc[i][4 * p], acc[i][4 * p + 2], v);
+                join(acc[i][4 * p + 1], acc[i][4 * p + 3], g);
+            } else {
+                join(acc[i][2 * p], acc[i][2 * p + 1], v);
+            }
+            if (r >= left || c >= n)
+                continue;
             if constexpr (EPILOGUE) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    v[k] += bias[0][k];
+                    v[k] += bias[p][0][k];
                 if (a.pre)
-                    store8(a.pre + (row0 + i) * a.spre, c, n, v);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    v[k] = act_value(a.act, v[k]);
+                    store8(a.pre + row * a.spre, c, n, v);
+                act_values(a.act, v);
                 if constexpr (GATED) {
-                    float g[8];
-                    read(lc + 16, g);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        g[k] += bias[1][k];
+                        g[k] += bias[p][1][k];
                     if (a.pre)
-                        store8(a.pre + (row0 + i) * a.spre + n, c, n, g);
+                        store8(a.pre + row * a.spre + n, c, n, g);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         v[k] *= g[k];
                 }
                 if (a.resid) {
-                    const Piece<uint16_t> x = load8(a.resid + (row0 + i) * a.sr, c, n);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        v[k] += x.get(k);
+                        v[k] += resid[(i / STEP) & 1][p].get(k);
                 }
             }
-            store8(out + (row0 + i) * so, c, n, v);
+            store8(out + row * so, c, n, v);
         }
-        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// The sums of a part as they are, for linear_join_kernel: z's columns in their
+// places, a gate's and its value's apart.
+template <typename TILE, bool GATED>
+__device__ __forceinline__ void store_part(const LinearArgs &a, float4v (&acc)[TILE::FP][TILE::FQ], int64_t row0, int left,
+                                           int c0, int n, float *out)
+{
+    constexpr int FP = TILE::FP, FQ = TILE::FQ;
+    const int wave = uniform(threadIdx.x >> 6), wp = wave / TILE::WN, wq = wave % TILE::WN;
+    const int lane = threadIdx.x & 63, fr = lane & 15, fk = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < FP; ++i) {
+        const int r = wp * FP * 16 + i * 16 + fr;
+        float *row = out + (row0 + r) * a.ldparts;
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) {
+            const int f = wq * FQ + j, c = c0 + (GATED ? f / 2 : f) * 16 + 4 * fk;
+            if (r >= left || c >= n)
+                continue;
+            float *to = row + (GATED && (f & 1) ? n : 0) + c;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c + k < n)
+                    to[k] = acc[i][j][k];
+        }
     }
 }
 
@@ -511,96 +730,512 @@ __device__ __forceinline__ void clear_tile(uint16_t *out, int64_t so, int64_t ro
 
 // ---------------------------------------------------------------- kernels
 
-// One tile per workgroup.
-template <int MODE, typename TILE, bool GATED, bool MX>
-__global__ __launch_bounds__(TILE::THREADS, 2) void linear_kernel(LinearArgs a)
-{
-    constexpr bool PT = MODE == kGradW, QT = MODE != kForward;
-    typedef LinearStages<TILE, PT, QT, MX> S;
-    __shared__ __attribute__((aligned(16))) char lds[TILE::NST * S::BYTES];
-    constexpr int TM = TILE::TM, TN = TILE::TN, TJ = GATED ? TN / 2 : TN;
-    const int tn = (a.n + TJ - 1) / TJ;
-    int e, i0, c0, left, k;
-    int64_t row0;
-    if constexpr (MODE == kGradW) {
-        // every expert's (wide, width) result; the sum runs over the group's rows
-        const int tm = (a.wide + TM - 1) / TM, total = a.experts * tm * tn, t = spread(blockIdx.x, total);
-        if (t >= total)
-            return;
-        e = t / (tm * tn);
-        int bi, bj, start;
-        band_tile(t % (tm * tn), tm, tn, bi, bj);
-        group_rows(a.offs, a.experts, a.rows, e, start, k);
-        row0 = uniform(start);
-        k = uniform(k);
-        i0 = bi * TM;
-        c0 = bj * TN;
-        left = a.wide - i0;
-    } else {
-        const int tm = count_row_tiles<TM>(a), total = tm * tn, t = spread(blockIdx.x, total);
-        if (t >= total)
-            return;
-        int bi, bj, r0;
-        band_tile(t, tm, tn, bi, bj);
-        find_row_tile<TM>(a, bi, e, r0, left);
-        row0 = r0;
-        i0 = 0;
-        c0 = bj * TJ;
-        if (e >= a.experts) {
-            clear_tile<TM, TJ, TILE::THREADS>(a.out, a.so, row0, left, c0, a.n);
-            if (MODE == kForward && a.pre) {
-                clear_tile<TM, TJ, TILE::THREADS>(a.pre, a.spre, row0, left, c0, a.n);
-                if (GATED)
-                    clear_tile<TM, TJ, TILE::THREADS>(a.pre + a.n, a.spre, row0, left, c0, a.n);
-            }
-            return;
+// A tile of the results.
+struct TileAt {
+    int e;                // its expert; `experts`: rows of no group, to clear
+    int i0, c0;           // grad W: first row of dW; first result column
+    int left;             // result rows from the tile's first on
+    int k;                // length of the sum
+    int64_t row0;         // first row among the tokens
+};
+
+template <int MODE, typename TILE, bool GATED>
+struct LinearGrid {
+    static constexpr int TM = TILE::TM, TJ = GATED ? TILE::TN / 2 : TILE::TN;
+    int tm, tn, total;
+    __device__ __forceinline__ LinearGrid(const LinearArgs &a)
+    {
+        tn = (a.n + TJ - 1) / TJ;
+        tm = MODE == kGradW ? (a.wide + TM - 1) / TM : count_row_tiles<TM>(a);
+        total = MODE == kGradW ? a.experts * tm * tn : tm * tn;
+    }
+    __device__ __forceinline__ TileAt at(const LinearArgs &a, int t) const
+    {
+        // uniform(): divisions come out of vector registers, and from there a
+        // descriptor would be made for each lane
+        TileAt x;
+        int bi, bj, e, row0, left;
+        if constexpr (MODE == kGradW) {
+            // every expert's (wide, width) result; the sum runs over the group's rows
+            e = uniform(t / (tm * tn));
+            band_tile(uniform(t - e * tm * tn), tm, tn, bi, bj);
+            bi = uniform(bi);
+            int len;
+            group_rows(a.offs, a.experts, a.rows, e, row0, len);
+            x.k = uniform(len);
+            x.i0 = bi * TM;
+            left = a.wide - x.i0;
+        } else {
+            band_tile(t, tm, tn, bi, bj);
+            find_row_tile<TM>(a, uniform(bi), e, row0, left);
+            x.i0 = 0;
+            x.k = MODE == kForward ? a.width : a.wide;
         }
-        k = MODE == kForward ? a.width : a.wide;
+        x.e = uniform(e);
+        x.row0 = uniform(row0);
+        x.left = uniform(left);
+        x.c0 = uniform(bj) * TJ;
+        return x;
+    }
+};
+
+template <int MODE, typename TILE, bool GATED, bool MX>
+struct LinearTask {
+    static constexpr bool PT = MODE == kGradW, QT = MODE != kForward;
+    typedef LinearStages<TILE, PT, QT, MX> S;
+    static constexpr int TM = TILE::TM, TN = TILE::TN, TJ = GATED ? TN / 2 : TN;
+
+    // operands of a tile
+    static __device__ __forceinline__ void operands(const LinearArgs &a, const TileAt &x, S &st)
+    {
+        // bytes of k of one row, in whole chunks: rows whose length is not are padded
+        const int kb = MX ? x.k : 2 * ((x.k + 7) & ~7);
+        st.stages = MODE == kGradW ? (x.k + 63) / 64 : (kb + kRowBytes - 1) / kRowBytes;
+        st.live = MODE == kGradW ? 8 : ((kb - 1) % kRowBytes + 16) / 16;
+        if constexpr (MODE == kGradW) {
+            st.p.set_turned(a.p + x.row0 * a.ldp + (int64_t)x.i0 * 2, a.ldp, (uint32_t)(((a.wide + 7) & ~7) - x.i0) * 2, x.k);
+            st.q.set_turned(a.q + x.row0 * a.ldq + (int64_t)x.c0 * 2, a.ldq, (uint32_t)(((a.n + 7) & ~7) - x.c0) * 2, x.k);
+        } else {
+            const int rows = min(x.left, TM);
+            st.p.set_rows(a.p + x.row0 * a.ldp, a.ldp, (uint32_t)((rows - 1) * a.ldp) + kb,
+                          [&](int r) { return r < rows ? r : -1; });
+            const char *q = a.q + x.e * a.qe;
+            if constexpr (QT) {
+                st.q.set_turned(q + (int64_t)x.c0 * 2, a.ldq, (uint32_t)(((a.n + 7) & ~7) - x.c0) * 2, a.wide);
+            } else {
+                // tile row r: gated, fragments of 16 rows of the gate and of
+                // the value in turn
+                const int n = a.n - x.c0;
+                auto row = [&](int r) {
+                    const int at = GATED ? (r >> 5) * 16 + (r & 15) : r;
+                    return at >= n ? -1 : GATED && (r & 16) ? at + a.n : at;
+                };
+                const int last = GATED ? a.wide - 1 - x.c0 : min(n, TN) - 1;
+                st.q.set_rows(q + x.c0 * a.ldq, a.ldq, (uint32_t)(last * a.ldq) + kb, row);
+                if constexpr (MX) {
+#pragma unroll
+                    for (int l = 0; l < S::LS; ++l) {
+                        const int t = l * TILE::THREADS + threadIdx.x, r = row(min(max(t - TM, 0), TN - 1));
+                        st.scales[l] = t < TM ? a.sp + (x.row0 + min(t, rows - 1)) * a.ldsp
+                                              : a.sq + x.e * a.sqe + (int64_t)(x.c0 + max(r, 0)) * a.ldsq;
+                    }
+                }
+            }
+        }
     }
 
-    S st;
+    static __device__ __forceinline__ void clear(const LinearArgs &a, const TileAt &x)
+    {
+        clear_tile<TM, TJ, TILE::THREADS>(a.out, a.so, x.row0, x.left, x.c0, a.n);
+        if (MODE == kForward && a.pre) {
+            clear_tile<TM, TJ, TILE::THREADS>(a.pre, a.spre, x.row0, x.left, x.c0, a.n);
+            if (GATED)
+                clear_tile<TM, TJ, TILE::THREADS>(a.pre + a.n, a.spre, x.row0, x.left, x.c0, a.n);
+        }
+    }
+
+    static __device__ __forceinline__ void start(float4v (&acc)[TILE::FP][TILE::FQ])
+    {
+#pragma unroll
+        for (int i = 0; i < TILE::FP; ++i)
+#pragma unroll
+            for (int j = 0; j < TILE::FQ; ++j)
+                acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    static __device__ __forceinline__ void store(const LinearArgs &a, const TileAt &x, float4v (&acc)[TILE::FP][TILE::FQ])
+    {
+        uint16_t *out = MODE == kGradW ? a.out + x.e * a.oe : a.out;
+        linear_store<TILE, GATED, MODE == kForward>(a, acc, x.e, MODE == kGradW ? x.i0 : x.row0, x.left, x.c0, a.n, out, a.so);
+    }
+};
+
+// One tile, or with SPLIT a part of its sum, per workgroup.
+template <int MODE, typename TILE, bool GATED, bool MX, bool SPLIT>
+__global__ __launch_bounds__(TILE::THREADS, 2) void linear_kernel(LinearArgs a)
+{
+    typedef LinearTask<MODE, TILE, GATED, MX> Task;
+    __shared__ __attribute__((aligned(16))) char lds[TILE::NST * Task::S::BYTES];
+    const LinearGrid<MODE, TILE, GATED> grid(a);
+    const int work = SPLIT ? grid.total * a.splits : grid.total;
+    int t = spread(blockIdx.x, work), part = 0;
+    if (t >= work)
+        return;
+    if constexpr (SPLIT) {
+        part = uniform(t / grid.total);
+        t -= part * grid.total;
+    }
+    const TileAt x = grid.at(a, t);
+    if (MODE != kGradW && x.e >= a.experts) {
+        if (!SPLIT)
+            Task::clear(a, x);
+        return;
+    }
+    typename Task::S st;
     st.lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-    // bytes of k of one row, in whole chunks: rows whose length is not are padded
-    const int kb = MX ? k : 2 * ((k + 7) & ~7);
-    st.stages = MODE == kGradW ? (k + 63) / 64 : (kb + kRowBytes - 1) / kRowBytes;
-    st.live = MODE == kGradW ? 8 : ((kb - 1) % kRowBytes + 16) / 16;
-    if constexpr (MODE == kGradW) {
-        st.p.set_turned(a.p + row0 * a.ldp + (int64_t)i0 * 2, a.ldp, (uint32_t)(((a.wide + 7) & ~7) - i0) * 2, k);
-        st.q.set_turned(a.q + row0 * a.ldq + (int64_t)c0 * 2, a.ldq, (uint32_t)(((a.n + 7) & ~7) - c0) * 2, k);
+    Task::operands(a, x, st);
+    if constexpr (SPLIT)
+        st.part(uniform(st.stages * part / a.splits), uniform(st.stages * (part + 1) / a.splits));
+    float4v acc[TILE::FP][TILE::FQ];
+    Task::start(acc);
+    const int wave = uniform(threadIdx.x >> 6);
+    if (st.stages > 0)
+        linear_pipeline<TILE, Task::PT, Task::QT, MX>(st, wave / TILE::WN * TILE::FP * 16, wave % TILE::WN * TILE::FQ * 16, acc);
+    if constexpr (SPLIT) {
+        // grad W: experts' results one after the other
+        const int64_t row0 = MODE == kGradW ? (int64_t)x.e * a.wide + x.i0 : x.row0;
+        store_part<TILE, GATED>(a, acc, row0, x.left, x.c0, a.n, a.parts + part * a.part_size);
     } else {
-        const int rows = min(left, TM);
-        st.p.set_rows(a.p + row0 * a.ldp, a.ldp, (uint32_t)((rows - 1) * a.ldp) + kb, [&](int r) { return r < rows ? r : -1; });
-        const char *q = a.q + e * a.qe;
-        if constexpr (QT) {
-            st.q.set_turned(q + (int64_t)c0 * 2, a.ldq, (uint32_t)(((a.n + 7) & ~7) - c0) * 2, a.wide);
+        Task::store(a, x, acc);
+    }
+}
+
+// The parts of the sums, in order, and what follows the product: a workgroup per
+// result row and 1024 columns.  MODE and GATED as of the product.
+template <int MODE, bool GATED>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a)
+{
+    const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
+    const int64_t all = MODE == kGradW ? (int64_t)a.experts * a.wide : a.rows;
+    for (int64_t r = blockIdx.x; r < all; r += gridDim.x) {
+        int e = 0;
+        uint16_t *out = a.out + r * a.so;
+        bool none = false;
+        if constexpr (MODE == kGradW) {
+            e = uniform((int)(r / a.wide));
+            out = a.out + e * a.oe + (r - (int64_t)e * a.wide) * a.so;
+        } else if (a.offs) {
+            // the group that holds row r: the first that ends past it
+            int g0 = 0;
+            for (;; g0 += 64) {
+                const int g = g0 + (threadIdx.x & 63);
+                const uint64_t past = __ballot(g >= a.experts || min(max(a.offs[g], 0), a.rows) > r);
+                if (past) {
+                    e = g0 + __builtin_ctzll(past);
+                    break;
+                }
+            }
+            none = e >= a.experts;
+        }
+        if (c >= a.n)
+            continue;
+        auto sum = [&](int at, float (&v)[4]) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = 0.0f;
+            for (int p = 0; p < a.splits; ++p) {
+                const float *from = a.parts + p * a.part_size + r * a.ldparts + at;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (c + k < a.n)
+                        v[k] += from[k];
+            }
+        };
+        float v[4] = {}, g[4] = {};
+        if (!none) {
+            sum(c, v);
+            if (GATED)
+                sum(a.n + c, g);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = c + k;
+            if (at >= a.n)
+                continue;
+            float y = v[k];
+            if constexpr (MODE == kForward) {
+                const bool bias = a.bias && !none;
+                y += bias ? bias_at(a.bias, a.bias_f32, e * a.sb + at) : 0.0f;
+                if (a.pre)
+                    a.pre[r * a.spre + at] = Piece<uint16_t>::from_f32(y);
+                y = act_value(a.act, y);
+                if constexpr (GATED) {
+                    const float z = g[k] + (bias ? bias_at(a.bias, a.bias_f32, e * a.sb + a.n + at) : 0.0f);
+                    if (a.pre)
+                        a.pre[r * a.spre + a.n + at] = Piece<uint16_t>::from_f32(z);
+                    y *= z;
+                }
+                if (a.resid && !none)
+                    y += Piece<uint16_t>::to_f32(a.resid[r * a.sr + at]);
+            }
+            out[at] = Piece<uint16_t>::from_f32(y);
+        }
+    }
+}
+
+// A workgroup per CU takes one tile after the other: where the next one is and
+// its first loads come before the results of the last are written, so that
+// neither the search nor the first loads' latency is waited for.  A last round
+// of at most half the workgroups is taken as half tiles by all of them.
+template <int MODE, bool GATED, bool MX>
+__global__ __launch_bounds__(LinearLarge::THREADS, 2) void linear_large_kernel(LinearArgs a)
+{
+    typedef LinearTask<MODE, LinearLarge, GATED, MX> Task;
+    typedef LinearTask<MODE, LinearHalf, GATED, MX> Half;
+    typedef LinearAlternating<LinearLarge, Task::PT, Task::QT, MX> Loop;
+    typedef LinearAlternating<LinearHalf, Task::PT, Task::QT, MX> HalfLoop;
+    __shared__ __attribute__((aligned(16))) char lds[2 * Task::S::BYTES];
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+    const LinearGrid<MODE, LinearLarge, GATED> grid(a);
+    const int wgs = gridDim.x, rest = uniform(grid.total % wgs), whole = 2 * rest <= wgs ? grid.total - rest : grid.total;
+    const int padded = (whole + 255) & ~255;
+    const int wave = uniform(threadIdx.x >> 6), wp = wave >> 2, wq = wave & 3;
+    typename Task::S st;
+    st.lds0 = lds0;
+    // the next tile of this workgroup from grid number b on
+    auto next = [&](int &b, TileAt &x) {
+        for (; b < padded; b += wgs) {
+            const int t = spread(b, whole);
+            if (t >= whole)
+                continue;
+            x = grid.at(a, t);
+            b += wgs;
+            return true;
+        }
+        return false;
+    };
+    int b = blockIdx.x;
+    TileAt x, y;
+    bool more = next(b, x);
+    auto sums = [&](const TileAt &t) { return MODE == kGradW ? t.k > 0 : t.e < a.experts && t.k > 0; };
+    if (more && sums(x)) {
+        Task::operands(a, x, st);
+        Loop::first_loads(st);
+    }
+    while (more) {
+        more = next(b, y);
+        if (MODE != kGradW && x.e >= a.experts) {
+            if (more && sums(y)) {
+                Task::operands(a, y, st);
+                Loop::first_loads(st);
+            }
+            Task::clear(a, x);
         } else {
-            // tile row r: gated, fragments of 16 rows of the gate and of the
-            // value in turn
-            const int n = a.n - c0;
-            auto row = [&](int r) {
-                const int at = GATED ? (r >> 5) * 16 + (r & 15) : r;
-                return at >= n ? -1 : GATED && (r & 16) ? at + a.n : at;
-            };
-            const int last = GATED ? a.wide - 1 - c0 : min(n, TN) - 1;
-            st.q.set_rows(q + c0 * a.ldq, a.ldq, (uint32_t)(last * a.ldq) + kb, row);
-            if constexpr (MX) {
-                const int t = threadIdx.x, r = row(min(max(t - TM, 0), TN - 1));
-                st.scales = t < TM ? a.sp + (row0 + min(t, rows - 1)) * a.ldsp
-                                   : a.sq + e * a.sqe + (int64_t)(c0 + max(r, 0)) * a.ldsq;
+            float4v acc[LinearLarge::FP][LinearLarge::FQ];
+            Task::start(acc);
+            if (sums(x))
+                Loop(st, wp * 128, wq * 64).run(acc);
+            if (more && sums(y)) {
+                Task::operands(a, y, st);
+                Loop::first_loads(st);
+            }
+            Task::store(a, x, acc);
+        }
+        x = y;
+    }
+    if (whole == grid.total)
+        return;
+    const int id = spread(blockIdx.x, 2 * rest);
+    if (id >= 2 * rest)
+        return;
+    x = grid.at(a, whole + (id >> 1));
+    x.c0 += (id & 1) * Half::TJ;
+    if (x.c0 >= a.n)
+        return;
+    if (MODE != kGradW && x.e >= a.experts) {
+        Half::clear(a, x);
+        return;
+    }
+    typename Half::S hs;
+    hs.lds0 = lds0;
+    float4v acc[LinearHalf::FP][LinearHalf::FQ];
+    Half::start(acc);
+    if (sums(x)) {
+        Half::operands(a, x, hs);
+        HalfLoop::first_loads(hs);
+        HalfLoop(hs, wp * 128, wq * 32).run(acc);
+    }
+    Half::store(a, x, acc);
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Groups of few rows: bound by the weights, which go straight from memory into
+// registers, as many loads on their way as there is room for.  A workgroup has
+// 16 rows of W (gated: 16 of the gate and of the value) of one expert and up to
+// 16 FT of the group's rows at a time; its eight waves take the parts of the
+// sum and meet in LDS.
+constexpr int kFewWaves = 8;
+
+template <int NF, int FT, int U>
+__device__ __forceinline__ void few_range(const LinearArgs &a, const char *const (&w)[NF], const char *const (&x)[FT],
+                                          const bool (&there)[FT], int k0, int k1, float4v (&acc)[NF][FT])
+{
+    int k = k0;
+    for (; k + U * 32 <= k1; k += U * 32) {
+        WeightStep<false> s[NF][U];
+        bf16x8 t[FT][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+                s[i][u].load(w[i], nullptr, k + u * 32);
+#pragma unroll
+            for (int f = 0; f < FT; ++f)
+                t[f][u] = there[f] ? token_piece<false>(reinterpret_cast<const uint16_t *>(x[f]), k + u * 32, 0) : zero_piece();
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int f = 0; f < FT; ++f)
+                    acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[i][u].piece(0), t[f][u], acc[i][f], 0, 0, 0);
+    }
+    for (; k < k1; k += 32) {
+        WeightStep<false> s[NF];
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+            s[i].load_tail(w[i], nullptr, k, a.width);
+#pragma unroll
+        for (int f = 0; f < FT; ++f) {
+            const bf16x8 t = there[f] ? token_piece_tail<false>(reinterpret_cast<const uint16_t *>(x[f]), k, 0, a.width) : zero_piece();
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+                acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[i].piece(0), t, acc[i][f], 0, 0, 0);
+        }
+    }
+}
+
+template <int NF, int FT, int U>
+__device__ __forceinline__ void few_range_mx(const LinearArgs &a, const char *const (&w)[NF], const uint8_t *const (&ws)[NF],
+                                             const char *const (&x)[FT], const uint8_t *const (&xs)[FT],
+                                             const bool (&there)[FT], int k0, int k1, float4v (&acc)[NF][FT])
+{
+    auto some = [&](auto steps, int k, int end) {
+        constexpr int N = decltype(steps)::value;
+        int8v s[N][NF], t[N][FT];
+        int ss[N][NF], ts[N][FT];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                s[u][i] = scaled_values(reinterpret_cast<const uint8_t *>(w[i]), k + u * 128, end, true);
+                ss[u][i] = scaled_scale(ws[i], a.sbq, k + u * 128, end, true);
+            }
+#pragma unroll
+            for (int f = 0; f < FT; ++f) {
+                t[u][f] = scaled_values(reinterpret_cast<const uint8_t *>(x[f]), k + u * 128, end, there[f]);
+                ts[u][f] = scaled_scale(xs[f], a.sbp, k + u * 128, end, there[f]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int i = 0; i < NF; ++i)
+#pragma unroll
+                for (int f = 0; f < FT; ++f)
+                    acc[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(s[u][i], t[u][f], acc[i][f], 0, 0, 0,
+                                                                                ss[u][i], 0, ts[u][f]);
+    };
+    int k = k0;
+    for (; k + U * 128 <= k1; k += U * 128)
+        some(std::integral_constant<int, U>(), k, 1 << 30);
+    for (; k < k1; k += 128)
+        some(std::integral_constant<int, 1>(), k, a.width);
+}
+
+template <bool GATED, bool MX>
+__global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(LinearArgs a)
+{
+    constexpr int FT = 1, NF = GATED ? 2 : 1, STEP = MX ? 128 : 32, U = MX ? 4 : 8;
+    __shared__ float4v sums[kFewWaves][NF][FT][64];
+    const int e = blockIdx.y, c0 = blockIdx.x * 16, wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, fr = lane & 15;
+    int start, len;
+    group_rows(a.offs, a.experts, a.rows, e, start, len);
+    start = uniform(start);
+    len = uniform(len);
+    if (len == 0)
+        return;
+    if (e >= a.experts) {
+        for (int64_t at = threadIdx.x; at < (int64_t)len * 16; at += kFewWaves * 64) {
+            const int64_t r = start + at / 16;
+            const int c = c0 + (int)(at % 16);
+            if (c >= a.n)
+                continue;
+            a.out[r * a.so + c] = 0;
+            if (a.pre)
+                a.pre[r * a.spre + c] = 0;
+            if (a.pre && GATED)
+                a.pre[r * a.spre + a.n + c] = 0;
+        }
+        return;
+    }
+    const char *w[NF];
+    const uint8_t *ws[NF];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+        // past the last row: the last one's, whose results are dropped
+        const int64_t r = min(c0 + fr, a.n - 1) + i * a.n;
+        w[i] = a.q + e * a.qe + r * a.ldq;
+        ws[i] = MX ? a.sq + e * a.sqe + r * a.ldsq : nullptr;
+    }
+    const int steps = (a.width + STEP - 1) / STEP;
+    const int k0 = steps * wave / kFewWaves * STEP, k1 = min(steps * (wave + 1) / kFewWaves * STEP, a.width);
+    for (int first = 0; first < len; first += 16 * FT) {
+        const char *x[FT];
+        const uint8_t *xs[FT];
+        bool there[FT];
+#pragma unroll
+        for (int f = 0; f < FT; ++f) {
+            there[f] = first + f * 16 + fr < len;
+            const int64_t r = start + (there[f] ? first + f * 16 + fr : 0);
+            x[f] = a.p + r * a.ldp;
+            xs[f] = MX ? a.sp + r * a.ldsp : nullptr;
+        }
+        float4v acc[NF][FT];
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int f = 0; f < FT; ++f)
+                acc[i][f] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (MX)
+            few_range_mx<NF, FT, U>(a, w, ws, x, xs, there, k0, k1, acc);
+        else
+            few_range<NF, FT, U>(a, w, x, there, k0, k1, acc);
+        if (first)
+            __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+            for (int f = 0; f < FT; ++f)
+                sums[wave][i][f][lane] = acc[i][f];
+        __syncthreads();
+        // a lane has four columns of a row
+        for (int at = threadIdx.x; at < FT * 64; at += kFewWaves * 64) {
+            const int f = at / 64, l = at & 63, t = first + f * 16 + (l & 15);
+            if (t >= len)
+                continue;
+            float4v z[NF];
+#pragma unroll
+            for (int i = 0; i < NF; ++i) {
+                z[i] = sums[0][i][f][l];
+#pragma unroll
+                for (int v = 1; v < kFewWaves; ++v)
+                    z[i] += sums[v][i][f][l];
+            }
+            const int64_t r = start + t;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int c = c0 + 4 * (l >> 4) + k;
+                if (c >= a.n)
+                    continue;
+                float v = z[0][k] + (a.bias ? bias_at(a.bias, a.bias_f32, e * a.sb + c) : 0.0f);
+                if (a.pre)
+                    a.pre[r * a.spre + c] = Piece<uint16_t>::from_f32(v);
+                v = act_value(a.act, v);
+                if constexpr (GATED) {
+                    const float g = z[1][k] + (a.bias ? bias_at(a.bias, a.bias_f32, e * a.sb + a.n + c) : 0.0f);
+                    if (a.pre)
+                        a.pre[r * a.spre + a.n + c] = Piece<uint16_t>::from_f32(g);
+                    v *= g;
+                }
+                if (a.resid)
+                    v += Piece<uint16_t>::to_f32(a.resid[r * a.sr + c]);
+                a.out[r * a.so + c] = Piece<uint16_t>::from_f32(v);
             }
         }
     }
-    float4v acc[TILE::FP][TILE::FQ];
-#pragma unroll
-    for (int i = 0; i < TILE::FP; ++i)
-#pragma unroll
-        for (int j = 0; j < TILE::FQ; ++j)
-            acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-    const int wave = uniform(threadIdx.x >> 6), r0 = wave / TILE::WN * TILE::FP * 16, q0 = wave % TILE::WN * TILE::FQ * 16;
-    if (st.stages > 0)
-        linear_pipeline<TILE, PT, QT, MX>(st, r0, q0, acc);
-    uint16_t *out = MODE == kGradW ? a.out + e * a.oe : a.out;
-    linear_store<TILE, GATED, MODE == kForward>(lds, a, acc, e, MODE == kGradW ? i0 : row0, left, c0, a.n, out, a.so);
 }
 
 // ---------------------------------------------------------------- around them

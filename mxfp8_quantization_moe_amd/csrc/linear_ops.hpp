@@ -60,6 +60,24 @@ __device__ __forceinline__ float act_value(int act, float x)
     return x;
 }
 
+// eight values; one branch for all of them
+__device__ __forceinline__ void act_values(int act, float (&v)[8])
+{
+    if (act == kActRelu) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = act_value(kActRelu, v[k]);
+    } else if (act == kActGelu) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = act_value(kActGelu, v[k]);
+    } else if (act == kActSilu) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = act_value(kActSilu, v[k]);
+    }
+}
+
 // act'(x)
 __device__ __forceinline__ float act_slope(int act, float x)
 {

@@ -21,6 +21,7 @@
 #include <stdint.h>
 
 #include "linear_ops.hpp"
+#include "stream_ops.hpp"
 #include "mxq_device.hpp"
 #include "tile_ops.hpp"
 #include "wave_ops.hpp"
@@ -159,88 +160,11 @@ __device__ __forceinline__ int bits_before(const uint32_t *bits, int &total)
     return upto - n;
 }
 
-// ---------------------------------------------------------------- weights
-
-// Steps of a sum, 16 rows of weights and 16 tokens each.
-//   bf16  32 values: lane 16 q + i holds values 8 q .. 8 q + 7 of row i
-//   MX    64 values: lane 16 q + i holds values 16 q .. 16 q + 15 of row i, one
-//         16-byte load, and takes them as two steps of 32 (the order of a sum
-//         is free as long as weights and tokens agree); e4m3 times a power of
-//         two is exact in bf16
-template <bool MX>
-struct WeightStep;
-
-template <>
-struct WeightStep<false> {
-    static constexpr int K = 32, PIECES = 1;
-    Piece<uint16_t> v;
-    __device__ __forceinline__ void load(const LayerWeights &, const void *row, const uint8_t *, int k)
-    {
-        v = ld_piece<uint16_t>(reinterpret_cast<const uint16_t *>(row) + k + ((threadIdx.x & 63) >> 4) * 8);
-    }
-    __device__ __forceinline__ void load_tail(const LayerWeights &, const void *row, const uint8_t *, int k, int end)
-    {
-        const int c = k + ((threadIdx.x & 63) >> 4) * 8;
-        v = load8(reinterpret_cast<const uint16_t *>(row), min(c, end), end);
-    }
-    __device__ __forceinline__ bf16x8 piece(int) const { return __builtin_bit_cast(bf16x8, v.v); }
-};
-
-template <>
-struct WeightStep<true> {
-    static constexpr int K = 64, PIECES = 2;
-    uint4 v;
-    float scale;
-    __device__ __forceinline__ void load(const LayerWeights &, const void *row, const uint8_t *scales, int k)
-    {
-        const int c = k + ((threadIdx.x & 63) >> 4) * 16;
-        v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(row) + c);
-        scale = __uint_as_float((uint32_t)scales[c >> 5] << 23);
-    }
-    __device__ __forceinline__ void load_tail(const LayerWeights &w, const void *row, const uint8_t *scales, int k, int end)
-    {
-        v = make_uint4(0, 0, 0, 0);
-        scale = 1.0f;
-        if (k + (int)((threadIdx.x & 63) >> 4) * 16 < end)
-            load(w, row, scales, k);
-    }
-    __device__ __forceinline__ bf16x8 piece(int h) const
-    {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        struct Four {
-            bf16x2 p[4];
-        } r;
-        const uint32_t a = h ? v.z : v.x, b = h ? v.w : v.y;
-        r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false);
-        r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true);
-        r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false);
-        r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true);
-        return __builtin_bit_cast(bf16x8, r);
-    }
-};
-
-// the tokens' values for piece h of a step, zeros past `end`
-template <bool MX>
-__device__ __forceinline__ bf16x8 token_piece(const uint16_t *row, int k, int h)
-{
-    const int q = (threadIdx.x & 63) >> 4, c = MX ? k + q * 16 + h * 8 : k + q * 8;
-    return __builtin_bit_cast(bf16x8, ld_piece<uint16_t>(row + c).v);
-}
-template <bool MX>
-__device__ __forceinline__ bf16x8 token_piece_tail(const uint16_t *row, int k, int h, int end)
-{
-    const int q = (threadIdx.x & 63) >> 4, c = MX ? k + q * 16 + h * 8 : k + q * 8;
-    return __builtin_bit_cast(bf16x8, load8(row, min(c, end), end).v);
-}
-
-__device__ __forceinline__ bf16x8 zero_piece() { return __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0)); }
-
 // ---------------------------------------------------------------- up
 
 // acc[i][f] += rows i of weights times tokens f over [k0, k1) of the sum
 template <bool MX, int FT, int U>
-__device__ __forceinline__ void up_range(const LayerWeights &w, const void *const (&row)[2],
-                                         const uint8_t *const (&scales)[2], const uint16_t *const (&x)[FT],
+__device__ __forceinline__ void up_range(const void *const (&row)[2], const uint8_t *const (&scales)[2], const uint16_t *const (&x)[FT],
                                          const bool (&there)[FT], int k0, int k1, int end, float4v (&acc)[2][FT])
 {
     typedef WeightStep<MX> Step;
@@ -252,7 +176,7 @@ __device__ __forceinline__ void up_range(const LayerWeights &w, const void *cons
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                s[i][u].load(w, row[i], scales[i], k + u * Step::K);
+                s[i][u].load(row[i], scales[i], k + u * Step::K);
 #pragma unroll
             for (int f = 0; f < FT; ++f)
 #pragma unroll
@@ -273,7 +197,7 @@ __device__ __forceinline__ void up_range(const LayerWeights &w, const void *cons
         Step s[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            s[i].load_tail(w, row[i], scales[i], k, end);
+            s[i].load_tail(row[i], scales[i], k, end);
 #pragma unroll
         for (int h = 0; h < Step::PIECES; ++h)
 #pragma unroll
@@ -318,7 +242,7 @@ __device__ __forceinline__ void up_tokens(const LayerArgs &a, int e, int r0, con
             acc[i][f] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
     const int steps = (a.width + Step::K - 1) / Step::K;
     up_range<MX, FT, FT == 1 ? 8 / Step::PIECES : 4 / Step::PIECES>(
-        a.up, row, scales, x, there, steps * wave / 4 * Step::K, min(steps * (wave + 1) / 4 * Step::K, a.width), a.width, acc);
+        row, scales, x, there, steps * wave / 4 * Step::K, min(steps * (wave + 1) / 4 * Step::K, a.width), a.width, acc);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -500,9 +424,9 @@ __global__ __launch_bounds__(kLayerThreads) void layer_down_kernel(LayerArgs a, 
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             if (whole)
-                s[i].load(a.down, row, scales, k0 + i * Step::K);
+                s[i].load(row, scales, k0 + i * Step::K);
             else
-                s[i].load_tail(a.down, row, scales, k0 + i * Step::K, a.hidden);
+                s[i].load_tail(row, scales, k0 + i * Step::K, a.hidden);
         }
 #pragma unroll
         for (int f = 0; f < FT; ++f) {

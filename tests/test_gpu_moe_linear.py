@@ -129,6 +129,39 @@ def test_strides_and_alignment(pad, shift):
     check(80, 104, 72, [31, 49], "silu", True, None, True, pad=pad, shift=shift)
 
 
+def spread(total, parts, seed, empty=()):
+    """Group sizes that sum to `total`, none of them round, some empty."""
+    g = torch.Generator().manual_seed(seed)
+    w = torch.rand(parts, generator=g) + 0.2
+    w[list(empty)] = 0
+    sizes = (w / w.sum() * total).long()
+    sizes[int(w.argmax())] += total - int(sizes.sum())
+    return sizes.tolist()
+
+
+# by the extents alone (rows, width, n, experts): calls of up to 16 rows; small
+# tiles; long sums in parts; more small tiles than fit at a time; large tiles as
+# halves alone, in whole rounds, in rounds and halves
+EXTENTS = [(1, 520, 96, None), (16, 1032, 40, None), (11, 264, 33, spread(9, 6, 0)), (16, 3000, 24, spread(16, 3, 1)),
+           (200, 2048, 72, None), (130, 4104, 136, spread(120, 4, 2, [1])), (90, 1160, 1030, None),
+           (1100, 72, 3400, None), (1000, 136, 1500, spread(980, 20, 3, [0, 7])),
+           (2400, 136, 1800, None), (2500, 200, 2050, spread(2444, 5, 4, [2])),
+           (4400, 72, 6000, spread(4300, 3, 5)), (4608, 136, 4100, None), (8200, 64, 2300, spread(8192, 9, 6, [8]))]
+
+
+@pytest.mark.parametrize("rows,width,n,sizes", EXTENTS)
+def test_every_kernel(rows, width, n, sizes):
+    check(rows, width, n, sizes, "gelu", False, torch.float32, True)
+    check(rows, width, n // 2, sizes, "silu", True, torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,width,n,sizes", [(9000, 72, 130, None), (20000, 136, 70, spread(19990, 2, 7)),
+                                                (3000, 200, 2304, spread(2900, 3, 8, [0])), (700, 2300, 2200, spread(650, 4, 9))])
+def test_long_sums_over_rows(rows, width, n, sizes):
+    """Weight gradients of many rows: parts of few small tiles, and large tiles."""
+    check(rows, width, n, sizes, "relu", False, torch.float32)
+
+
 def test_repeated_rows():
     """One row for all tokens, one matrix for all experts, an expanded gradient."""
     x, w, offs, _, _ = make(90, 64, 64, [40, 50], False, None, False)
@@ -214,6 +247,36 @@ def mx(x):
 MX_SUM = 2.0 ** -9
 
 
+def test_captured_and_replayed():
+    """Forward and gradients of one layer in a graph: every replay, with eager
+    work and a synchronization between, gives the eager call's bits."""
+    rows, width, n, sizes = 700, 264, 132, [300, 0, 377]
+    x, w, offs, b, _ = make(rows, width, n, sizes, True, torch.float32, False)
+    dy = normal(rows, n, seed=8)
+
+    def step():
+        y, pre = mxq.moe_linear(x, w, offs, bias=b, activation="silu", gated=True, save_pre=True)
+        return (y, pre) + mxq.moe_linear_backward(dy, x, w, offs, pre=pre, activation="silu", gated=True, bias=True)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for seed in range(4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for t in (x, w, dy):
+            t.normal_(generator=g)
+        offs.copy_(offsets([100 * seed, 50, 500 - 100 * seed]))
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(outs, want))
+
+
 def check_mx(rows, width, n, sizes=None, act="none", gated=False, bias=None, resid=False):
     x, w, offs, b, r = make(rows, width, n, sizes, gated, bias, resid)
     # blocks of very different size: the scales matter
@@ -240,6 +303,13 @@ def test_mx_widths(width):
 def test_mx_sizes(rows, n, sizes):
     for gated in (False, True):
         check_mx(rows, 320, n, sizes, "gelu", gated, torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,width,n,sizes", EXTENTS)
+def test_every_mx_kernel(rows, width, n, sizes):
+    width = (width + 31) // 32 * 32
+    check_mx(rows, width, n, sizes, "gelu", False, torch.float32, True)
+    check_mx(rows, 4 * width, n // 2, sizes, "silu", True, torch.bfloat16)
 
 
 def test_mx_weights_along_n():
