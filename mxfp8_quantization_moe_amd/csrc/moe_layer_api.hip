@@ -24,19 +24,20 @@ bool sizes_ok(int64_t tokens, int64_t width, int64_t hidden, int32_t experts, in
            k <= experts;
 }
 
-// Workgroups per 16 rows of the down product, each with a part of its sums.
+// Workgroups per 8 rows of the down product, each with a part of its sums: as
+// many as fill the CUs, with some steps for every wave.
 int layer_splits(int64_t tokens, int64_t width, int64_t hidden, int32_t experts, int32_t k)
 {
-    const int64_t blocks = (width + 15) / 16, units = std::min<int64_t>(experts, tokens * k) * ((hidden + kUnit - 1) / kUnit);
+    const int64_t blocks = (width + 7) / 8, steps = std::min<int64_t>(experts, tokens * k) * ((hidden + 63) / 64);
     int s = 1;
-    while (s < 8 && blocks * s < 512 && units >= 8 * s)
+    while (s < 8 && blocks * s <= 128 && steps >= 8 * kDownWaves * s)
         s *= 2;
     return s;
 }
 
 struct LayerLayout {
-    int64_t ids, share, hi, lo, parts, bytes;
-    int hp, splits;
+    int64_t ids, share, active, begin, order, hi, lo, parts, bytes;
+    int hp, splits, most;
 };
 
 LayerLayout layer_layout(int64_t tokens, int64_t width, int64_t hidden, int32_t experts, int32_t k)
@@ -45,12 +46,22 @@ LayerLayout layer_layout(int64_t tokens, int64_t width, int64_t hidden, int32_t 
     const int64_t slots = tokens * k;
     l.hp = (int)round_up(hidden, 8);
     l.splits = layer_splits(tokens, width, hidden, experts, k);
-    l.ids = 0;
-    l.share = round_up(slots * 4, 16);
-    l.hi = l.share + round_up(slots * 4, 16);
-    l.lo = l.hi + slots * l.hp * 2;
-    l.parts = l.lo + slots * l.hp * 2;
-    l.bytes = l.parts + (l.splits > 1 ? l.splits * tokens * width * 4 : 0);
+    l.most = (int)std::min<int64_t>(experts, slots);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t from = at;
+        at += round_up(bytes, 16);
+        return from;
+    };
+    l.ids = take(slots * 4);
+    l.share = take(slots * 4);
+    l.active = take(l.most * 4);
+    l.begin = take((l.most + 2) * 4);
+    l.order = take(slots * 4);
+    l.hi = take(slots * l.hp * 2);
+    l.lo = take(slots * l.hp * 2);
+    l.parts = take(l.splits > 1 ? l.splits * tokens * width * 4 : 0);
+    l.bytes = at;
     return l;
 }
 
@@ -73,42 +84,40 @@ mxq_status weights_status(const void *w, const uint8_t *scales, int32_t format, 
     return MXQ_OK;
 }
 
+// 16 rows of U per workgroup where 32 would leave fewer than four workgroups per
+// CU, else 32, for half the searches and half the loads of the tokens' values.
 template <typename T, bool MX, bool GATED>
-void launch_up(const LayerArgs &a, bool select, hipStream_t st)
+void launch_up(const LayerArgs &a, hipStream_t st)
 {
-    const int slots = a.tokens * a.k, rows = GATED ? 16 : 32;
-    const dim3 grid((unsigned)((a.hidden + rows - 1) / rows), (unsigned)std::min(a.experts, slots));
-    // the waves' sums of up to 16, 32 or 64 tokens
-    const int ft = a.tokens <= 16 ? 1 : a.tokens <= 32 ? 2 : 4;
-    const size_t lds = ((slots * 8 + 15) & ~15) + (size_t)4 * 2 * ft * 64 * 16;
-    auto go = [&](auto kernel) { kernel<<<grid, dim3(kLayerThreads), lds, st>>>(a); };
-    if (ft > 1)
-        go(layer_up_kernel<T, MX, GATED, 4, false>);
+    auto grid = [&](int fragments) {
+        const int rows = (GATED ? 8 : 16) * fragments;
+        return dim3((unsigned)((a.hidden + rows - 1) / rows), (unsigned)a.most);
+    };
+    auto go = [&](auto kernel, int fragments) { kernel<<<grid(fragments), dim3(kLayerThreads), 0, st>>>(a); };
+    if (a.tokens == 1)
+        go(layer_up_one_kernel<T, MX, GATED>, 1);
+    else if (a.tokens <= 16)
+        (int64_t)grid(2).x * a.most < 1024 ? go(layer_up_kernel<MX, GATED, 1, 1>, 1) : go(layer_up_kernel<MX, GATED, 2, 1>, 2);
     else
-        select ? go(layer_up_kernel<T, MX, GATED, 1, true>) : go(layer_up_kernel<T, MX, GATED, 1, false>);
+        a.tokens <= 32 ? go(layer_up_kernel<MX, GATED, 2, 2>, 2) : go(layer_up_kernel<MX, GATED, 2, 4>, 2);
 }
 
 template <bool MX>
 void launch_down(const LayerArgs &a, hipStream_t st)
 {
-    const int most = std::min(a.experts, a.tokens * a.k);
-    const dim3 grid((unsigned)((a.width + 15) / 16), (unsigned)a.splits);
-    const size_t lds = round_up((most + a.experts) * 2 + most * a.tokens, 16);
-    auto go = [&](auto kernel) { kernel<<<grid, dim3(kLayerThreads), lds, st>>>(a, most); };
-    a.tokens <= 16 ? go(layer_down_kernel<MX, 1>) : a.tokens <= 32 ? go(layer_down_kernel<MX, 2>) : go(layer_down_kernel<MX, 4>);
+    const dim3 grid((unsigned)((a.width + 7) / 8), (unsigned)a.splits);
+    constexpr int WAVES = MX ? kDownWavesMx : kDownWaves;
+    const size_t lds = ((size_t)WAVES * 2 * a.tokens * 8 + 2 * a.most + 1 + a.tokens * a.k) * 4;
+    auto go = [&](auto kernel) { kernel<<<grid, dim3(WAVES * 64), lds, st>>>(a); };
+    a.hidden % (2 * WeightStep<MX>::K) == 0 ? go(layer_down_kernel<MX, true>) : go(layer_down_kernel<MX, false>);
 }
-
-// tokens up to which every workgroup selects for itself instead of waiting for
-// a kernel that does (at most 16)
-constexpr int kSelectTokens = 8;
 
 template <typename T, bool MX>
 void launch_layer(const LayerArgs &a, int gated, hipStream_t st)
 {
-    const bool inside = a.tokens <= kSelectTokens;
-    if (!inside)
-        layer_select_kernel<T><<<dim3((unsigned)a.tokens), dim3(64), 0, st>>>(a);
-    gated ? launch_up<T, MX, true>(a, inside, st) : launch_up<T, MX, false>(a, inside, st);
+    if (a.tokens > 1)
+        layer_select_kernel<T><<<dim3(1), dim3(kSelectThreads), 0, st>>>(a);
+    gated ? launch_up<T, MX, true>(a, st) : launch_up<T, MX, false>(a, st);
     launch_down<MX>(a, st);
     if (a.splits > 1)
         layer_join_kernel<<<dim3((unsigned)((a.width + kLayerThreads - 1) / kLayerThreads), (unsigned)a.tokens),
@@ -181,6 +190,10 @@ mxq_status mxq_moe_layer(const uint16_t *x, int64_t tokens, int64_t width, int64
     a.sy = sy_t;
     a.ids = reinterpret_cast<int32_t *>(ws + l.ids);
     a.share = reinterpret_cast<float *>(ws + l.share);
+    a.active = reinterpret_cast<int32_t *>(ws + l.active);
+    a.begin = reinterpret_cast<int32_t *>(ws + l.begin);
+    a.order = reinterpret_cast<int32_t *>(ws + l.order);
+    a.most = l.most;
     a.hi = reinterpret_cast<uint16_t *>(ws + l.hi);
     a.lo = reinterpret_cast<uint16_t *>(ws + l.lo);
     a.hp = l.hp;
@@ -191,8 +204,8 @@ mxq_status mxq_moe_layer(const uint16_t *x, int64_t tokens, int64_t width, int64
     if (hidden == 0) {
         // nothing to multiply: biases and residual alone
         a.splits = 0;
-        logits_dtype == MXQ_BF16 ? layer_select_kernel<uint16_t><<<dim3((unsigned)tokens), dim3(64), 0, st>>>(a)
-                                 : layer_select_kernel<float><<<dim3((unsigned)tokens), dim3(64), 0, st>>>(a);
+        logits_dtype == MXQ_BF16 ? layer_select_kernel<uint16_t><<<dim3(1), dim3(kSelectThreads), 0, st>>>(a)
+                                 : layer_select_kernel<float><<<dim3(1), dim3(kSelectThreads), 0, st>>>(a);
         layer_join_kernel<<<dim3((unsigned)((width + kLayerThreads - 1) / kLayerThreads), (unsigned)tokens),
                             dim3(kLayerThreads), 0, st>>>(a);
     } else if (logits_dtype == MXQ_BF16) {
