@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "mxq.h"
 #include "api_common.hpp"
@@ -402,15 +403,16 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
 
 namespace {
 
-// slices of kSliceRows rows that any group ends can need
-int64_t slice_count(int64_t rows, int32_t experts, bool grouped)
+// Rows of a slice of the activation's gradient: 64, or 16 where that leaves less
+// than four workgroups per CU (6147 x 777 over 13 experts 25 us with 64).
+int slice_rows(int64_t rows, int32_t experts, int64_t n)
 {
-    return row_tiles(rows, experts, grouped, kSliceRows);
+    return usual_row_tiles(rows, experts, 64) * ((n + 511) / 512) < 4 * kCUs ? 16 : 64;
 }
 
-int64_t slices_bytes(int64_t rows, int32_t experts, int64_t wide)
+int64_t slices_bytes(int64_t rows, int32_t experts, int64_t wide, int64_t n)
 {
-    return round_up(slice_count(rows, experts, true) * wide * 4, 256);
+    return round_up(row_tiles(rows, experts, true, slice_rows(rows, experts, n)) * wide * 4, 256);
 }
 
 }  // namespace
@@ -421,7 +423,7 @@ int64_t mxq_moe_linear_backward_workspace_bytes(int64_t rows, int64_t width, int
     if (!sizes_ok(rows, width, num_experts, wide) || !act_ok(activation, gated, wide))
         return -1;
     const Rows z = {nullptr, 0, 0, rows, wide}, x = {nullptr, 0, 0, rows, width}, w = {nullptr, 0, 0, wide, width};
-    int64_t need = bias ? slices_bytes(rows, num_experts, wide) : 0;
+    int64_t need = bias ? slices_bytes(rows, num_experts, wide, gated ? wide / 2 : wide) : 0;
     if (activation != MXQ_ACT_NONE || gated || !aligned || wide % 8)
         need += z.packed_bytes(1);
     if (!aligned || width % 8)
@@ -455,7 +457,7 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         return MXQ_ERR_INVALID_ARG;
     const Rows yr = {grad_y, 0, sg_r, rows, n}, zr = {nullptr, 0, 0, rows, wide}, xr = {x, 0, sx_r, rows, width},
                wr = {w, sw_e, sw_n, wide, width};
-    int64_t need = grad_bias ? slices_bytes(rows, num_experts, wide) : 0;
+    int64_t need = grad_bias ? slices_bytes(rows, num_experts, wide, n) : 0;
     if (saved || !yr.direct())
         need += zr.packed_bytes(1);
     if (grad_w && !xr.direct())
@@ -480,7 +482,8 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
     a.width = (int)width;
     a.wide = (int)wide;
     a.act = activation;
-    float *parts = grad_bias ? reinterpret_cast<float *>(room.take(slices_bytes(rows, num_experts, wide))) : nullptr;
+    float *parts = grad_bias ? reinterpret_cast<float *>(room.take(slices_bytes(rows, num_experts, wide, n))) : nullptr;
+    const int slice = slice_rows(rows, num_experts, n);
     Rows z = yr;
     if (saved) {
         z = {room.take(zr.packed_bytes(1)), 0, round_up(wide, 8), rows, wide};
@@ -488,16 +491,29 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         z = readable(yr, 1, room, st);
     }
     if (rows > 0 && wide > 0 && (saved || parts)) {
-        const int64_t slices = slice_count(rows, num_experts, offs != nullptr);
+        const int64_t slices = row_tiles(rows, num_experts, offs != nullptr, slice);
         const dim3 grid((unsigned)std::min<int64_t>(slices, 1 << 20), (unsigned)((n + 511) / 512));
         uint16_t *dz = const_cast<uint16_t *>(reinterpret_cast<const uint16_t *>(z.p));
         auto go = [&](auto kernel) {
             kernel<<<grid, dim3(256), 0, st>>>(a, grad_y, sg_r, pre, sp_r, saved ? dz : nullptr, z.sr, parts);
         };
-        gated ? go(linear_dact_kernel<true, true>) : saved ? go(linear_dact_kernel<false, true>) : go(linear_dact_kernel<false, false>);
+        auto by_act = [&](auto g, auto sl) {
+            constexpr bool G = decltype(g)::value;
+            constexpr int S = decltype(sl)::value;
+            switch (activation) {
+            case MXQ_ACT_RELU: go(linear_dact_kernel<G, true, kActRelu, S>); break;
+            case MXQ_ACT_GELU: go(linear_dact_kernel<G, true, kActGelu, S>); break;
+            case MXQ_ACT_SILU: go(linear_dact_kernel<G, true, kActSilu, S>); break;
+            default: go(linear_dact_kernel<G, G, kActNone, S>); break;
+            }
+        };
+        auto by_slice = [&](auto g) {
+            slice == 16 ? by_act(g, std::integral_constant<int, 16>()) : by_act(g, std::integral_constant<int, 64>());
+        };
+        gated ? by_slice(std::true_type()) : by_slice(std::false_type());
     }
     if (grad_bias && wide > 0)
-        linear_bias_kernel<<<dim3((unsigned)((wide + 255) / 256), (unsigned)num_experts), dim3(256), 0, st>>>(a, parts, grad_bias);
+        linear_bias_kernel<<<dim3((unsigned)((wide + 63) / 64), (unsigned)num_experts), dim3(256), 0, st>>>(a, slice, parts, grad_bias);
     a.p = reinterpret_cast<const char *>(z.p);
     a.ldp = z.sr * 2;
     a.n = (int)width;

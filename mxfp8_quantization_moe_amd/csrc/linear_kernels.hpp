@@ -1278,67 +1278,83 @@ __global__ __launch_bounds__(256) void linear_pack_scales_kernel(const uint8_t *
 }
 
 // dz from dy and the saved z (PRE), and the columns' sums over each group in
-// parts of kSliceRows rows.
+// parts of SLICE rows.
 //   plain  dz = dy act'(z)        gated  dz = [dy value act'(gate), dy act(gate)]
 // dz is rounded to bf16, the type that the two products take; the sums are of
 // the values before that rounding.  A wave has every fourth row of a slice and
 // 512 columns.
-constexpr int kSliceRows = 64;
-
-template <bool GATED, bool PRE>
+template <bool GATED, bool PRE, int ACT, int SLICE>
 __global__ __launch_bounds__(256) void linear_dact_kernel(LinearArgs a, const uint16_t *__restrict__ dy, int64_t sy,
                                                           const uint16_t *__restrict__ pre, int64_t spre,
                                                           uint16_t *dz, int64_t sdz, float *parts)
 {
     __shared__ float sums[4][GATED ? 2 : 1][512];
-    const int slices = count_row_tiles<kSliceRows>(a);
+    const int slices = count_row_tiles<SLICE>(a);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = GATED ? a.wide / 2 : a.wide;
     const int c = blockIdx.y * 512 + lane * 8;
     for (int s = blockIdx.x; s < slices; s += gridDim.x) {
         int e, row0, left;
-        find_row_tile<kSliceRows>(a, s, e, row0, left);
+        find_row_tile<SLICE>(a, s, e, row0, left);
         if (e >= a.experts)
             return;  // and so are all slices after it
-        const int end = min(left, kSliceRows);
+        const int end = min(left, SLICE);
         float total[GATED ? 2 : 1][8] = {};
-        for (int r = wave; r < end && c < n; r += 4) {
-            const int64_t row = (int64_t)row0 + r;
-            const Piece<uint16_t> d = load8(dy + row * sy, c, n);
-            float g[8], v[8];
+        // four rows at a time: their loads before their values
+        constexpr int AT_ONCE = 4;
+        for (int r0 = wave; r0 < end && c < n; r0 += 4 * AT_ONCE) {
+            Piece<uint16_t> d[AT_ONCE], z[AT_ONCE], w[AT_ONCE];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                g[k] = d.get(k);
-            if constexpr (PRE) {
-                const Piece<uint16_t> z = load8(pre + row * spre, c, n);
-                uint16_t *to = dz + row * sdz;
-                if constexpr (GATED) {
-                    const Piece<uint16_t> w = load8(pre + row * spre + n, c, n);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        v[k] = g[k] * act_value(a.act, z.get(k));
-                        g[k] = g[k] * w.get(k) * act_slope(a.act, z.get(k));
-                    }
-                    store8(to, c, n, g);
-                    store8(to + n, c, n, v);
-                    if (c + 8 >= n)
-                        for (int k = 2 * n; k < sdz; ++k)  // the padding
-                            to[k] = 0;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        g[k] *= act_slope(a.act, z.get(k));
-                    if (c + 8 > n)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            g[k] = c + k < n ? g[k] : 0.0f;
-                    store8(to, c, (int)sdz, g);
-                }
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int64_t row = (int64_t)row0 + min(r0 + 4 * i, end - 1);
+                d[i] = load8(dy + row * sy, c, n);
+                if constexpr (PRE)
+                    z[i] = load8(pre + row * spre, c, n);
+                if constexpr (GATED)
+                    w[i] = load8(pre + row * spre + n, c, n);
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                total[0][k] += g[k];
-                if constexpr (GATED)
-                    total[1][k] += v[k];
+            for (int i = 0; i < AT_ONCE; ++i) {
+                if (r0 + 4 * i >= end)
+                    continue;
+                float g[8], v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    g[k] = d[i].get(k);
+                if constexpr (PRE) {
+                    uint16_t *to = dz + ((int64_t)row0 + r0 + 4 * i) * sdz;
+                    if constexpr (GATED) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float y, slope;
+                            act_both(ACT, z[i].get(k), y, slope);
+                            v[k] = g[k] * y;
+                            g[k] = g[k] * w[i].get(k) * slope;
+                        }
+                        store8(to, c, n, g);
+                        store8(to + n, c, n, v);
+                        if (c + 8 >= n)
+                            for (int k = 2 * n; k < sdz; ++k)  // the padding
+                                to[k] = 0;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float y, slope;
+                            act_both(ACT, z[i].get(k), y, slope);
+                            g[k] *= slope;
+                        }
+                        if (c + 8 > n)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                g[k] = c + k < n ? g[k] : 0.0f;
+                        store8(to, c, (int)sdz, g);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    total[0][k] += g[k];
+                    if constexpr (GATED)
+                        total[1][k] += v[k];
+                }
             }
         }
         if (!parts)
@@ -1359,15 +1375,17 @@ __global__ __launch_bounds__(256) void linear_dact_kernel(LinearArgs a, const ui
     }
 }
 
-// The slices' sums of each group, in order, in fp64.
-__global__ __launch_bounds__(256) void linear_bias_kernel(LinearArgs a, const float *__restrict__ parts,
+// The slices' sums of each group in fp64: a workgroup per group and 64 columns,
+// every fourth slice to a wave, the waves in order.
+__global__ __launch_bounds__(256) void linear_bias_kernel(LinearArgs a, int slice, const float *__restrict__ parts,
                                                           float *__restrict__ out)
 {
-    const int e = blockIdx.y;
+    __shared__ double sums[4][64];
+    const int e = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     int before = 0, own = 0, start, len;
-    for (int g = threadIdx.x & 63; g <= e; g += 64) {
+    for (int g = lane; g <= e; g += 64) {
         group_rows(a.offs, a.experts, a.rows, g, start, len);
-        const int n = (len + kSliceRows - 1) / kSliceRows;
+        const int n = (len + slice - 1) / slice;
         (g < e ? before : own) += n;
     }
 #pragma unroll
@@ -1375,13 +1393,18 @@ __global__ __launch_bounds__(256) void linear_bias_kernel(LinearArgs a, const fl
         before += __shfl_xor(before, m, 64);
         own += __shfl_xor(own, m, 64);
     }
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.wide)
-        return;
+    const int c = blockIdx.x * 64 + lane;
     double s = 0.0;
-    for (int i = 0; i < own; ++i)
-        s += parts[(int64_t)(before + i) * a.wide + c];
-    out[(int64_t)e * a.wide + c] = (float)s;
+    if (c < a.wide) {
+        const float *p = parts + (int64_t)before * a.wide + c;
+#pragma unroll 8
+        for (int i = wave; i < own; i += 4)
+            s += p[(int64_t)i * a.wide];
+    }
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < a.wide)
+        out[(int64_t)e * a.wide + c] = (float)((sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]));
 }
 
 }  // namespace mxq

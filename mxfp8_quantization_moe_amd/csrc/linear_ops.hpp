@@ -78,21 +78,24 @@ __device__ __forceinline__ void act_values(int act, float (&v)[8])
     }
 }
 
-// act'(x)
-__device__ __forceinline__ float act_slope(int act, float x)
+// act(x) and act'(x)
+__device__ __forceinline__ void act_both(int act, float x, float &y, float &slope)
 {
-    if (act == kActRelu)
-        return x > 0.0f ? 1.0f : 0.0f;
-    if (act == kActGelu) {
+    y = x;
+    slope = 1.0f;
+    if (act == kActRelu) {
+        y = act_value(kActRelu, x);
+        slope = x > 0.0f ? 1.0f : 0.0f;
+    } else if (act == kActGelu) {
         float cdf, e;
         normal_cdf(x, cdf, e);
-        return fmaf(x * 0.39894228f, e, cdf);
-    }
-    if (act == kActSilu) {
+        y = x * cdf;
+        slope = fmaf(x * 0.39894228f, e, cdf);
+    } else if (act == kActSilu) {
         const float s = sigmoid(x);
-        return s * fmaf(x, 1.0f - s, 1.0f);
+        y = x * s;
+        slope = s * fmaf(x, 1.0f - s, 1.0f);
     }
-    return 1.0f;
 }
 
 __device__ __forceinline__ float bias_at(const void *bias, int f32, int64_t at)
