@@ -11,7 +11,8 @@ allocated on that stream.
 from __future__ import annotations
 
 from . import MXQError, _check, _torch
-from ._capi import (MXQ_ACT_GELU, MXQ_ACT_NONE, MXQ_ACT_RELU, MXQ_ACT_SILU, MXQ_BF16, MXQ_ERR_INVALID_ARG, MXQ_F32,
+from ._capi import (MXQ_ACT_GELU, MXQ_ACT_NONE, MXQ_ACT_RELU, MXQ_ACT_SILU, MXQ_BF16, MXQ_ERR_INVALID_ARG,
+                    MXQ_ERR_WORKSPACE, MXQ_F32,
                     mxq_moe_layer, mxq_moe_layer_workspace_bytes, mxq_moe_linear, mxq_moe_linear_backward, mxq_moe_linear_backward_workspace_bytes,
                     mxq_moe_linear_mx, mxq_moe_linear_mx_workspace_bytes, mxq_moe_linear_workspace_bytes)
 from .moe import _plain, _run, _unit
@@ -61,39 +62,45 @@ def _experts(w, x_width: int, offs, device, dtype, name: str):
     return w
 
 
-class _Epilogue:
-    """Bias, activation, gate and residual of a call, checked, and its
-    outputs."""
-
-    def __init__(self, rows, E, wide, device, bias, activation, gated, residual):
+def _epilogue(rows, E, wide, device, bias, activation, gated, residual):
+    """(columns of the result, the C call's arguments from bias to residual),
+    checked."""
+    act, gated = _activation(activation), 1 if gated else 0
+    if gated and wide % 2:
+        raise TypeError(f"a gated product needs an even number of weight rows, got {wide}")
+    n = wide // 2 if gated else wide
+    b = bs = 0
+    dtype = MXQ_F32
+    if bias is not None:
         torch = _torch()
-        self.act, self.gated = _activation(activation), int(bool(gated))
-        if self.gated and wide % 2:
-            raise TypeError(f"a gated product needs an even number of weight rows, got {wide}")
-        self.n = wide // 2 if self.gated else wide
-        if bias is not None:
-            if bias.dim() == 1:
-                bias = bias[None]
-            if (bias.dtype not in (torch.bfloat16, torch.float32) or bias.shape != (E, wide) or bias.device != device
-                    or wide > 1 and bias.stride(1) != 1):
-                raise TypeError(f"bias must be a bfloat16 or float32 tensor of shape {(E, wide)} and unit stride on "
-                                f"{device}, got {bias.dtype} {tuple(bias.shape)} on {bias.device}")
-        if residual is not None:
-            _rows(residual, (rows, self.n), device, "residual")
-        self.bias, self.residual = bias, residual
-
-    def args(self, y, pre):
-        b, r = self.bias, self.residual
-        return (0 if b is None else b.data_ptr(), MXQ_BF16 if b is not None and b.dtype == _torch().bfloat16 else MXQ_F32,
-                0 if b is None else b.stride(0), self.act, self.gated, 0 if r is None else r.data_ptr(),
-                0 if r is None else r.stride(0), 1 if r is None else r.stride(1), y.data_ptr(), max(self.n, 1), 1,
-                0 if pre is None else pre.data_ptr(), 0 if pre is None else pre.stride(0), 1)
+        if bias.dim() == 1:
+            bias = bias[None]
+        if (bias.dtype not in (torch.bfloat16, torch.float32) or bias.shape != (E, wide) or bias.device != device
+                or wide > 1 and bias.stride(1) != 1):
+            raise TypeError(f"bias must be a bfloat16 or float32 tensor of shape {(E, wide)} and unit stride on "
+                            f"{device}, got {bias.dtype} {tuple(bias.shape)} on {bias.device}")
+        b, bs = bias.data_ptr(), bias.stride(0)
+        if bias.dtype is torch.bfloat16:
+            dtype = MXQ_BF16
+    r, rs, rc = 0, 0, 1
+    if residual is not None:
+        _rows(residual, (rows, n), device, "residual")
+        r = residual.data_ptr()
+        rs, rc = residual.stride()
+    return n, (b, dtype, bs, act, gated, r, rs, rc)
 
 
-def _workspace(need: int, what: str, device):
-    if need < 0:
-        raise MXQError(MXQ_ERR_INVALID_ARG, what)
-    return _torch().empty(need, dtype=_torch().uint8, device=device) if need else None
+def _call(fn, what: str, args, need, device, st) -> None:
+    """The C call without a workspace, which most need not have; if it asks for
+    one, of need() bytes, once more with it."""
+    code = fn(*args, 0, 0, st)
+    if code == MXQ_ERR_WORKSPACE:
+        n = need()
+        if n < 0:
+            raise MXQError(MXQ_ERR_INVALID_ARG, what)
+        ws = _torch().empty(n, dtype=_torch().uint8, device=device)
+        code = fn(*args, ws.data_ptr(), n, st)
+    _check(code, what)
 
 
 def _ptr(t) -> int:
@@ -116,16 +123,15 @@ def moe_linear(x, w, offs=None, *, bias=None, activation: str = "none", gated: b
     rows, width = x.shape
     w = _experts(w, width, offs, x.device, torch.bfloat16, "w")
     E, wide, _ = w.shape
-    ep = _Epilogue(rows, E, wide, x.device, bias, activation, gated, residual)
+    n, epilogue = _epilogue(rows, E, wide, x.device, bias, activation, gated, residual)
 
     def call(st):
-        y = torch.empty((rows, ep.n), dtype=x.dtype, device=x.device)
+        y = torch.empty((rows, n), dtype=x.dtype, device=x.device)
         pre = torch.empty((rows, wide), dtype=x.dtype, device=x.device) if save_pre else None
-        need = mxq_moe_linear_workspace_bytes(rows, width, E, wide, _aligned(x, w))
-        ws = _workspace(need, "mxq_moe_linear", x.device)
-        code = mxq_moe_linear(x.data_ptr(), rows, width, *x.stride(), w.data_ptr(), E, wide, *w.stride(), _ptr(offs),
-                              *ep.args(y, pre), _ptr(ws), max(need, 0), st)
-        _check(code, "mxq_moe_linear")
+        _call(mxq_moe_linear, "mxq_moe_linear",
+              (x.data_ptr(), rows, width, *x.stride(), w.data_ptr(), E, wide, *w.stride(), _ptr(offs), *epilogue,
+               y.data_ptr(), n or 1, 1, _ptr(pre), wide or 1, 1),
+              lambda: mxq_moe_linear_workspace_bytes(rows, width, E, wide, _aligned(x, w)), x.device, st)
         return (y, pre) if save_pre else y
 
     return _run(x, stream, call)
@@ -142,9 +148,11 @@ def moe_linear_backward(grad_y, x, w, offs=None, *, pre=None, activation: str = 
     rows, width = x.shape
     w = _experts(w, width, offs, x.device, torch.bfloat16, "w")
     E, wide, _ = w.shape
-    ep = _Epilogue(rows, E, wide, x.device, None, activation, gated, None)
-    _rows(grad_y, (rows, ep.n), x.device, "grad_y")
-    saved = ep.act != MXQ_ACT_NONE or ep.gated
+    act, gated = _activation(activation), 1 if gated else 0
+    if gated and wide % 2:
+        raise TypeError(f"a gated product needs an even number of weight rows, got {wide}")
+    _rows(grad_y, (rows, wide // 2 if gated else wide), x.device, "grad_y")
+    saved = act != MXQ_ACT_NONE or gated
     if saved:
         if pre is None:
             raise TypeError("an activation or a gate needs pre, what moe_linear(..., save_pre=True) returned")
@@ -152,18 +160,15 @@ def moe_linear_backward(grad_y, x, w, offs=None, *, pre=None, activation: str = 
 
     def call(st):
         g = _unit(grad_y)
-        new = lambda *s, dtype=x.dtype: torch.empty(s, dtype=dtype, device=x.device)  # noqa: E731
-        dx = new(rows, width) if need_x else None
-        dw = new(E, wide, width) if need_w else None
-        db = new(E, wide, dtype=torch.float32) if bias else None
-        need = mxq_moe_linear_backward_workspace_bytes(rows, width, E, wide, ep.act, ep.gated, int(bool(bias)),
-                                                       _aligned(g, x, w))
-        ws = _workspace(need, "mxq_moe_linear_backward", x.device)
-        code = mxq_moe_linear_backward(
-            g.data_ptr(), *g.stride(), x.data_ptr(), rows, width, *x.stride(), w.data_ptr(), E, wide, *w.stride(),
-            _ptr(offs), pre.data_ptr() if saved else 0, pre.stride(0) if saved else 0, pre.stride(1) if saved else 1,
-            ep.act, ep.gated, _ptr(dx), width, 1, _ptr(dw), wide * width, width, 1, _ptr(db), _ptr(ws), max(need, 0), st)
-        _check(code, "mxq_moe_linear_backward")
+        dx = torch.empty((rows, width), dtype=x.dtype, device=x.device) if need_x else None
+        dw = torch.empty((E, wide, width), dtype=x.dtype, device=x.device) if need_w else None
+        db = torch.empty((E, wide), dtype=torch.float32, device=x.device) if bias else None
+        _call(mxq_moe_linear_backward, "mxq_moe_linear_backward",
+              (g.data_ptr(), *g.stride(), x.data_ptr(), rows, width, *x.stride(), w.data_ptr(), E, wide, *w.stride(),
+               _ptr(offs), pre.data_ptr() if saved else 0, pre.stride(0) if saved else 0, pre.stride(1) if saved else 1,
+               act, gated, _ptr(dx), width, 1, _ptr(dw), wide * width, width, 1, _ptr(db)),
+              lambda: mxq_moe_linear_backward_workspace_bytes(rows, width, E, wide, act, gated, 1 if bias else 0,
+                                                              _aligned(g, x, w)), x.device, st)
         return dx, dw, db
 
     return _run(x, stream, call)
@@ -191,19 +196,20 @@ def moe_linear_mx(x, x_scales, w, w_scales, offs=None, *, bias=None, activation:
         _tensor(t, torch.uint8, len(shape), x.device, name)
         if t.shape != shape or width % 32:
             raise TypeError(f"{name} must have shape {shape} for blocks of 32 of {width}, got {tuple(t.shape)}")
-    ep = _Epilogue(rows, E, wide, x.device, bias, activation, gated, residual)
+    n, epilogue = _epilogue(rows, E, wide, x.device, bias, activation, gated, residual)
 
-    def call(st):
-        y = torch.empty((rows, ep.n), dtype=torch.bfloat16, device=x.device)
-        pre = torch.empty((rows, wide), dtype=torch.bfloat16, device=x.device) if save_pre else None
+    def need():
         words = all(t.data_ptr() % 4 == 0 and t.stride(-1) == 1 and not any(s % 4 for s in t.stride()[:-1])
                     for t in (x_scales, w_scales))
-        need = mxq_moe_linear_mx_workspace_bytes(rows, width, E, wide, int(words))
-        ws = _workspace(need, "mxq_moe_linear_mx", x.device)
-        code = mxq_moe_linear_mx(x.data_ptr(), rows, width, *x.stride(), x_scales.data_ptr(), *x_scales.stride(),
-                                 w.data_ptr(), E, wide, *w.stride(), w_scales.data_ptr(), *w_scales.stride(), _ptr(offs),
-                                 *ep.args(y, pre), _ptr(ws), max(need, 0), st)
-        _check(code, "mxq_moe_linear_mx")
+        return mxq_moe_linear_mx_workspace_bytes(rows, width, E, wide, int(words))
+
+    def call(st):
+        y = torch.empty((rows, n), dtype=torch.bfloat16, device=x.device)
+        pre = torch.empty((rows, wide), dtype=torch.bfloat16, device=x.device) if save_pre else None
+        _call(mxq_moe_linear_mx, "mxq_moe_linear_mx",
+              (x.data_ptr(), rows, width, *x.stride(), x_scales.data_ptr(), *x_scales.stride(), w.data_ptr(), E, wide,
+               *w.stride(), w_scales.data_ptr(), *w_scales.stride(), _ptr(offs), *epilogue, y.data_ptr(), n or 1, 1,
+               _ptr(pre), wide or 1, 1), need, x.device, st)
         return (y, pre) if save_pre else y
 
     return _run(x, stream, call)
