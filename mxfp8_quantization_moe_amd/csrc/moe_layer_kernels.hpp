@@ -163,15 +163,19 @@ __device__ __forceinline__ void select_tokens(const LayerArgs &a, int first, int
         select_wave<T, 16, (NT + 1) / 2>(a, first, step, ids, share);
 }
 
-// What the other kernels need to find their slots.  Slots of an expert come in
-// any order: each is a column of its own in the products.
+// What the other kernels need to find their slots.  An expert's slots are in
+// the order of their tokens, a token naming it at most once: the down product
+// takes an expert's first 8 slots otherwise than the rest, so another order would
+// round otherwise.
 template <typename T>
 __global__ __launch_bounds__(kSelectThreads) void layer_select_kernel(LayerArgs a)
 {
-    __shared__ int counts[kLayerExperts], sums[kSelectThreads / 64], ids[kLayerTokens * kLayerSlots];
+    static_assert(kLayerTokens == 64 && kSelectThreads == kLayerExperts, "a bit a token, a thread an expert");
+    __shared__ unsigned long long tokens[kLayerExperts];
+    __shared__ int begin[kLayerExperts], sums[kSelectThreads / 64], ids[kLayerTokens * kLayerSlots];
     __shared__ float share[kLayerTokens * kLayerSlots];
     const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, slots = a.tokens * a.k;
-    counts[tid] = 0;
+    tokens[tid] = 0;
     if (a.tokens > kSelectThreads / 64)
         select_tokens<T, 4>(a, wave, kSelectThreads / 64, ids, share);
     else
@@ -181,12 +185,12 @@ __global__ __launch_bounds__(kSelectThreads) void layer_select_kernel(LayerArgs 
         a.ids[s] = ids[s];
         a.share[s] = share[s];
         if (ids[s] >= 0)
-            atomicAdd(&counts[ids[s]], 1);
+            atomicOr(&tokens[ids[s]], 1ull << s / a.k);
     }
     __syncthreads();
     // expert tid: slots before its own, and its place among the active ones,
     // in the low and the high half of one sum
-    const int own = counts[tid], v = own | (own > 0) << 16, upto = wave_scan(v);
+    const int own = __popcll(tokens[tid]), v = own | (own > 0) << 16, upto = wave_scan(v);
     if (lane == 63)
         sums[wave] = upto;
     __syncthreads();
@@ -204,11 +208,11 @@ __global__ __launch_bounds__(kSelectThreads) void layer_select_kernel(LayerArgs 
         a.begin[total >> 16] = total & 0xffff;
         a.begin[a.most + 1] = total >> 16;
     }
-    counts[tid] = before & 0xffff;
+    begin[tid] = before & 0xffff;
     __syncthreads();
     for (int s = tid; s < slots; s += kSelectThreads)
         if (ids[s] >= 0)
-            a.order[atomicAdd(&counts[ids[s]], 1)] = s;
+            a.order[begin[ids[s]] + __popcll(tokens[ids[s]] & ((1ull << s / a.k) - 1))] = s;
 }
 
 // ---------------------------------------------------------------- up

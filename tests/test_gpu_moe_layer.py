@@ -135,6 +135,18 @@ def test_every_token_to_the_same_experts():
     check(64, 300, 3, 96, 64, "mx", logits=logits)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "mx"])
+def test_equal_calls_give_equal_bits(fmt):
+    """Also of experts with more tokens than one pass of the down product takes."""
+    T, E, k, D, H = 64, 6, 4, 2048, 512
+    x, logits = normal(T, D), normal(T, E, seed=3, dtype=torch.float32)
+    up, down = normal(E, 2 * H, D, seed=1, scale=D ** -0.5), normal(E, D, H, seed=2, scale=H ** -0.5)
+    u, d = (mx(up), mx(down)) if fmt == "mx" else (up, down)
+    want = mxq.moe_layer(x, logits, u, d, k)
+    for _ in range(20):
+        assert torch.equal(mxq.moe_layer(x, logits, u, d, k), want)
+
+
 def test_ties_go_to_the_lower_expert():
     logits = torch.tensor([[0.0, -0.0, 1.0, 1.0, 0.0, -2.0], [5.0] * 6, [-1e30] * 6], device=DEV)
     for k in (1, 3, 4, 6):
