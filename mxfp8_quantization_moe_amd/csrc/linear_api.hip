@@ -59,6 +59,13 @@ struct Room {
     }
 };
 
+// Grid of a copy of `items` per group, 256 a workgroup and no more than cover the
+// chip: 2^28 threads at most, whatever the groups.
+dim3 copy_grid(int64_t items, int64_t count)
+{
+    return dim3((unsigned)std::min((items + 255) / 256, std::max<int64_t>(std::min<int64_t>(8192, (1 << 20) / count), 1)), (unsigned)count);
+}
+
 // the operand in place or a copy in padded rows
 Rows readable(const Rows &r, int64_t count, Room &room, hipStream_t st)
 {
@@ -69,7 +76,7 @@ Rows readable(const Rows &r, int64_t count, Room &room, hipStream_t st)
     to.p = room.take(r.packed_bytes(count));
     const int64_t pieces = r.rows * to.sr / 8;
     if (pieces > 0)
-        linear_pack_kernel<<<dim3((unsigned)std::min<int64_t>((pieces + 255) / 256, 8192), (unsigned)count), dim3(256), 0, st>>>(
+        linear_pack_kernel<<<copy_grid(pieces, count), dim3(256), 0, st>>>(
             reinterpret_cast<const uint16_t *>(r.p), r.se, r.sr, (int)r.rows, (int)r.cols,
             const_cast<uint16_t *>(reinterpret_cast<const uint16_t *>(to.p)), (int)to.sr);
     return to;
@@ -95,7 +102,7 @@ Scales readable(const Scales &s, int64_t count, Room &room, hipStream_t st)
     to.p = reinterpret_cast<uint8_t *>(room.take(s.packed_bytes(count)));
     const int64_t words = s.rows * to.sr / 4;
     if (words > 0)
-        linear_pack_scales_kernel<<<dim3((unsigned)std::min<int64_t>((words + 255) / 256, 8192), (unsigned)count), dim3(256), 0, st>>>(
+        linear_pack_scales_kernel<<<copy_grid(words, count), dim3(256), 0, st>>>(
             s.p, s.se, s.sr, s.sb, (int)s.rows, (int)s.blocks, const_cast<uint8_t *>(to.p), (int)to.sr);
     return to;
 }
@@ -147,7 +154,8 @@ Choice choose(LinearMode mode, bool mx, int64_t rows, int32_t experts, int64_t w
         const int64_t r = mode == kGradW ? experts * ((wide + tm - 1) / tm) : usual_row_tiles(rows, experts, tm);
         return r * ((cols + tn - 1) / tn);
     };
-    if (mode == kForward && rows <= 16)
+    // 16 columns of an expert a workgroup: past 2^32 threads the tiles take it
+    if (mode == kForward && rows <= 16 && (wide + 15) / 16 * (experts + 1) < ((int64_t)1 << 32) / (kFewWaves * 64))
         return {kFew, 1};
     if (tiles(256, 256) >= 72 && (mode == kGradW || rows >= 64 * (int64_t)experts))
         return {kLarge, 1};

@@ -108,3 +108,11 @@ def test_workspace_queries(lib):
     assert lin(1000, 64, 4, 33, 1) == 0 and lin(1000, 64, 4, 33, 0) > 0 and lin(1000, 63, 4, 33, 1) > 0
     assert mx(1000, 48, 4, 33, 1) == -1 and mx(1000, 128, 4, 33, 1) == 0 and mx(1000, 128, 4, 33, 0) > 0
     assert back(10, 8, 2, 7, 0, 1, 0, 1) == -1 and back(10, 8, 2, 8, 4, 0, 0, 1) == -1
+
+
+def test_few_rows_over_more_columns_than_one_grid_takes(lib):
+    """Such a call goes to the tiles, which copy operands of any alignment."""
+    assert lib.mxq_moe_linear_workspace_bytes(16, 64, 4096, 2048, 0) == 0
+    assert lib.mxq_moe_linear_workspace_bytes(16, 64, 4096, 65536, 0) >= 4096 * 65536 * 64 * 2
+    assert lib.mxq_moe_linear_mx_workspace_bytes(16, 64, 4096, 2048, 0) == 0
+    assert lib.mxq_moe_linear_mx_workspace_bytes(16, 64, 4096, 65536, 0) >= 4096 * 65536 * 4
