@@ -155,7 +155,7 @@ Choice choose(LinearMode mode, bool mx, int64_t rows, int32_t experts, int64_t w
         return r * ((cols + tn - 1) / tn);
     };
     // 16 columns of an expert a workgroup: past 2^32 threads the tiles take it
-    if (mode == kForward && rows <= 16 && (wide + 15) / 16 * (experts + 1) < ((int64_t)1 << 32) / (kFewWaves * 64))
+    if (mode == kForward && rows <= kFewRows && (wide + 15) / 16 * (experts + 1) < ((int64_t)1 << 32) / (kFewWaves * 64))
         return {kFew, 1};
     if (tiles(256, 256) >= 72 && (mode == kGradW || rows >= 64 * (int64_t)experts))
         return {kLarge, 1};

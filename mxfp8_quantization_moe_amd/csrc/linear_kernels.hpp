@@ -1050,62 +1050,55 @@ __global__ __launch_bounds__(LinearLarge::THREADS, 2) void linear_large_kernel(L
 
 // ---------------------------------------------------------------- few rows
 
-// Groups of few rows: bound by the weights, which go straight from memory into
+// Up to 16 rows in all: bound by the weights, which go straight from memory into
 // registers, as many loads on their way as there is room for.  A workgroup has
-// 16 rows of W (gated: 16 of the gate and of the value) of one expert and up to
-// 16 FT of the group's rows at a time; its eight waves take the parts of the
-// sum and meet in LDS.
-constexpr int kFewWaves = 8;
+// 16 rows of W (gated: 16 of the gate and of the value) of one expert against
+// the group's rows, all of which one matrix instruction takes; its eight waves
+// take the parts of the sum and meet in LDS.  One row x 4096 x 4096 (34 MB of
+// weights) 11 us a call, 16 rows x 5120 x 8192 (84 MB) 30.
+constexpr int kFewWaves = 8, kFewRows = 16;
 
-template <int NF, int FT, int U>
-__device__ __forceinline__ void few_range(const LinearArgs &a, const char *const (&w)[NF], const char *const (&x)[FT],
-                                          const bool (&there)[FT], int k0, int k1, float4v (&acc)[NF][FT])
+template <int NF, int U>
+__device__ __forceinline__ void few_range(const LinearArgs &a, const char *const (&w)[NF], const char *x, bool there,
+                                          int k0, int k1, float4v (&acc)[NF])
 {
     int k = k0;
     for (; k + U * 32 <= k1; k += U * 32) {
         WeightStep<false> s[NF][U];
-        bf16x8 t[FT][U];
+        bf16x8 t[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int i = 0; i < NF; ++i)
                 s[i][u].load(w[i], nullptr, k + u * 32);
-#pragma unroll
-            for (int f = 0; f < FT; ++f)
-                t[f][u] = there[f] ? token_piece<false>(reinterpret_cast<const uint16_t *>(x[f]), k + u * 32, 0) : zero_piece();
+            t[u] = there ? token_piece<false>(reinterpret_cast<const uint16_t *>(x), k + u * 32, 0) : zero_piece();
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < NF; ++i)
-#pragma unroll
-                for (int f = 0; f < FT; ++f)
-                    acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[i][u].piece(0), t[f][u], acc[i][f], 0, 0, 0);
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[i][u].piece(0), t[u], acc[i], 0, 0, 0);
     }
     for (; k < k1; k += 32) {
         WeightStep<false> s[NF];
 #pragma unroll
         for (int i = 0; i < NF; ++i)
             s[i].load_tail(w[i], nullptr, k, a.width);
+        const bf16x8 t = there ? token_piece_tail<false>(reinterpret_cast<const uint16_t *>(x), k, 0, a.width) : zero_piece();
 #pragma unroll
-        for (int f = 0; f < FT; ++f) {
-            const bf16x8 t = there[f] ? token_piece_tail<false>(reinterpret_cast<const uint16_t *>(x[f]), k, 0, a.width) : zero_piece();
-#pragma unroll
-            for (int i = 0; i < NF; ++i)
-                acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[i].piece(0), t, acc[i][f], 0, 0, 0);
-        }
+        for (int i = 0; i < NF; ++i)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[i].piece(0), t, acc[i], 0, 0, 0);
     }
 }
 
-template <int NF, int FT, int U>
+template <int NF, int U>
 __device__ __forceinline__ void few_range_mx(const LinearArgs &a, const char *const (&w)[NF], const uint8_t *const (&ws)[NF],
-                                             const char *const (&x)[FT], const uint8_t *const (&xs)[FT],
-                                             const bool (&there)[FT], int k0, int k1, float4v (&acc)[NF][FT])
+                                             const char *x, const uint8_t *xs, bool there, int k0, int k1, float4v (&acc)[NF])
 {
     auto some = [&](auto steps, int k, int end) {
         constexpr int N = decltype(steps)::value;
-        int8v s[N][NF], t[N][FT];
-        int ss[N][NF], ts[N][FT];
+        int8v s[N][NF], t[N];
+        int ss[N][NF], ts[N];
 #pragma unroll
         for (int u = 0; u < N; ++u) {
 #pragma unroll
@@ -1113,20 +1106,14 @@ __device__ __forceinline__ void few_range_mx(const LinearArgs &a, const char *co
                 s[u][i] = scaled_values(reinterpret_cast<const uint8_t *>(w[i]), k + u * 128, end, true);
                 ss[u][i] = scaled_scale(ws[i], a.sbq, k + u * 128, end, true);
             }
-#pragma unroll
-            for (int f = 0; f < FT; ++f) {
-                t[u][f] = scaled_values(reinterpret_cast<const uint8_t *>(x[f]), k + u * 128, end, there[f]);
-                ts[u][f] = scaled_scale(xs[f], a.sbp, k + u * 128, end, there[f]);
-            }
+            t[u] = scaled_values(reinterpret_cast<const uint8_t *>(x), k + u * 128, end, there);
+            ts[u] = scaled_scale(xs, a.sbp, k + u * 128, end, there);
         }
 #pragma unroll
         for (int u = 0; u < N; ++u)
 #pragma unroll
             for (int i = 0; i < NF; ++i)
-#pragma unroll
-                for (int f = 0; f < FT; ++f)
-                    acc[i][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(s[u][i], t[u][f], acc[i][f], 0, 0, 0,
-                                                                                ss[u][i], 0, ts[u][f]);
+                acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(s[u][i], t[u], acc[i], 0, 0, 0, ss[u][i], 0, ts[u]);
     };
     int k = k0;
     for (; k + U * 128 <= k1; k += U * 128)
@@ -1138,8 +1125,8 @@ __device__ __forceinline__ void few_range_mx(const LinearArgs &a, const char *co
 template <bool GATED, bool MX>
 __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(LinearArgs a)
 {
-    constexpr int FT = 1, NF = GATED ? 2 : 1, STEP = MX ? 128 : 32, U = MX ? 4 : 8;
-    __shared__ float4v sums[kFewWaves][NF][FT][64];
+    constexpr int NF = GATED ? 2 : 1, STEP = MX ? 128 : 32, U = MX ? 4 : 8;
+    __shared__ float4v sums[kFewWaves][NF][64];
     const int e = blockIdx.y, c0 = blockIdx.x * 16, wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, fr = lane & 15;
     int start, len;
     group_rows(a.offs, a.experts, a.rows, e, start, len);
@@ -1148,16 +1135,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(LinearArgs a
     if (len == 0)
         return;
     if (e >= a.experts) {
-        for (int64_t at = threadIdx.x; at < (int64_t)len * 16; at += kFewWaves * 64) {
-            const int64_t r = start + at / 16;
-            const int c = c0 + (int)(at % 16);
-            if (c >= a.n)
-                continue;
-            a.out[r * a.so + c] = 0;
-            if (a.pre)
-                a.pre[r * a.spre + c] = 0;
-            if (a.pre && GATED)
-                a.pre[r * a.spre + a.n + c] = 0;
+        clear_tile<kFewRows, 16, kFewWaves * 64>(a.out, a.so, start, len, c0, a.n);
+        if (a.pre) {
+            clear_tile<kFewRows, 16, kFewWaves * 64>(a.pre, a.spre, start, len, c0, a.n);
+            if (GATED)
+                clear_tile<kFewRows, 16, kFewWaves * 64>(a.pre + a.n, a.spre, start, len, c0, a.n);
         }
         return;
     }
@@ -1172,69 +1154,49 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(LinearArgs a
     }
     const int steps = (a.width + STEP - 1) / STEP;
     const int k0 = steps * wave / kFewWaves * STEP, k1 = min(steps * (wave + 1) / kFewWaves * STEP, a.width);
-    for (int first = 0; first < len; first += 16 * FT) {
-        const char *x[FT];
-        const uint8_t *xs[FT];
-        bool there[FT];
+    const bool there = fr < len;
+    const int64_t own = start + (there ? fr : 0);
+    float4v acc[NF];
 #pragma unroll
-        for (int f = 0; f < FT; ++f) {
-            there[f] = first + f * 16 + fr < len;
-            const int64_t r = start + (there[f] ? first + f * 16 + fr : 0);
-            x[f] = a.p + r * a.ldp;
-            xs[f] = MX ? a.sp + r * a.ldsp : nullptr;
+    for (int i = 0; i < NF; ++i)
+        acc[i] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (MX)
+        few_range_mx<NF, U>(a, w, ws, a.p + own * a.ldp, a.sp + own * a.ldsp, there, k0, k1, acc);
+    else
+        few_range<NF, U>(a, w, a.p + own * a.ldp, there, k0, k1, acc);
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+        sums[wave][i][lane] = acc[i];
+    __syncthreads();
+    // a lane of the first wave has four columns of a row
+    if (wave > 0 || !there)
+        return;
+    float4v z[NF];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+        z[i] = sums[0][i][lane];
+#pragma unroll
+        for (int v = 1; v < kFewWaves; ++v)
+            z[i] += sums[v][i][lane];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = c0 + 4 * (lane >> 4) + k;
+        if (c >= a.n)
+            continue;
+        float v = z[0][k] + (a.bias ? bias_at(a.bias, a.bias_f32, e * a.sb + c) : 0.0f);
+        if (a.pre)
+            a.pre[own * a.spre + c] = Piece<uint16_t>::from_f32(v);
+        v = act_value(a.act, v);
+        if constexpr (GATED) {
+            const float g = z[1][k] + (a.bias ? bias_at(a.bias, a.bias_f32, e * a.sb + a.n + c) : 0.0f);
+            if (a.pre)
+                a.pre[own * a.spre + a.n + c] = Piece<uint16_t>::from_f32(g);
+            v *= g;
         }
-        float4v acc[NF][FT];
-#pragma unroll
-        for (int i = 0; i < NF; ++i)
-#pragma unroll
-            for (int f = 0; f < FT; ++f)
-                acc[i][f] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (MX)
-            few_range_mx<NF, FT, U>(a, w, ws, x, xs, there, k0, k1, acc);
-        else
-            few_range<NF, FT, U>(a, w, x, there, k0, k1, acc);
-        if (first)
-            __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NF; ++i)
-#pragma unroll
-            for (int f = 0; f < FT; ++f)
-                sums[wave][i][f][lane] = acc[i][f];
-        __syncthreads();
-        // a lane has four columns of a row
-        for (int at = threadIdx.x; at < FT * 64; at += kFewWaves * 64) {
-            const int f = at / 64, l = at & 63, t = first + f * 16 + (l & 15);
-            if (t >= len)
-                continue;
-            float4v z[NF];
-#pragma unroll
-            for (int i = 0; i < NF; ++i) {
-                z[i] = sums[0][i][f][l];
-#pragma unroll
-                for (int v = 1; v < kFewWaves; ++v)
-                    z[i] += sums[v][i][f][l];
-            }
-            const int64_t r = start + t;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int c = c0 + 4 * (l >> 4) + k;
-                if (c >= a.n)
-                    continue;
-                float v = z[0][k] + (a.bias ? bias_at(a.bias, a.bias_f32, e * a.sb + c) : 0.0f);
-                if (a.pre)
-                    a.pre[r * a.spre + c] = Piece<uint16_t>::from_f32(v);
-                v = act_value(a.act, v);
-                if constexpr (GATED) {
-                    const float g = z[1][k] + (a.bias ? bias_at(a.bias, a.bias_f32, e * a.sb + a.n + c) : 0.0f);
-                    if (a.pre)
-                        a.pre[r * a.spre + a.n + c] = Piece<uint16_t>::from_f32(g);
-                    v *= g;
-                }
-                if (a.resid)
-                    v += Piece<uint16_t>::to_f32(a.resid[r * a.sr + c]);
-                a.out[r * a.so + c] = Piece<uint16_t>::from_f32(v);
-            }
-        }
+        if (a.resid)
+            v += Piece<uint16_t>::to_f32(a.resid[own * a.sr + c]);
+        a.out[own * a.so + c] = Piece<uint16_t>::from_f32(v);
     }
 }
 
