@@ -2,14 +2,13 @@
 operators end to end:
 
     router -> token groups -> dispatch -> MXFP8 operands -> expert products
-    -> combine (+ residual) -> loss, balance and z losses
-    -> gradients back through combine, dispatch and router
+    with the activation -> combine (+ residual) -> loss, balance and z losses
+    -> gradients back through combine, products, dispatch and router
     -> Muon update of the 3-D expert weights, quantized again next step
 
-The group ends never leave the device.  The products themselves are plain
-torch on the dequantized operands (the library has no grouped GEMM), each
-expert over all rows and kept where the row is its own; gradients pass the
-quantizers straight through.
+The group ends never leave the device.  The products run on MXFP8 operands,
+their gradients on the bf16 ones: gradients pass the quantizers straight
+through.  ``MoeLayer.decode`` runs the trained layer for a few tokens.
 
     python examples/moe_train_step.py [--steps 60]
 """
@@ -68,42 +67,26 @@ class Combine(torch.autograd.Function):
         return grad_yg, grad_weights, grad_y, None
 
 
-class QuantizeRows(torch.autograd.Function):
-    """bf16 rows through MXFP8 (1 x 32 blocks) and back; straight-through gradient."""
+class ExpertProducts(torch.autograd.Function):
+    """Row r of x times its expert's (N, K) weights, transposed, on MXFP8
+    operands with 1 x 32 blocks along K; then the activation."""
 
     @staticmethod
-    def forward(ctx, x):
+    def forward(ctx, x, w, offs, activation):
         q, scales = mxq.quantize_mx_rowwise(x)
-        factor = torch.exp2(scales.float() - 127.0).repeat_interleave(32, 1)
-        return (q.float() * factor).to(x.dtype)
+        wq, wscales = mxq.quantize_mx_rowwise(w.view(-1, w.shape[2]))
+        y, pre = mxq.moe_linear_mx(q, scales, wq.view(w.shape), wscales.view(*w.shape[:2], -1), offs,
+                                   activation=activation, save_pre=True)
+        ctx.activation = activation
+        ctx.save_for_backward(x, w, offs, pre)
+        return y
 
     @staticmethod
-    def backward(ctx, grad):
-        return grad
-
-
-class QuantizeWeights(torch.autograd.Function):
-    """Expert weights (E, N, K) through MXFP8 (32 x 1 blocks along N)."""
-
-    @staticmethod
-    def forward(ctx, w):
-        q, scales = mxq.quantize_mx_3d_colwise(w)
-        factor = torch.exp2(scales.float() - 127.0).repeat_interleave(32, 1)
-        return (q.float() * factor).to(w.dtype)
-
-    @staticmethod
-    def backward(ctx, grad):
-        return grad
-
-
-def expert_products(xg, w, offs):
-    """Row r of xg times its expert's (N, K) weights, transposed: (rows, N)."""
-    rows = torch.arange(xg.shape[0], device=xg.device)
-    expert = torch.searchsorted(offs, rows, right=True)
-    y = torch.zeros(xg.shape[0], w.shape[1], dtype=xg.dtype, device=xg.device)
-    for e in range(w.shape[0]):
-        y = torch.where((expert == e)[:, None], xg @ w[e].t().contiguous(), y)
-    return y
+    def backward(ctx, grad_y):
+        x, w, offs, pre = ctx.saved_tensors
+        grad_x, grad_w, _ = mxq.moe_linear_backward(grad_y, x, w, offs, pre=pre, activation=ctx.activation,
+                                                    need_x=ctx.needs_input_grad[0], need_w=ctx.needs_input_grad[1])
+        return grad_x, grad_w, None, None
 
 
 class MoeLayer:
@@ -121,10 +104,15 @@ class MoeLayer:
         box = []
         weights, losses = Route.apply(x.float() @ self.router.t(), self.top_k, self.align, box)
         route = box[0]
-        xg = QuantizeRows.apply(Dispatch.apply(x, route))
-        h = torch.relu(expert_products(xg, QuantizeWeights.apply(self.up), route.offs))
-        yg = expert_products(QuantizeRows.apply(h), QuantizeWeights.apply(self.down), route.offs)
+        h = ExpertProducts.apply(Dispatch.apply(x, route), self.up, route.offs, "relu")
+        yg = ExpertProducts.apply(h, self.down, route.offs, "none")
         return Combine.apply(yg, weights, x, route), losses, route
+
+    def decode(self, x):
+        """The layer for up to 64 tokens, the weights as they are."""
+        with torch.no_grad():
+            return mxq.moe_layer(x, x.float() @ self.router.t(), self.up, self.down, self.top_k, activation="relu",
+                                 gated=False, residual=x)
 
     def update(self, lr, router_lr):
         with torch.no_grad():
@@ -152,8 +140,11 @@ def train(steps=60, tokens=2048, width=256, hidden=512, experts=8, top_k=2, verb
         (fit + 1e-2 * losses[0] + 1e-3 * losses[1]).backward()
         layer.update(lr=2e-2 * (1 - step / steps), router_lr=0.1)
         history.append(torch.stack([fit.detach(), losses[0].detach(), route.counts.max().float()]))
+    few = x[:16].to(torch.bfloat16)
+    off = torch.linalg.vector_norm(layer.decode(few).float() - layer(few)[0].float()).item()
     history = torch.stack(history).tolist()
     if verbose:
+        print(f"16 tokens decoded with bf16 weights, {off:.3g} (2-norm) from the MXFP8 products")
         for step in sorted({0, steps // 4, steps // 2, steps - 1}):
             fit, balance, most = history[step]
             print(f"step {step:4d}  fit {fit:.4f}  balance {balance:.4f}  fullest expert {most:.0f} of "

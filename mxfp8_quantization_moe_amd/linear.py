@@ -12,9 +12,9 @@ from __future__ import annotations
 
 from . import MXQError, _check, _torch
 from ._capi import (MXQ_ACT_GELU, MXQ_ACT_NONE, MXQ_ACT_RELU, MXQ_ACT_SILU, MXQ_BF16, MXQ_ERR_INVALID_ARG,
-                    MXQ_ERR_WORKSPACE, MXQ_F32,
-                    mxq_moe_layer, mxq_moe_layer_workspace_bytes, mxq_moe_linear, mxq_moe_linear_backward, mxq_moe_linear_backward_workspace_bytes,
-                    mxq_moe_linear_mx, mxq_moe_linear_mx_workspace_bytes, mxq_moe_linear_workspace_bytes)
+                    MXQ_ERR_WORKSPACE, MXQ_F32, mxq_moe_layer, mxq_moe_layer_workspace_bytes, mxq_moe_linear,
+                    mxq_moe_linear_backward, mxq_moe_linear_backward_workspace_bytes, mxq_moe_linear_mx,
+                    mxq_moe_linear_mx_workspace_bytes, mxq_moe_linear_workspace_bytes)
 from .moe import _plain, _run, _unit
 
 ACTIVATIONS = {"none": MXQ_ACT_NONE, "relu": MXQ_ACT_RELU, "gelu": MXQ_ACT_GELU, "silu": MXQ_ACT_SILU}
