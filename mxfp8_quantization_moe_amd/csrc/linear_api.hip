@@ -183,7 +183,7 @@ int64_t grid_of(int64_t tiles, int64_t threads)
     return g * threads < ((int64_t)1 << 32) && g <= INT32_MAX ? g : 0;
 }
 
-template <int MODE, typename TILE, bool GATED, bool MX, bool SPLIT>
+template <int MODE, typename TILE, bool GATED, int F, bool SPLIT>
 mxq_status launch_tile(const LinearArgs &a, hipStream_t st)
 {
     const int64_t tj = GATED ? TILE::TN / 2 : TILE::TN, tn = (a.n + tj - 1) / tj;
@@ -192,7 +192,7 @@ mxq_status launch_tile(const LinearArgs &a, hipStream_t st)
     const int64_t grid = grid_of(tm * tn * (SPLIT ? a.splits : 1), TILE::THREADS);
     if (grid == 0)
         return MXQ_ERR_UNSUPPORTED;
-    linear_kernel<MODE, TILE, GATED, MX, SPLIT><<<dim3((unsigned)grid), dim3(TILE::THREADS), 0, st>>>(a);
+    linear_kernel<MODE, TILE, GATED, F, SPLIT><<<dim3((unsigned)grid), dim3(TILE::THREADS), 0, st>>>(a);
     return launch_status();
 }
 
@@ -205,42 +205,45 @@ mxq_status launch_few(const LinearArgs &a, hipStream_t st)
 }
 
 // `room`: where parts may go
-template <int MODE, bool GATED, bool MX>
+template <int MODE, bool GATED, int F>
 mxq_status launch(LinearArgs a, const Choice &c, Room &room, hipStream_t st)
 {
     if (a.n == 0 || (MODE == kGradW ? a.wide : a.rows) == 0)
         return MXQ_OK;
-    if (c.kernel == kLarge) {
-        const int64_t tn = (a.n + 127) / 128, tm = MODE == kGradW ? a.experts * ((a.wide + 255) / 256) : row_tiles(a.rows, a.experts, a.offs != nullptr, 256);
-        if (tm * tn > (1 << 30))
-            return MXQ_ERR_UNSUPPORTED;
-        linear_large_kernel<MODE, GATED, MX><<<dim3((unsigned)kCUs), dim3(LinearLarge::THREADS), 0, st>>>(a);
-        return launch_status();
+    if constexpr (F != kMxBytes) {
+        if (c.kernel == kLarge) {
+            const int64_t tn = (a.n + 127) / 128;
+            const int64_t tm = MODE == kGradW ? a.experts * ((a.wide + 255) / 256) : row_tiles(a.rows, a.experts, a.offs != nullptr, 256);
+            if (tm * tn > (1 << 30))
+                return MXQ_ERR_UNSUPPORTED;
+            linear_large_kernel<MODE, GATED, F><<<dim3((unsigned)kCUs), dim3(LinearLarge::THREADS), 0, st>>>(a);
+            return launch_status();
+        }
     }
     if constexpr (MODE == kForward)
         if (c.kernel == kFew)
-            return launch_few<GATED, MX>(a, st);
-    if constexpr (!MX)
+            return launch_few<GATED, F != kBf16>(a, st);
+    if constexpr (F == kBf16)
         if (c.kernel == kMedium)
-            return launch_tile<MODE, TileMedium, GATED, MX, false>(a, st);
+            return launch_tile<MODE, TileMedium, GATED, F, false>(a, st);
     if (c.splits == 1)
-        return launch_tile<MODE, TileSmall, GATED, MX, false>(a, st);
+        return launch_tile<MODE, TileSmall, GATED, F, false>(a, st);
     const int64_t rows = MODE == kGradW ? (int64_t)a.experts * a.wide : a.rows;
     a.splits = c.splits;
     a.ldparts = round_up(MODE == kForward ? a.wide : a.width, 4);
     a.part_size = rows * a.ldparts;
     a.parts = reinterpret_cast<float *>(room.take(parts_bytes((LinearMode)MODE, c.splits, a.rows, a.experts, a.width, a.wide)));
-    const mxq_status s = launch_tile<MODE, TileSmall, GATED, MX, true>(a, st);
+    const mxq_status s = launch_tile<MODE, TileSmall, GATED, F, true>(a, st);
     if (s != MXQ_OK)
         return s;
     linear_join_kernel<MODE, GATED><<<dim3((unsigned)std::min<int64_t>(rows, 1 << 20), (unsigned)((a.n + 1023) / 1024)), dim3(256), 0, st>>>(a);
     return launch_status();
 }
 
-template <bool MX>
+template <int F>
 mxq_status launch_forward(const LinearArgs &a, int gated, const Choice &c, Room &room, hipStream_t st)
 {
-    return gated ? launch<kForward, true, MX>(a, c, room, st) : launch<kForward, false, MX>(a, c, room, st);
+    return gated ? launch<kForward, true, F>(a, c, room, st) : launch<kForward, false, F>(a, c, room, st);
 }
 
 // a 2-D operand or result of bf16: rows of unit stride
@@ -325,7 +328,7 @@ mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_
     a.so = sy_r;
     a.pre = pre;
     a.spre = sp_r;
-    return launch_forward<false>(a, gated, choice, room, st);
+    return launch_forward<kBf16>(a, gated, choice, room, st);
 }
 
 int64_t mxq_moe_linear_mx_workspace_bytes(int64_t rows, int64_t width, int32_t num_experts, int64_t wide, int32_t aligned)
@@ -334,7 +337,7 @@ int64_t mxq_moe_linear_mx_workspace_bytes(int64_t rows, int64_t width, int32_t n
         return -1;
     const Choice c = choose(kForward, true, rows, num_experts, width, wide);
     const int64_t parts = parts_bytes(kForward, c.splits, rows, num_experts, width, wide);
-    if (c.kernel == kFew || (aligned && width % 128 == 0))
+    if (c.kernel != kLarge || (aligned && width % 128 == 0))
         return parts;
     return parts + Scales{nullptr, 0, 0, 1, rows, width / 32}.packed_bytes(1) +
            Scales{nullptr, 0, 0, 1, wide, width / 32}.packed_bytes(num_experts);
@@ -368,7 +371,8 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
     const Scales ws = {w_scales, sws_e, sws_n, sws_b, wide, width / 32};
     const Choice choice = choose(kForward, true, rows, num_experts, width, wide);
     const bool few = choice.kernel == kFew;
-    const int64_t need = (few || xs.direct() ? 0 : xs.packed_bytes(1)) + (few || ws.direct() ? 0 : ws.packed_bytes(num_experts)) +
+    const bool words = choice.kernel == kLarge;  // else scales are read from where they are
+    const int64_t need = (words && !xs.direct() ? xs.packed_bytes(1) : 0) + (words && !ws.direct() ? ws.packed_bytes(num_experts) : 0) +
                          parts_bytes(kForward, choice.splits, rows, num_experts, width, wide);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return MXQ_ERR_WORKSPACE;
@@ -376,7 +380,7 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
         return MXQ_ERR_UNSUPPORTED;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     Room room = {reinterpret_cast<char *>(workspace), nullptr};
-    const Scales xo = few ? xs : readable(xs, 1, room, st), wo = few ? ws : readable(ws, num_experts, room, st);
+    const Scales xo = words ? readable(xs, 1, room, st) : xs, wo = words ? readable(ws, num_experts, room, st) : ws;
     LinearArgs a = {};
     a.p = reinterpret_cast<const char *>(x);
     a.ldp = sx_r;
@@ -406,7 +410,8 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
     a.so = sy_r;
     a.pre = pre;
     a.spre = sp_r;
-    return launch_forward<true>(a, gated, choice, room, st);
+    return choice.kernel == kLarge || (xo.direct() && wo.direct()) ? launch_forward<kMxWords>(a, gated, choice, room, st)
+                                                                   : launch_forward<kMxBytes>(a, gated, choice, room, st);
 }
 
 namespace {
@@ -534,7 +539,7 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         b.qe = wo.se * 2;
         b.out = grad_x;
         b.so = sdx_r;
-        status = launch<kGradX, false, false>(b, cx, room, st);
+        status = launch<kGradX, false, kBf16>(b, cx, room, st);
     }
     if (grad_w && status == MXQ_OK && wide > 0 && width > 0) {
         const Rows xo = readable(xr, 1, room, st);
@@ -544,7 +549,7 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         b.out = grad_w;
         b.so = sdw_n;
         b.oe = sdw_e;
-        status = launch<kGradW, false, false>(b, cw, room, st);
+        status = launch<kGradW, false, kBf16>(b, cw, room, st);
     }
     return status;
 }

@@ -38,14 +38,17 @@
 namespace mxq {
 
 enum LinearMode { kForward, kGradX, kGradW };
+// Operands: bf16, or MXFP8 with the scales of a row in whole words, or of any
+// strides.
+enum LinearFormat { kBf16, kMxWords, kMxBytes };
 // Operands and results of a call; leading strides in bytes for what is read
 // into LDS, else in elements.
 struct LinearArgs {
     const char *p, *q;            // see the modes
     int64_t ldp, ldq, qe;         // qe: from expert to expert
-    const uint8_t *sp, *sq;       // e8m0 scales (MXFP8), rows of whole words
+    const uint8_t *sp, *sq;       // e8m0 scales (MXFP8)
     int64_t ldsp, ldsq, sqe;
-    int64_t sbp, sbq;             // from block to block (few rows; else 1)
+    int64_t sbp, sbq;             // from block to block (kMxWords: 1)
     const int32_t *offs;          // NULL: one group of all rows
     int experts, rows;
     int width, wide;              // inner extents: of x, and of z
@@ -286,12 +289,12 @@ struct Panel {
 // lane's four results lie along j.  The scaled product takes both halves of a
 // stage at once (128 values of k): lane 16 b + i holds bytes 16 b and 64 + 16 b
 // of row i and supplies the scale of its 32-value block b.
-template <bool MX, int I0, int N, int FP, int FQ>
+template <int F, int I0, int N, int FP, int FQ>
 __device__ __forceinline__ void multiply_stage(const half8 (&p0)[N], const half8 (&p1)[N], const half8 (&q0)[FQ],
                                                const half8 (&q1)[FQ], const int (&sp)[FP], const int (&sq)[FQ],
                                                float4v (&acc)[FP][FQ])
 {
-    if constexpr (MX) {
+    if constexpr (F != kBf16) {
         // both halves of a fragment
         auto whole = [](const half8 &x, const half8 &y) {
             typedef int int4v __attribute__((ext_vector_type(4)));
@@ -318,17 +321,24 @@ __device__ __forceinline__ void multiply_stage(const half8 (&p0)[N], const half8
 }
 
 // Both operands of a tile and, for MXFP8, the scales of their rows: a word of
-// four blocks per row and stage.
-template <typename TILE, bool PT, bool QT, bool MX>
+// four blocks per row and stage in LDS, or a byte per lane and fragment straight
+// into registers.  Bytes spare the small tiles a pass that lays the scales out in
+// words: 27 rows over 23 experts of 72 x 96 BYTES_SMALL us a call (WORDS_SMALL with it), MORE
+template <typename TILE, bool PT, bool QT, int F>
 struct LinearStages {
     typedef Panel<TILE::TM, TILE::THREADS, PT> PanelP;
     typedef Panel<TILE::TN, TILE::THREADS, QT> PanelQ;
-    static constexpr int LP = PanelP::LOADS, LQ = PanelQ::LOADS, LS = MX ? (TILE::TM + TILE::TN + TILE::THREADS - 1) / TILE::THREADS : 0;
+    static constexpr int LP = PanelP::LOADS, LQ = PanelQ::LOADS, LS = F == kMxWords ? (TILE::TM + TILE::TN + TILE::THREADS - 1) / TILE::THREADS : 0;
     static constexpr int LOADS = LP + LQ + LS;
     static constexpr int BYTES = TILE::STAGE + LS * TILE::THREADS * 4;
     PanelP p;
     PanelQ q;
-    const uint8_t *scales[LS > 0 ? LS : 1];  // this thread's rows
+    const uint8_t *scales[LS > 0 ? LS : 1];  // words: this thread's rows
+    // bytes: the rows of this lane in each fragment, the stride from block to
+    // block, and how many blocks there are
+    const uint8_t *byte_p[F == kMxBytes ? TILE::FP : 1], *byte_q[F == kMxBytes ? TILE::FQ : 1];
+    int64_t stride_p, stride_q;
+    int blocks;
     int stages, live;             // live: chunks of k in the last stage
     uint32_t lds0;
 
@@ -359,10 +369,19 @@ struct LinearStages {
     {
         p.skip(first);
         q.skip(first);
-        if constexpr (MX)
+        if constexpr (F == kMxWords)
 #pragma unroll
             for (int l = 0; l < LS; ++l)
                 scales[l] += first * 4;
+        if constexpr (F == kMxBytes) {
+#pragma unroll
+            for (int i = 0; i < TILE::FP; ++i)
+                byte_p[i] += first * 4 * stride_p;
+#pragma unroll
+            for (int i = 0; i < TILE::FQ; ++i)
+                byte_q[i] += first * 4 * stride_q;
+            blocks -= first * 4;
+        }
         live = last < stages ? 8 : live;
         stages = last - first;
     }
@@ -372,7 +391,7 @@ struct LinearStages {
     template <int N>
     __device__ __forceinline__ void read_scales(int s, int first, int (&v)[N]) const
     {
-        if constexpr (MX) {
+        if constexpr (F == kMxWords) {
             const int fr = threadIdx.x & 15, fk = (threadIdx.x & 63) >> 4;
             const uint32_t a = lds0 + s * BYTES + TILE::STAGE + (uint32_t)(first + fr) * 4;
 #pragma unroll
@@ -380,16 +399,39 @@ struct LinearStages {
                 v[i] = *(__attribute__((address_space(3))) const int *)(uintptr_t)(a + i * 64) >> (8 * fk);
         }
     }
+
+    // bytes: those of stage kt; a block past the last one counts as zero (its
+    // values are, and a scale that is none must not make them NaN)
+    __device__ __forceinline__ void load_scales(int kt, int (&sp)[TILE::FP], int (&sq)[TILE::FQ]) const
+    {
+        if constexpr (F == kMxBytes) {
+            const int own = kt * 4 + ((threadIdx.x & 63) >> 4), b = min(own, blocks - 1);
+#pragma unroll
+            for (int i = 0; i < TILE::FP; ++i)
+                sp[i] = byte_p[i][b * stride_p];
+#pragma unroll
+            for (int i = 0; i < TILE::FQ; ++i)
+                sq[i] = byte_q[i][b * stride_q];
+            if (own >= blocks) {
+#pragma unroll
+                for (int i = 0; i < TILE::FP; ++i)
+                    sp[i] = 0;
+#pragma unroll
+                for (int i = 0; i < TILE::FQ; ++i)
+                    sq[i] = 0;
+            }
+        }
+    }
 };
 
 // Fragments are read one stage ahead of their MFMAs.  At a stage's one barrier
 // every wave has read stage kt and has stage kt + 1; the load of stage kt + NST
 // overwrites stage kt.
-template <typename TILE, bool PT, bool QT, bool MX>
-__device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT, MX> &st, int row0, int col0,
+template <typename TILE, bool PT, bool QT, int F>
+__device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT, F> &st, int row0, int col0,
                                                 float4v (&acc)[TILE::FP][TILE::FQ])
 {
-    typedef LinearStages<TILE, PT, QT, MX> S;
+    typedef LinearStages<TILE, PT, QT, F> S;
     constexpr int NST = TILE::NST, FP = TILE::FP, FQ = TILE::FQ;
     const typename S::PanelP::template Reads<FP> rp(st.lds0, row0);
     const typename S::PanelQ::template Reads<FQ> rq(st.lds0 + TILE::TM * 128, col0);
@@ -407,6 +449,7 @@ __device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT,
         st.read_scales(s, TILE::TM + col0, x.sq);
     };
     const int end = st.stages;
+    st.load_scales(0, f[0].sp, f[0].sq);
     for (int s = 0; s < NST; ++s)
         if (s < end)
             st.load(s, s);
@@ -423,11 +466,13 @@ __device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT,
                 wait_stage<(NST - 2) * S::LOADS>();
             else
                 wait_stage<0>();
+            // loads return in order: before those of a later stage
+            st.load_scales(kt + 1, y.sp, y.sq);
             if (kt + NST < end)
                 st.load(now, kt + NST);
             read(next, y);
         }
-        multiply_stage<MX, 0>(x.p0, x.p1, x.q0, x.q1, x.sp, x.sq, acc);
+        multiply_stage<F, 0>(x.p0, x.p1, x.q0, x.q1, x.sp, x.sq, acc);
         now = next;
         ++kt;
     };
@@ -459,9 +504,9 @@ __device__ __forceinline__ void linear_pipeline(const LinearStages<TILE, PT, QT,
 // for ra(t + 1) have landed when only those issued since are pending, 2 of t + 1
 // and the FIRST of t + 2, at the end of its ma(t) those for rb(t) when again as
 // many are.
-template <typename TILE, bool PT, bool QT, bool MX>
+template <typename TILE, bool PT, bool QT, int F>
 struct LinearAlternating {
-    typedef LinearStages<TILE, PT, QT, MX> S;
+    typedef LinearStages<TILE, PT, QT, F> S;
     static_assert(TILE::NST == 2 && TILE::WM == 2 && TILE::WN == 4 && TILE::TM == 256 && S::LP == 4,
                   "loads 0-3 are the quarters, the rest Q and the scales");
     static constexpr int FP = TILE::FP, FQ = TILE::FQ, H = FP / 2;
@@ -511,7 +556,7 @@ struct LinearAlternating {
     __device__ __forceinline__ void products(float4v (&acc)[FP][FQ])
     {
         __builtin_amdgcn_s_setprio(1);
-        multiply_stage<MX, I0>(p0, p1, q0, q1, sp, sq, acc);
+        multiply_stage<F, I0>(p0, p1, q0, q1, sp, sq, acc);
         __builtin_amdgcn_s_setprio(0);
     }
 
@@ -779,17 +824,17 @@ struct LinearGrid {
     }
 };
 
-template <int MODE, typename TILE, bool GATED, bool MX>
+template <int MODE, typename TILE, bool GATED, int F>
 struct LinearTask {
     static constexpr bool PT = MODE == kGradW, QT = MODE != kForward;
-    typedef LinearStages<TILE, PT, QT, MX> S;
+    typedef LinearStages<TILE, PT, QT, F> S;
     static constexpr int TM = TILE::TM, TN = TILE::TN, TJ = GATED ? TN / 2 : TN;
 
     // operands of a tile
     static __device__ __forceinline__ void operands(const LinearArgs &a, const TileAt &x, S &st)
     {
         // bytes of k of one row, in whole chunks: rows whose length is not are padded
-        const int kb = MX ? x.k : 2 * ((x.k + 7) & ~7);
+        const int kb = F != kBf16 ? x.k : 2 * ((x.k + 7) & ~7);
         st.stages = MODE == kGradW ? (x.k + 63) / 64 : (kb + kRowBytes - 1) / kRowBytes;
         st.live = MODE == kGradW ? 8 : ((kb - 1) % kRowBytes + 16) / 16;
         if constexpr (MODE == kGradW) {
@@ -812,13 +857,27 @@ struct LinearTask {
                 };
                 const int last = GATED ? a.wide - 1 - x.c0 : min(n, TN) - 1;
                 st.q.set_rows(q + x.c0 * a.ldq, a.ldq, (uint32_t)(last * a.ldq) + kb, row);
-                if constexpr (MX) {
+                if constexpr (F == kMxWords) {
 #pragma unroll
                     for (int l = 0; l < S::LS; ++l) {
                         const int t = l * TILE::THREADS + threadIdx.x, r = row(min(max(t - TM, 0), TN - 1));
                         st.scales[l] = t < TM ? a.sp + (x.row0 + min(t, rows - 1)) * a.ldsp
                                               : a.sq + x.e * a.sqe + (int64_t)(x.c0 + max(r, 0)) * a.ldsq;
                     }
+                }
+                if constexpr (F == kMxBytes) {
+                    // rows past the last: another one's, whose results are dropped
+                    const int wave = uniform(threadIdx.x >> 6), fr = threadIdx.x & 15;
+#pragma unroll
+                    for (int i = 0; i < TILE::FP; ++i)
+                        st.byte_p[i] = a.sp + (x.row0 + min((wave / TILE::WN * TILE::FP + i) * 16 + fr, rows - 1)) * a.ldsp;
+#pragma unroll
+                    for (int j = 0; j < TILE::FQ; ++j)
+                        st.byte_q[j] = a.sq + x.e * a.sqe +
+                                       (int64_t)(x.c0 + max(row((wave % TILE::WN * TILE::FQ + j) * 16 + fr), 0)) * a.ldsq;
+                    st.stride_p = a.sbp;
+                    st.stride_q = a.sbq;
+                    st.blocks = x.k / 32;
                 }
             }
         }
@@ -851,10 +910,10 @@ struct LinearTask {
 };
 
 // One tile, or with SPLIT a part of its sum, per workgroup.
-template <int MODE, typename TILE, bool GATED, bool MX, bool SPLIT>
+template <int MODE, typename TILE, bool GATED, int F, bool SPLIT>
 __global__ __launch_bounds__(TILE::THREADS, 2) void linear_kernel(LinearArgs a)
 {
-    typedef LinearTask<MODE, TILE, GATED, MX> Task;
+    typedef LinearTask<MODE, TILE, GATED, F> Task;
     __shared__ __attribute__((aligned(16))) char lds[TILE::NST * Task::S::BYTES];
     const LinearGrid<MODE, TILE, GATED> grid(a);
     const int work = SPLIT ? grid.total * a.splits : grid.total;
@@ -880,7 +939,7 @@ __global__ __launch_bounds__(TILE::THREADS, 2) void linear_kernel(LinearArgs a)
     Task::start(acc);
     const int wave = uniform(threadIdx.x >> 6);
     if (st.stages > 0)
-        linear_pipeline<TILE, Task::PT, Task::QT, MX>(st, wave / TILE::WN * TILE::FP * 16, wave % TILE::WN * TILE::FQ * 16, acc);
+        linear_pipeline<TILE, Task::PT, Task::QT, F>(st, wave / TILE::WN * TILE::FP * 16, wave % TILE::WN * TILE::FQ * 16, acc);
     if constexpr (SPLIT) {
         // grad W: experts' results one after the other
         const int64_t row0 = MODE == kGradW ? (int64_t)x.e * a.wide + x.i0 : x.row0;
@@ -967,13 +1026,13 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a)
 // its first loads come before the results of the last are written, so that
 // neither the search nor the first loads' latency is waited for.  A last round
 // of at most half the workgroups is taken as half tiles by all of them.
-template <int MODE, bool GATED, bool MX>
+template <int MODE, bool GATED, int F>
 __global__ __launch_bounds__(LinearLarge::THREADS, 2) void linear_large_kernel(LinearArgs a)
 {
-    typedef LinearTask<MODE, LinearLarge, GATED, MX> Task;
-    typedef LinearTask<MODE, LinearHalf, GATED, MX> Half;
-    typedef LinearAlternating<LinearLarge, Task::PT, Task::QT, MX> Loop;
-    typedef LinearAlternating<LinearHalf, Task::PT, Task::QT, MX> HalfLoop;
+    typedef LinearTask<MODE, LinearLarge, GATED, F> Task;
+    typedef LinearTask<MODE, LinearHalf, GATED, F> Half;
+    typedef LinearAlternating<LinearLarge, Task::PT, Task::QT, F> Loop;
+    typedef LinearAlternating<LinearHalf, Task::PT, Task::QT, F> HalfLoop;
     __shared__ __attribute__((aligned(16))) char lds[2 * Task::S::BYTES];
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
     const LinearGrid<MODE, LinearLarge, GATED> grid(a);

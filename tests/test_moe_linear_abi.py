@@ -77,10 +77,11 @@ def test_mx_refusals(lib):
     for kw in (dict(width=48), dict(x=A + 8), dict(w=A + 8), dict(sxr=72), dict(swn=72), dict(swe=8), dict(xs=0), dict(wsc=0),
                dict(xsr=-1), dict(xsb=-1), dict(wse=-1), dict(wsn=-1), dict(wsb=-1), dict(sxr=-16), dict(sxr=1 << 22)):
         assert call(**kw) == 1, kw
-    need = lib.mxq_moe_linear_mx_workspace_bytes(100, 64, 3, 96, 1)  # rows of two scales: no whole words
-    assert need >= 4 * (100 + 3 * 96)
+    need = lib.mxq_moe_linear_mx_workspace_bytes(4096, 64, 3, 4096, 1)  # rows of two scales: no whole words
+    assert need >= 4 * (4096 + 3 * 4096)
+    large = dict(rows=4096, wide=4096, syr=4096)
     for kw in (dict(bytes=need - 1), dict(bytes=0), dict(ws=0)):
-        assert call(**kw) == 4, kw
+        assert call(**large, **kw) == 4, kw
 
 
 def test_backward_refusals(lib):
@@ -106,7 +107,8 @@ def test_workspace_queries(lib):
     for bad in ((-1, 4, 1, 4), (1, -1, 1, 4), (1, 4, 0, 4), (1, 4, 4097, 4), (1, 4, 1, -1), (1, 65537, 1, 4), (1, 4, 1, 65537)):
         assert lin(*bad, 1) == -1 and mx(*bad, 1) == -1 and back(*bad, 0, 0, 0, 1) == -1, bad
     assert lin(1000, 64, 4, 33, 1) == 0 and lin(1000, 64, 4, 33, 0) > 0 and lin(1000, 63, 4, 33, 1) > 0
-    assert mx(1000, 48, 4, 33, 1) == -1 and mx(1000, 128, 4, 33, 1) == 0 and mx(1000, 128, 4, 33, 0) > 0
+    assert mx(1000, 48, 4, 33, 1) == -1 and mx(4096, 128, 4, 4096, 1) == 0 and mx(4096, 128, 4, 4096, 0) > 0
+    assert mx(1000, 128, 4, 33, 0) == 0  # small tiles read the scales from where they are
     assert back(10, 8, 2, 7, 0, 1, 0, 1) == -1 and back(10, 8, 2, 8, 4, 0, 0, 1) == -1
 
 
@@ -114,5 +116,3 @@ def test_few_rows_over_more_columns_than_one_grid_takes(lib):
     """Such a call goes to the tiles, which copy operands of any alignment."""
     assert lib.mxq_moe_linear_workspace_bytes(16, 64, 4096, 2048, 0) == 0
     assert lib.mxq_moe_linear_workspace_bytes(16, 64, 4096, 65536, 0) >= 4096 * 65536 * 64 * 2
-    assert lib.mxq_moe_linear_mx_workspace_bytes(16, 64, 4096, 2048, 0) == 0
-    assert lib.mxq_moe_linear_mx_workspace_bytes(16, 64, 4096, 65536, 0) >= 4096 * 65536 * 4
