@@ -59,26 +59,36 @@ struct Room {
     }
 };
 
-// Grid of a copy of `items` per group, 256 a workgroup and no more than cover the
-// chip: 2^28 threads at most, whatever the groups.
-dim3 copy_grid(int64_t items, int64_t count)
-{
-    return dim3((unsigned)std::min((items + 255) / 256, std::max<int64_t>(std::min<int64_t>(8192, (1 << 20) / count), 1)), (unsigned)count);
-}
+// The copies that a call needs, launched together.
+struct Copies {
+    LinearCopies list = {};
+    int n = 0, blocks = 0;
+    void launch(hipStream_t st) const
+    {
+        if (blocks > 0)
+            linear_pack_kernel<<<dim3((unsigned)blocks), dim3(256), 0, st>>>(list);
+    }
+};
 
-// the operand in place or a copy in padded rows
-Rows readable(const Rows &r, int64_t count, Room &room, hipStream_t st)
+// the operand in place or a copy in padded rows, which copies.launch() makes
+Rows readable(const Rows &r, int64_t count, Room &room, Copies &copies)
 {
     if (r.direct())
         return r;
     Rows to = {nullptr, 0, round_up(r.cols, 8), r.rows, r.cols};
     to.se = r.rows * to.sr;
     to.p = room.take(r.packed_bytes(count));
-    const int64_t pieces = r.rows * to.sr / 8;
-    if (pieces > 0)
-        linear_pack_kernel<<<copy_grid(pieces, count), dim3(256), 0, st>>>(
-            reinterpret_cast<const uint16_t *>(r.p), r.se, r.sr, (int)r.rows, (int)r.cols,
-            const_cast<uint16_t *>(reinterpret_cast<const uint16_t *>(to.p)), (int)to.sr);
+    const int64_t all = count * r.rows;
+    if (all * to.sr > 0) {
+        int shift = 0;
+        while (shift < 8 && (8 << shift) < to.sr)
+            ++shift;
+        const int blocks = (int)std::min<int64_t>(((all << shift) + 255) / 256, 8192);
+        copies.list.c[copies.n++] = {reinterpret_cast<const uint16_t *>(r.p), r.se, r.sr, (int)r.rows, (int)r.cols,
+                                     (int)to.sr, shift, (uint32_t)all, blocks,
+                                     const_cast<uint16_t *>(reinterpret_cast<const uint16_t *>(to.p))};
+        copies.blocks += blocks;
+    }
     return to;
 }
 
@@ -92,6 +102,13 @@ struct Scales {
     }
     int64_t packed_bytes(int64_t count) const { return round_up(count * rows * round_up(blocks, 4), 256); }
 };
+
+// Grid of a copy of `items` per group, 256 a workgroup and no more than cover the
+// chip: 2^28 threads at most, whatever the groups.
+dim3 copy_grid(int64_t items, int64_t count)
+{
+    return dim3((unsigned)std::min((items + 255) / 256, std::max<int64_t>(std::min<int64_t>(8192, (1 << 20) / count), 1)), (unsigned)count);
+}
 
 Scales readable(const Scales &s, int64_t count, Room &room, hipStream_t st)
 {
@@ -305,7 +322,9 @@ mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_
         return MXQ_ERR_UNSUPPORTED;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     Room room = {reinterpret_cast<char *>(workspace), nullptr};
-    const Rows xo = few ? xr : readable(xr, 1, room, st), wo = few ? wr : readable(wr, num_experts, room, st);
+    Copies copies;
+    const Rows xo = few ? xr : readable(xr, 1, room, copies), wo = few ? wr : readable(wr, num_experts, room, copies);
+    copies.launch(st);
     LinearArgs a = {};
     a.p = reinterpret_cast<const char *>(xo.p);
     a.ldp = xo.sr * 2;
@@ -497,12 +516,15 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
     a.act = activation;
     float *parts = grad_bias ? reinterpret_cast<float *>(room.take(slices_bytes(rows, num_experts, wide, n))) : nullptr;
     const int slice = slice_rows(rows, num_experts, n);
+    Copies copies;
     Rows z = yr;
     if (saved) {
         z = {room.take(zr.packed_bytes(1)), 0, round_up(wide, 8), rows, wide};
     } else {
-        z = readable(yr, 1, room, st);
+        z = readable(yr, 1, room, copies);
     }
+    const Rows wo = grad_x ? readable(wr, num_experts, room, copies) : wr, xo = grad_w ? readable(xr, 1, room, copies) : xr;
+    copies.launch(st);
     if (rows > 0 && wide > 0 && (saved || parts)) {
         const int64_t slices = row_tiles(rows, num_experts, offs != nullptr, slice);
         const dim3 grid((unsigned)std::min<int64_t>(slices, 1 << 20), (unsigned)((n + 511) / 512));
@@ -532,7 +554,6 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
     a.n = (int)width;
     mxq_status status = launch_status();
     if (grad_x && status == MXQ_OK && rows > 0 && width > 0) {
-        const Rows wo = readable(wr, num_experts, room, st);
         LinearArgs b = a;
         b.q = reinterpret_cast<const char *>(wo.p);
         b.ldq = wo.sr * 2;
@@ -542,7 +563,6 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         status = launch<kGradX, false, kBf16>(b, cx, room, st);
     }
     if (grad_w && status == MXQ_OK && wide > 0 && width > 0) {
-        const Rows xo = readable(xr, 1, room, st);
         LinearArgs b = a;
         b.q = reinterpret_cast<const char *>(xo.p);
         b.ldq = xo.sr * 2;

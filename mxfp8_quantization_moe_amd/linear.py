@@ -10,6 +10,8 @@ allocated on that stream.
 """
 from __future__ import annotations
 
+import functools
+
 from . import MXQError, _check, _torch
 from ._capi import (MXQ_ACT_GELU, MXQ_ACT_NONE, MXQ_ACT_RELU, MXQ_ACT_SILU, MXQ_BF16, MXQ_ERR_INVALID_ARG,
                     MXQ_ERR_WORKSPACE, MXQ_F32, mxq_moe_layer, mxq_moe_layer_workspace_bytes, mxq_moe_linear,
@@ -37,14 +39,6 @@ def _rows(t, shape, device, name: str) -> None:
     _tensor(t, _torch().bfloat16, 2, device, name)
     if t.shape != shape:
         raise TypeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _aligned(*tensors) -> int:
-    """Every operand's rows start on 16 bytes and do not overlap."""
-    for t in tensors:
-        if t.data_ptr() % 16 or any(s % 8 for s in t.stride()[:-1]) or t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]:
-            return 0
-    return 1
 
 
 def _experts(w, x_width: int, offs, device, dtype, name: str):
@@ -90,16 +84,22 @@ def _epilogue(rows, E, wide, device, bias, activation, gated, residual):
     return n, (b, dtype, bs, act, gated, r, rs, rc)
 
 
-def _call(fn, what: str, args, need, device, st) -> None:
-    """The C call without a workspace, which most need not have; if it asks for
-    one, of need() bytes, once more with it."""
-    code = fn(*args, 0, 0, st)
-    if code == MXQ_ERR_WORKSPACE:
-        n = need()
-        if n < 0:
-            raise MXQError(MXQ_ERR_INVALID_ARG, what)
-        ws = _torch().empty(n, dtype=_torch().uint8, device=device)
-        code = fn(*args, ws.data_ptr(), n, st)
+@functools.lru_cache(maxsize=4096)
+def _need(query, *extents) -> int:
+    """Workspace bytes, which the extents alone decide."""
+    return query(*extents)
+
+
+def _call(fn, what: str, args, query, extents, device, st) -> None:
+    """The C call with the workspace that aligned operands need, most none; if
+    it asks for more, with that for any operands."""
+    torch = _torch()
+    for aligned in (1, 0):
+        n = max(_need(query, *extents, aligned), 0)
+        ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None  # alive until all is launched
+        code = fn(*args, _ptr(ws), n, st)
+        if code != MXQ_ERR_WORKSPACE:
+            break
     _check(code, what)
 
 
@@ -131,7 +131,7 @@ def moe_linear(x, w, offs=None, *, bias=None, activation: str = "none", gated: b
         _call(mxq_moe_linear, "mxq_moe_linear",
               (x.data_ptr(), rows, width, *x.stride(), w.data_ptr(), E, wide, *w.stride(), _ptr(offs), *epilogue,
                y.data_ptr(), n or 1, 1, _ptr(pre), wide or 1, 1),
-              lambda: mxq_moe_linear_workspace_bytes(rows, width, E, wide, _aligned(x, w)), x.device, st)
+              mxq_moe_linear_workspace_bytes, (rows, width, E, wide), x.device, st)
         return (y, pre) if save_pre else y
 
     return _run(x, stream, call)
@@ -167,8 +167,7 @@ def moe_linear_backward(grad_y, x, w, offs=None, *, pre=None, activation: str = 
               (g.data_ptr(), *g.stride(), x.data_ptr(), rows, width, *x.stride(), w.data_ptr(), E, wide, *w.stride(),
                _ptr(offs), pre.data_ptr() if saved else 0, pre.stride(0) if saved else 0, pre.stride(1) if saved else 1,
                act, gated, _ptr(dx), width, 1, _ptr(dw), wide * width, width, 1, _ptr(db)),
-              lambda: mxq_moe_linear_backward_workspace_bytes(rows, width, E, wide, act, gated, 1 if bias else 0,
-                                                              _aligned(g, x, w)), x.device, st)
+              mxq_moe_linear_backward_workspace_bytes, (rows, width, E, wide, act, gated, 1 if bias else 0), x.device, st)
         return dx, dw, db
 
     return _run(x, stream, call)
@@ -198,18 +197,13 @@ def moe_linear_mx(x, x_scales, w, w_scales, offs=None, *, bias=None, activation:
             raise TypeError(f"{name} must have shape {shape} for blocks of 32 of {width}, got {tuple(t.shape)}")
     n, epilogue = _epilogue(rows, E, wide, x.device, bias, activation, gated, residual)
 
-    def need():
-        words = all(t.data_ptr() % 4 == 0 and t.stride(-1) == 1 and not any(s % 4 for s in t.stride()[:-1])
-                    for t in (x_scales, w_scales))
-        return mxq_moe_linear_mx_workspace_bytes(rows, width, E, wide, int(words))
-
     def call(st):
         y = torch.empty((rows, n), dtype=torch.bfloat16, device=x.device)
         pre = torch.empty((rows, wide), dtype=torch.bfloat16, device=x.device) if save_pre else None
         _call(mxq_moe_linear_mx, "mxq_moe_linear_mx",
               (x.data_ptr(), rows, width, *x.stride(), x_scales.data_ptr(), *x_scales.stride(), w.data_ptr(), E, wide,
                *w.stride(), w_scales.data_ptr(), *w_scales.stride(), _ptr(offs), *epilogue, y.data_ptr(), n or 1, 1,
-               _ptr(pre), wide or 1, 1), need, x.device, st)
+               _ptr(pre), wide or 1, 1), mxq_moe_linear_mx_workspace_bytes, (rows, width, E, wide), x.device, st)
         return (y, pre) if save_pre else y
 
     return _run(x, stream, call)
