@@ -190,7 +190,7 @@ int64_t parts_bytes(LinearMode mode, int splits, int64_t rows, int32_t experts, 
     if (splits <= 1)
         return 0;
     const int64_t r = mode == kGradW ? experts * wide : rows, c = mode == kForward ? wide : width;
-    return round_up(splits * r * round_up(c, 4) * 4, 256);
+    return round_up(splits * r * round_up(c, 8) * 4, 256);
 }
 
 // a grid that `spread` covers, or 0 if it is past what one launch takes
@@ -247,7 +247,7 @@ mxq_status launch(LinearArgs a, const Choice &c, Room &room, hipStream_t st)
         return launch_tile<MODE, TileSmall, GATED, F, false>(a, st);
     const int64_t rows = MODE == kGradW ? (int64_t)a.experts * a.wide : a.rows;
     a.splits = c.splits;
-    a.ldparts = round_up(MODE == kForward ? a.wide : a.width, 4);
+    a.ldparts = round_up(MODE == kForward ? a.wide : a.width, 8);
     a.part_size = rows * a.ldparts;
     a.parts = reinterpret_cast<float *>(room.take(parts_bytes((LinearMode)MODE, c.splits, a.rows, a.experts, a.width, a.wide)));
     const mxq_status s = launch_tile<MODE, TileSmall, GATED, F, true>(a, st);

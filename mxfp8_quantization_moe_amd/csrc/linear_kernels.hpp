@@ -60,7 +60,7 @@ struct LinearArgs {
     int64_t sr;
     uint16_t *out, *pre;          // pre: z, forward only
     int64_t so, spre, oe;         // oe: grad W, from expert to expert
-    float *parts;                 // sums in parts: (splits, result rows, ldparts)
+    float *parts;                 // sums in parts: (splits, result rows, ldparts), rows of whole 8
     int64_t ldparts, part_size;   // part_size: from part to part
     int splits;
 };
@@ -734,8 +734,8 @@ __device__ __forceinline__ void linear_store(const LinearArgs &a, float4v (&acc)
     }
 }
 
-// The sums of a part as they are, for linear_join_kernel: z's columns in their
-// places, a gate's and its value's apart.
+// The sums of a part as they are, for linear_join_kernel: whole pieces of four
+// columns, a gate's value half a row further.
 template <typename TILE, bool GATED>
 __device__ __forceinline__ void store_part(const LinearArgs &a, float4v (&acc)[TILE::FP][TILE::FQ], int64_t row0, int left,
                                            int c0, int n, float *out)
@@ -752,11 +752,7 @@ __device__ __forceinline__ void store_part(const LinearArgs &a, float4v (&acc)[T
             const int f = wq * FQ + j, c = c0 + (GATED ? f / 2 : f) * 16 + 4 * fk;
             if (r >= left || c >= n)
                 continue;
-            float *to = row + (GATED && (f & 1) ? n : 0) + c;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (c + k < n)
-                    to[k] = acc[i][j][k];
+            *reinterpret_cast<float4v *>(row + (GATED && (f & 1) ? a.ldparts / 2 : 0) + c) = acc[i][j];
         }
     }
 }
@@ -979,23 +975,27 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a)
         }
         if (c >= a.n)
             continue;
-        auto sum = [&](int at, float (&v)[4]) {
+        // four parts' loads before their sums
+        auto sum = [&](int64_t at) {
+            const float *from = a.parts + r * a.ldparts + at;
+            float4v v = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int p = 0; p < a.splits; p += 4) {
+                float4v x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[k] = 0.0f;
-            for (int p = 0; p < a.splits; ++p) {
-                const float *from = a.parts + p * a.part_size + r * a.ldparts + at;
+                for (int u = 0; u < 4; ++u)
+                    x[u] = *reinterpret_cast<const float4v *>(from + min(p + u, a.splits - 1) * a.part_size);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (c + k < a.n)
-                        v[k] += from[k];
+                for (int u = 0; u < 4; ++u)
+                    if (p + u < a.splits)
+                        v += x[u];
             }
+            return v;
         };
-        float v[4] = {}, g[4] = {};
+        float4v v = {0.0f, 0.0f, 0.0f, 0.0f}, g = v;
         if (!none) {
-            sum(c, v);
+            v = sum(c);
             if (GATED)
-                sum(a.n + c, g);
+                g = sum(a.ldparts / 2 + c);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
