@@ -532,15 +532,17 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
  * Strides in elements, the last dim has unit stride (others ->
  * MXQ_ERR_UNSUPPORTED); rows of inputs need only the element's alignment and
  * may repeat.  Operands whose rows do not start on 16 bytes, do not end on
- * them, or overlap are first copied into the workspace.  width, wide <= 65536;
- * a result of more tiles than one grid takes -> MXQ_ERR_UNSUPPORTED (from about
- * 2^30 rows x 64 columns on).
+ * them, or overlap are first copied into the workspace, except in a forward
+ * call of up to 16 rows.  Long sums of small results are taken in parts, which
+ * meet in the workspace.  width, wide <= 65536; a result of more tiles than one
+ * grid takes -> MXQ_ERR_UNSUPPORTED (from about 2^30 rows x 64 columns on), and
+ * so are wide x (row of w) of 2^31 bytes and more.
  */
 typedef enum mxq_activation { MXQ_ACT_NONE = 0, MXQ_ACT_RELU = 1, MXQ_ACT_GELU = 2, MXQ_ACT_SILU = 3 } mxq_activation;
 
-/* Workspace bytes of mxq_moe_linear; `aligned` != 0: x and w start on 16 bytes
- * and their strides are multiples of 8 elements, no rows overlapping.  0 for
- * aligned operands with width % 8 == 0; -1 for invalid arguments. */
+/* Workspace bytes of mxq_moe_linear, by the extents alone; `aligned` != 0: x
+ * and w start on 16 bytes and their strides are multiples of 8 elements, no rows
+ * overlapping.  -1 for invalid arguments. */
 int64_t mxq_moe_linear_workspace_bytes(int64_t rows, int64_t width, int32_t num_experts, int64_t wide, int32_t aligned);
 
 /*
@@ -561,8 +563,8 @@ mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_
                           uint16_t *y, int64_t sy_r, int64_t sy_c, uint16_t *pre, int64_t sp_r, int64_t sp_c,
                           void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Workspace bytes of mxq_moe_linear_backward for the outputs' superset; bias
- * != 0: grad_bias is asked for. */
+/* Workspace bytes of mxq_moe_linear_backward with every gradient; bias != 0:
+ * grad_bias too.  `aligned` as above, of grad_y, x and w. */
 int64_t mxq_moe_linear_backward_workspace_bytes(int64_t rows, int64_t width, int32_t num_experts, int64_t wide,
                                                 int32_t activation, int32_t gated, int32_t bias, int32_t aligned);
 
@@ -600,6 +602,9 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
  * 1.7e-3, hides; at most 2^-9 of the sum of magnitudes).  x and w start
  * on 16 bytes and their strides are multiples of 16 (else
  * MXQ_ERR_INVALID_ARG); scales take any strides.  An e8m0 code of 255 is NaN.
+ * In the workspace's size `aligned` != 0 says that both scales have unit stride
+ * along the blocks, start on 4 bytes and have other strides that are multiples
+ * of 4.
  */
 int64_t mxq_moe_linear_mx_workspace_bytes(int64_t rows, int64_t width, int32_t num_experts, int64_t wide,
                                           int32_t aligned);
