@@ -157,6 +157,32 @@ def test_the_chain_captured_and_replayed():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("width", [1357, 1344])
+def test_copies_and_parts_captured_and_replayed(width):
+    """Workspaces of the graph's own: odd rows are copied, long sums taken in parts."""
+    x, w = normal(92, width), normal(2, 130, width, seed=1, scale=width ** -0.5)
+    offs = torch.tensor([40, 90], dtype=torch.int32, device=DEV)
+
+    def step():
+        y, pre = mxq.moe_linear(x, w, offs, activation="silu", gated=True, save_pre=True)
+        return [y, pre, *mxq.moe_linear_backward(y, x, w, offs, pre=pre, activation="silu", gated=True, bias=True)]
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for seed in range(4):
+        x.normal_(generator=torch.Generator(device="cuda").manual_seed(seed))
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 def test_two_streams_at_once():
     """Calls that overlap share nothing: each has the bits it has alone."""
     T, E, k, D, H = 64, 6, 3, 512, 256
