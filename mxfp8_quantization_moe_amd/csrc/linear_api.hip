@@ -43,10 +43,18 @@ struct Rows {
     int64_t se, sr, rows, cols;
     bool direct() const
     {
-        return cols % 8 == 0 && aligned16(p) && se % 8 == 0 && sr % 8 == 0 && sr < (1 << 21) && (sr >= cols || rows <= 1);
+        return cols % 8 == 0 && aligned16(p) && se % 8 == 0 && sr % 8 == 0 && sr < (1 << 21) && sr >= cols;
     }
     int64_t packed_bytes(int64_t count) const { return round_up(count * rows * round_up(cols, 8) * 2, 256); }
 };
+
+// A single row's stride says nothing (0 of an expanded one), but the descriptor of
+// a turned operand ends with its last row only if the rows that a stage would have
+// after it lie further on.
+Rows rows_of(const void *p, int64_t se, int64_t sr, int64_t rows, int64_t cols)
+{
+    return {p, se, rows > 1 ? sr : round_up(cols, 8), rows, cols};
+}
 
 // What a call's workspace has been used for so far.
 struct Room {
@@ -311,14 +319,14 @@ mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_
         return MXQ_ERR_INVALID_ARG;
     if (rows == 0 || n == 0)
         return MXQ_OK;
-    const Rows xr = {x, 0, sx_r, rows, width}, wr = {w, sw_e, sw_n, wide, width};
+    const Rows xr = rows_of(x, 0, sx_r, rows, width), wr = rows_of(w, sw_e, sw_n, wide, width);
     const Choice choice = choose(kForward, false, rows, num_experts, width, wide);
     const bool few = choice.kernel == kFew;
     const int64_t need = (few || xr.direct() ? 0 : xr.packed_bytes(1)) + (few || wr.direct() ? 0 : wr.packed_bytes(num_experts)) +
                          parts_bytes(kForward, choice.splits, rows, num_experts, width, wide);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return MXQ_ERR_WORKSPACE;
-    if (!few && !reach_ok(wide, wr.direct() ? sw_n * 2 : round_up(width, 8) * 2))
+    if (!few && !reach_ok(wide, wr.direct() ? wr.sr * 2 : round_up(width, 8) * 2))
         return MXQ_ERR_UNSUPPORTED;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     Room room = {reinterpret_cast<char *>(workspace), nullptr};
@@ -487,8 +495,8 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         (grad_x && (!rows_ok(w, num_experts * wide, sw_n, false, width) || sw_e < 0 ||
                     !rows_ok(grad_x, rows, sdx_r, true, width))))
         return MXQ_ERR_INVALID_ARG;
-    const Rows yr = {grad_y, 0, sg_r, rows, n}, zr = {nullptr, 0, 0, rows, wide}, xr = {x, 0, sx_r, rows, width},
-               wr = {w, sw_e, sw_n, wide, width};
+    const Rows yr = rows_of(grad_y, 0, sg_r, rows, n), zr = {nullptr, 0, 0, rows, wide},
+               xr = rows_of(x, 0, sx_r, rows, width), wr = rows_of(w, sw_e, sw_n, wide, width);
     int64_t need = grad_bias ? slices_bytes(rows, num_experts, wide, n) : 0;
     if (saved || !yr.direct())
         need += zr.packed_bytes(1);
