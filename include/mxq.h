@@ -522,7 +522,11 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
  * with act one of mxq_activation (GELU with the normal distribution's cdf, SILU
  * x / (1 + exp(-x))).  Group e is rows [offs[e-1], offs[e]); offs NULL: one
  * group of all rows (num_experts 1).  Rows at or past offs[num_experts-1] come
- * out as zeros (y, pre, grad_x) and take part in nothing.
+ * out as zeros (y, pre, grad_x) and take part in nothing.  Precondition (not
+ * checkable without a sync): offs is non-decreasing; its values are cut to 0 and
+ * rows.  Ends that decrease give unspecified results, without an access outside
+ * the operands and the workspace while the groups together have fewer than 2^31
+ * rows.
  *
  * Numerics: bf16 operands, products summed in fp32 on the matrix cores, bias,
  * activation, gate and residual in fp32, one rounding to bf16.  The order of a

@@ -450,9 +450,15 @@ int slice_rows(int64_t rows, int32_t experts, int64_t n)
     return usual_row_tiles(rows, experts, 64) * ((n + 511) / 512) < 4 * kCUs ? 16 : 64;
 }
 
+// Slices of all groups at most, if their ends do not decrease; the kernels take no more.
+int64_t most_slices(int64_t rows, int32_t experts, int64_t n)
+{
+    return row_tiles(rows, experts, true, slice_rows(rows, experts, n));
+}
+
 int64_t slices_bytes(int64_t rows, int32_t experts, int64_t wide, int64_t n)
 {
-    return round_up(row_tiles(rows, experts, true, slice_rows(rows, experts, n)) * wide * 4, 256);
+    return round_up(most_slices(rows, experts, n) * wide * 4, 256);
 }
 
 }  // namespace
@@ -523,7 +529,7 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
     a.wide = (int)wide;
     a.act = activation;
     float *parts = grad_bias ? reinterpret_cast<float *>(room.take(slices_bytes(rows, num_experts, wide, n))) : nullptr;
-    const int slice = slice_rows(rows, num_experts, n);
+    const int slice = slice_rows(rows, num_experts, n), most = (int)most_slices(rows, num_experts, n);
     Copies copies;
     Rows z = yr;
     if (saved) {
@@ -538,7 +544,7 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         const dim3 grid((unsigned)std::min<int64_t>(slices, 1 << 20), (unsigned)((n + 511) / 512));
         uint16_t *dz = const_cast<uint16_t *>(reinterpret_cast<const uint16_t *>(z.p));
         auto go = [&](auto kernel) {
-            kernel<<<grid, dim3(256), 0, st>>>(a, grad_y, sg_r, pre, sp_r, saved ? dz : nullptr, z.sr, parts);
+            kernel<<<grid, dim3(256), 0, st>>>(a, grad_y, sg_r, pre, sp_r, saved ? dz : nullptr, z.sr, parts, most);
         };
         auto by_act = [&](auto g, auto sl) {
             constexpr bool G = decltype(g)::value;
@@ -556,7 +562,7 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
         gated ? by_slice(std::true_type()) : by_slice(std::false_type());
     }
     if (grad_bias && wide > 0)
-        linear_bias_kernel<<<dim3((unsigned)((wide + 63) / 64), (unsigned)num_experts), dim3(256), 0, st>>>(a, slice, parts, grad_bias);
+        linear_bias_kernel<<<dim3((unsigned)((wide + 63) / 64), (unsigned)num_experts), dim3(256), 0, st>>>(a, slice, parts, most, grad_bias);
     a.p = reinterpret_cast<const char *>(z.p);
     a.ldp = z.sr * 2;
     a.n = (int)width;

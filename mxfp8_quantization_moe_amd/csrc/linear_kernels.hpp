@@ -1335,15 +1335,16 @@ __global__ __launch_bounds__(256) void linear_pack_scales_kernel(const uint8_t *
 //   plain  dz = dy act'(z)        gated  dz = [dy value act'(gate), dy act(gate)]
 // dz is rounded to bf16, the type that the two products take; the sums are of
 // the values before that rounding.  A wave has every fourth row of a slice and
-// 512 columns.  Bound by memory: 8192 x 8192 97 us, 4.2 TB/s; gated 32768 x 2048
+// 512 columns.  `most`: slices that parts has room for, which only group ends that
+// decrease exceed.  Bound by memory: 8192 x 8192 97 us, 4.2 TB/s; gated 32768 x 2048
 // 167, 3.9 TB/s.
 template <bool GATED, bool PRE, int ACT, int SLICE>
 __global__ __launch_bounds__(256) void linear_dact_kernel(LinearArgs a, const uint16_t *__restrict__ dy, int64_t sy,
                                                           const uint16_t *__restrict__ pre, int64_t spre,
-                                                          uint16_t *dz, int64_t sdz, float *parts)
+                                                          uint16_t *dz, int64_t sdz, float *parts, int most)
 {
     __shared__ float sums[4][GATED ? 2 : 1][512];
-    const int slices = count_row_tiles<SLICE>(a);
+    const int slices = min(count_row_tiles<SLICE>(a), most);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = GATED ? a.wide / 2 : a.wide;
     const int c = blockIdx.y * 512 + lane * 8;
     for (int s = blockIdx.x; s < slices; s += gridDim.x) {
@@ -1432,7 +1433,7 @@ __global__ __launch_bounds__(256) void linear_dact_kernel(LinearArgs a, const ui
 // The slices' sums of each group in fp64: a workgroup per group and 64 columns,
 // every fourth slice to a wave, the waves in order.  Latency: 5 us for 4 MB.
 __global__ __launch_bounds__(256) void linear_bias_kernel(LinearArgs a, int slice, const float *__restrict__ parts,
-                                                          float *__restrict__ out)
+                                                          int most, float *__restrict__ out)
 {
     __shared__ double sums[4][64];
     const int e = blockIdx.y, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -1447,6 +1448,8 @@ __global__ __launch_bounds__(256) void linear_bias_kernel(LinearArgs a, int slic
         before += __shfl_xor(before, m, 64);
         own += __shfl_xor(own, m, 64);
     }
+    before = min(max(before, 0), most);
+    own = min(own, most - before);
     const int c = blockIdx.x * 64 + lane;
     double s = 0.0;
     if (c < a.wide) {
