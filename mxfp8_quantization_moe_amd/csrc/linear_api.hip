@@ -282,8 +282,12 @@ bool bias_ok(const void *bias, int32_t dtype, int64_t sb_e)
     return !bias || ((dtype == MXQ_BF16 || dtype == MXQ_F32) && aligned_to(bias, dtype == MXQ_BF16 ? 2 : 4) && sb_e >= 0);
 }
 
-// of a gated product a tile's rows of W lie `wide` / 2 apart
-bool reach_ok(int64_t wide, int64_t row_bytes) { return wide * row_bytes < ((int64_t)1 << 31); }
+// Offsets within a tile fit 31 bits: of a gated product its rows of W lie `wide` / 2
+// apart, of others they are neighbours, which the strides' limits keep in reach.
+bool reach_ok(int32_t gated, int64_t wide, int64_t row_bytes)
+{
+    return !gated || wide * row_bytes < ((int64_t)1 << 31);
+}
 
 }  // namespace
 
@@ -326,7 +330,7 @@ mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_
                          parts_bytes(kForward, choice.splits, rows, num_experts, width, wide);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return MXQ_ERR_WORKSPACE;
-    if (!few && !reach_ok(wide, wr.direct() ? wr.sr * 2 : round_up(width, 8) * 2))
+    if (!few && !reach_ok(gated, wide, wr.direct() ? wr.sr * 2 : round_up(width, 8) * 2))
         return MXQ_ERR_UNSUPPORTED;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     Room room = {reinterpret_cast<char *>(workspace), nullptr};
@@ -403,7 +407,7 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
                          parts_bytes(kForward, choice.splits, rows, num_experts, width, wide);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return MXQ_ERR_WORKSPACE;
-    if (!few && !reach_ok(wide, sw_n))
+    if (!few && !reach_ok(gated, wide, std::max(sw_n, width)))
         return MXQ_ERR_UNSUPPORTED;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     Room room = {reinterpret_cast<char *>(workspace), nullptr};
