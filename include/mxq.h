@@ -531,7 +531,8 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
  * Numerics: bf16 operands, products summed in fp32 on the matrix cores, bias,
  * activation, gate and residual in fp32, one rounding to bf16.  The order of a
  * sum depends on the extents alone, so equal calls give equal bits.  GELU's cdf
- * is within 2e-7 (absolute) of its value.
+ * is within 3e-7 (absolute) of its value and, below zero, within 1e-5 of it
+ * (relative) down to -13.
  *
  * Strides in elements, the last dim has unit stride (others ->
  * MXQ_ERR_UNSUPPORTED); rows of inputs need only the element's alignment and
