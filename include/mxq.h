@@ -606,8 +606,9 @@ mxq_status mxq_moe_linear_backward(const uint16_t *grad_y, int64_t sg_r, int64_t
  * what lies below 2^-13 of the largest is cut, sums of those are fp32 (1e-5 of
  * the result in the 2-norm for ordinary operands, which the rounding to bf16,
  * 1.7e-3, hides; at most 2^-9 of the sum of magnitudes).  x and w start
- * on 16 bytes and their strides are multiples of 16 (else
- * MXQ_ERR_INVALID_ARG); scales take any strides.  An e8m0 code of 255 is NaN.
+ * on 16 bytes and their strides are multiples of 16, those of rows below 2^22
+ * (else MXQ_ERR_INVALID_ARG); scales take any strides.  An e8m0 code of 255 is
+ * NaN.
  * In the workspace's size `aligned` != 0 says that both scales have unit stride
  * along the blocks, start on 4 bytes and have other strides that are multiples
  * of 4.
@@ -632,7 +633,8 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
  *   y_t  = residual_t + sum_j s_tj (D_e h_tj + b_e)
  *
  * Empty slots (a masked token, no expert left) add nothing.  Sums are fp32, h
- * passes between the products with 16 bits or more, y is rounded once to bf16.
+ * passes between the products in two bf16 parts, with 16 bits or more (so an
+ * infinite weight of down comes out as NaN), y is rounded once to bf16.
  * The order of a sum depends on the extents and on the experts that the tokens
  * take, not on the call: equal calls give equal bits.
  *
@@ -648,7 +650,9 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
  *             hidden), bf16, scales NULL.  MXQ_WEIGHTS_MX: e4m3 of the same
  *             shapes, with e8m0 scales of blocks of 32 along their last dim
  *             (width % 32 == 0, hidden % 32 == 0, matrices on 16 bytes, strides
- *             multiples of 16).  Their values enter the products exactly.
+ *             multiples of 16).  Their values enter the products exactly with
+ *             e8m0 codes from 3 to 246, past which they leave bf16's range; 255
+ *             is NaN.
  * bias_up     NULL, or (num_experts, wide), bias_down NULL, or (num_experts,
  *             width), both of bias_dtype, unit stride, sbu_e and sbd_e from
  *             expert to expert.
