@@ -172,6 +172,9 @@ struct Choice {
 //          (54).  With MXFP8 operands even or slower (1024 x 4096 x 4096 42
 //          against 45, 4096 rows over 64 experts of 2048 x 768 37 against 32)
 //   parts  sums of 16 stages and more with small tiles for half the room or less
+// Not measured on both sides: those limits of the parts, a weight gradient of few
+// stages on large tiles, and how the last round of tiles ends, which the rules do
+// not look at.
 Choice choose(LinearMode mode, bool mx, int64_t rows, int32_t experts, int64_t width, int64_t wide)
 {
     const int64_t cols = mode == kForward ? wide : width;

@@ -1029,14 +1029,18 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a)
 
 // A workgroup per CU takes one tile after the other: where the next one is and
 // its first loads come before the results of the last are written, so that
-// neither the search nor the first loads' latency is waited for.  A last round
-// of at most half the workgroups is taken as half tiles by all of them.
+// neither the search nor the first loads' latency is waited for.  In MXFP8 that
+// holds in part: the registers do not suffice, the compiler spills 3 of them, of
+// the gated form 14, and their reloads between two tiles wait for the loads that
+// are on their way.  A last round of at most half the workgroups is taken as half
+// tiles by all of them.
 // Bound by the matrix units and, above 60% of their cycles, by the clock that
 // their power leaves: 8192 x 5120 x 8192 with GELU 543 us, 1.27 PFLOP/s, MFMA busy
 // 70% (gradients 576 and 582, 60-63%: the transposing reads take two per
-// fragment); MXFP8 16384 x 5120 x 8192 751, 1.83 PFLOP/s, 45% (the same LDS
-// bytes for half the cycles).  On 64 x 64 tiles product and gradients took 3662
-// together (1779 here), MXFP8 1592.
+// fragment); MXFP8 16384 x 5120 x 8192 746, 1.84 PFLOP/s, 45%, and no one bound
+// that was found: a stage takes some 2050 cycles of scaled products at the nominal
+// rate, its fragments (196 KB) 1540 of LDS reads.  On 64 x 64 tiles product and
+// gradients took 3662 together (1759 here), MXFP8 1592.
 template <int MODE, bool GATED, int F>
 __global__ __launch_bounds__(LinearLarge::THREADS, 2) void linear_large_kernel(LinearArgs a)
 {
@@ -1121,11 +1125,13 @@ __global__ __launch_bounds__(LinearLarge::THREADS, 2) void linear_large_kernel(L
 // ---------------------------------------------------------------- few rows
 
 // Up to 16 rows in all: bound by the weights, which go straight from memory into
-// registers, as many loads on their way as there is room for.  A workgroup has
-// 16 rows of W (gated: 16 of the gate and of the value) of one expert against
-// the group's rows, all of which one matrix instruction takes; its eight waves
-// take the parts of the sum and meet in LDS.  One row x 4096 x 4096 (34 MB of
-// weights) 11 us a call, 16 rows x 5120 x 8192 (84 MB) 30.
+// registers.  A workgroup has 16 rows of W (gated: 16 of the gate and of the
+// value) of one expert against the group's rows, all of which one matrix
+// instruction takes; its eight waves take the parts of the sum and meet in LDS.
+// A wave asks for 256 of k at a time (MXFP8: 512) and multiplies before it asks
+// again: sums over 4096, 512 a wave, are two latencies one after the other.  The
+// grid has every expert, also those without a row, which end at once.  One row x
+// 4096 x 4096 (34 MB of weights) 11 us a call, 16 rows x 5120 x 8192 (84 MB) 30.
 constexpr int kFewWaves = 8, kFewRows = 16;
 
 template <int NF, int U>

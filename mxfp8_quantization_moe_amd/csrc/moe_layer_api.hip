@@ -24,8 +24,9 @@ bool sizes_ok(int64_t tokens, int64_t width, int64_t hidden, int32_t experts, in
            k <= experts;
 }
 
-// Workgroups per 8 rows of the down product, each with a part of its sums: as
-// many as fill the CUs, with some steps for every wave.
+// Workgroups per 8 rows of the down product, each with a part of its sums: up to
+// 256 in all, with some steps for every wave.  From 129 blocks on, widths above
+// 1024, there is one part; the limits were not measured on both sides.
 int layer_splits(int64_t tokens, int64_t width, int64_t hidden, int32_t experts, int32_t k)
 {
     const int64_t blocks = (width + 7) / 8, steps = std::min<int64_t>(experts, tokens * k) * ((hidden + 63) / 64);
@@ -85,7 +86,8 @@ mxq_status weights_status(const void *w, const uint8_t *scales, int32_t format, 
 }
 
 // 16 rows of U per workgroup where 32 would leave fewer than four workgroups per
-// CU, else 32, for half the searches and half the loads of the tokens' values.
+// CU, else 32, for half the searches and half the loads of the tokens' values: 8
+// tokens in MXFP8 over 256 experts of 2048 x 768 84 us a call (88 with 16).
 template <typename T, bool MX, bool GATED>
 void launch_up(const LayerArgs &a, hipStream_t st)
 {

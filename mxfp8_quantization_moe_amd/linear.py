@@ -112,9 +112,9 @@ def moe_linear(x, w, offs=None, *, bias=None, activation: str = "none", gated: b
     """Rows ``x`` (rows, width) times their expert's weights ``w`` (experts,
     wide, width), both bf16: ``act(x W^T + bias) + residual``, or with
     ``gated`` ``act(first half) * second half + residual`` over wide / 2
-    columns.  ``offs``: int32 group ends on the device (``route.offs``), which must
-    not decrease; without
-    them w is one expert's (2-D, or one of 3-D) and takes every row.
+    columns.  ``offs``: int32 group ends on the device (``route.offs``), which
+    must not decrease; without them w is one expert's (2-D, or one of 3-D) and
+    takes every row.
     ``activation``: "none", "relu", "gelu" or "silu"; ``bias`` (experts, wide),
     bf16 or fp32; ``residual`` (rows, n) bf16.  Returns y (rows, n) bf16, rows
     past the last group zeros; with ``save_pre`` also what the activation took
