@@ -542,7 +542,7 @@ mxq_status mxq_muon_orthogonalize(const void *g, int32_t dtype, int64_t count, i
  * results are taken in parts, which meet in the workspace.  width, wide <=
  * 65536; a result of more tiles than one grid takes -> MXQ_ERR_UNSUPPORTED
  * (from about 2^30 rows x 64 columns on), and so are, gated and with more than
- * 16 rows, wide x (row of w) of 2^31 bytes and more.
+ * 16 rows, weights of an expert that span 2^31 bytes and more.
  */
 typedef enum mxq_activation { MXQ_ACT_NONE = 0, MXQ_ACT_RELU = 1, MXQ_ACT_GELU = 2, MXQ_ACT_SILU = 3 } mxq_activation;
 

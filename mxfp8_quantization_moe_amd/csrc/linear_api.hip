@@ -287,9 +287,9 @@ bool bias_ok(const void *bias, int32_t dtype, int64_t sb_e)
 
 // Offsets within a tile fit 31 bits: of a gated product its rows of W lie `wide` / 2
 // apart, of others they are neighbours, which the strides' limits keep in reach.
-bool reach_ok(int32_t gated, int64_t wide, int64_t row_bytes)
+bool reach_ok(int32_t gated, int64_t wide, int64_t stride_bytes, int64_t row_bytes)
 {
-    return !gated || wide * row_bytes < ((int64_t)1 << 31);
+    return !gated || (wide - 1) * stride_bytes + row_bytes < ((int64_t)1 << 31);
 }
 
 }  // namespace
@@ -333,7 +333,8 @@ mxq_status mxq_moe_linear(const uint16_t *x, int64_t rows, int64_t width, int64_
                          parts_bytes(kForward, choice.splits, rows, num_experts, width, wide);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return MXQ_ERR_WORKSPACE;
-    if (!few && !reach_ok(gated, wide, wr.direct() ? wr.sr * 2 : round_up(width, 8) * 2))
+    const int64_t row_bytes = round_up(width, 8) * 2;
+    if (!few && !reach_ok(gated, wide, wr.direct() ? wr.sr * 2 : row_bytes, row_bytes))
         return MXQ_ERR_UNSUPPORTED;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     Room room = {reinterpret_cast<char *>(workspace), nullptr};
@@ -410,7 +411,7 @@ mxq_status mxq_moe_linear_mx(const uint8_t *x, int64_t rows, int64_t width, int6
                          parts_bytes(kForward, choice.splits, rows, num_experts, width, wide);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return MXQ_ERR_WORKSPACE;
-    if (!few && !reach_ok(gated, wide, std::max(sw_n, width)))
+    if (!few && !reach_ok(gated, wide, sw_n, width))
         return MXQ_ERR_UNSUPPORTED;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     Room room = {reinterpret_cast<char *>(workspace), nullptr};

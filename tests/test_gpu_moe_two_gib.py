@@ -3,6 +3,7 @@ every kernel takes them; of a gated product alone the reach is bounded."""
 import pytest
 import torch
 
+import linear_reference as ref
 import mxfp8_quantization_moe_amd as mxq
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +62,19 @@ def test_gated_weights_are_refused():
     w = torch.empty(2048 << 20, dtype=torch.bfloat16, device=DEV).view(2048, 1 << 20)[:, :64]
     with pytest.raises(mxq.MXQError):
         mxq.moe_linear(normal(17, 64), w, gated=True)
+
+
+def test_gated_rows_that_repeat():
+    """One row for all 65536: little memory, whatever the rows' length."""
+    torch.manual_seed(5)
+    wide, width = 65536, 32768
+    w, x = normal(1, width, scale=2.0 ** -7), normal(17, width)
+    (wq, ws), (xq, xs) = mxq.quantize_mx_rowwise(w), mxq.quantize_mx_rowwise(x)
+    y = mxq.moe_linear_mx(xq, xs, wq.view(torch.uint8).expand(wide, width).view(torch.float8_e4m3fn), ws.expand(wide, width // 32),
+                          gated=True)
+    assert torch.equal(y, y[:, :1].expand_as(y))
+    a, b = ref.mx_values(xq, xs), ref.mx_values(wq, ws)[0]
+    z, size = a @ b, a.abs() @ b.abs()
+    # what the scaled instruction cuts, 2^-9 of the magnitudes, and the sum's additions; squared by the gate
+    off = (2.0 ** -9 + (width + 8) * SUM) * size
+    assert ((y[:, 0].double() - z * z).abs() <= HALF * z * z + (1 + HALF) * (2 * z.abs() * off + off * off)).all()
